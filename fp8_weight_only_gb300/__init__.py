@@ -11,6 +11,9 @@ raised.
     y = linear(x, codes, e8, bias)              # bf16 x for M > 1
     qx, sx = quantize_act(x)                    # W8A8: per-token e4m3 activations
     y = linear_w8a8(qx, sx, codes, scales, bias, out_dtype=torch.bfloat16)
+    cache = KVCache(k_pages, v_pages)           # paged keys and values: bf16/fp16, or e4m3 codes with scales
+    q = rope_append(q, k, v, slots, cache, positions, Rope(table))
+    o = paged_attention(q, cache, block_table, lens)
 """
 import ctypes
 import os
@@ -23,14 +26,16 @@ LIB_PATH = os.path.join(HERE, "libfp8w.so")
 FP8W_BF16 = 1
 FP8W_F16 = 2
 FP8W_F32 = 3
+FP8W_E4M3 = 4
 KERNEL_AUTO, KERNEL_GEMV, KERNEL_SKINNY, KERNEL_PREFILL = 0, 1, 2, 3
 
 SYMBOLS = ("fp8w_quantize", "fp8w_linear", "fp8w_linear_ex",
            "fp8w_status_string", "fp8w_last_cuda_error", "fp8w_device_error", "fp8w_abi_version",
            "fp8w_linear_noalloc", "fp8w_dequantize", "fp8w_quantize_grouped", "fp8w_linear_grouped",
            "fp8w_quantize_mx", "fp8w_linear_mx", "fp8w_quantize_ex", "fp8w_dequantize_grouped",
-           "fp8w_dequantize_mx", "fp8w_quantize_act", "fp8w_linear_w8a8")
-ABI_VERSION = 12
+           "fp8w_dequantize_mx", "fp8w_quantize_act", "fp8w_linear_w8a8", "fp8w_rope", "fp8w_rope_append",
+           "fp8w_paged_attention")
+ABI_VERSION = 13
 FLAG_WEIGHTS_READY = 1
 
 
@@ -43,6 +48,18 @@ class Fp8wError(RuntimeError):
 class LinearConfig(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int), ("cluster", ctypes.c_int), ("tiles", ctypes.c_int),
                 ("flags", ctypes.c_int), ("reserved", ctypes.c_int * 4)]
+
+
+class RopeSpec(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("max_pos", ctypes.c_int64), ("rot_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("axes", ctypes.c_int), ("sections", ctypes.c_int * 4)]
+
+
+class KVCacheSpec(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("dtype", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("page_size", ctypes.c_int)]
 
 
 _lib = None
@@ -86,6 +103,15 @@ def lib():
         L.fp8w_quantize_act.argtypes = [P, c.c_int, c.c_int64, c.c_int64, P, P, P]
         L.fp8w_linear_w8a8.restype = c.c_int
         L.fp8w_linear_w8a8.argtypes = [P, P, c.c_int64, c.c_int64, P, P, P, c.c_int64, P, c.c_int, c.c_int, P]
+        RS, KC = c.POINTER(RopeSpec), c.POINTER(KVCacheSpec)
+        L.fp8w_rope.restype = c.c_int
+        L.fp8w_rope.argtypes = [P, c.c_int, c.c_int64, c.c_int, c.c_int, c.c_int64, P, RS, P, c.c_int64, P]
+        L.fp8w_rope_append.restype = c.c_int
+        L.fp8w_rope_append.argtypes = [P, P, P, c.c_int, c.c_int64, c.c_int, c.c_int64, c.c_int64, c.c_int64, P, RS,
+                                       P, KC, P, c.c_int64, P]
+        L.fp8w_paged_attention.restype = c.c_int
+        L.fp8w_paged_attention.argtypes = [P, c.c_int, c.c_int64, c.c_int, c.c_int64, KC, P, c.c_int64, P, P,
+                                           c.c_int64, c.c_float, c.c_int64, c.c_int64, c.c_int64, P, c.c_int64, P]
         L.fp8w_status_string.restype = c.c_char_p
         L.fp8w_status_string.argtypes = [c.c_int]
         L.fp8w_last_cuda_error.restype = c.c_char_p
@@ -296,6 +322,153 @@ def linear_w8a8(x_codes, x_scales, codes, scales, bias=None, out=None, out_dtype
     return out
 
 
+class Rope:
+    """Rotary positions for rope and rope_append: table fp32 [max_pos, rot_dim]
+    (CUDA, contiguous), each row the cosines of rot_dim / 2 angles and then
+    their sines.  Pair i of a head is values (i, i + rot_dim / 2), or
+    (2 i, 2 i + 1) with interleaved.  sections: pairs that turn by each axis'
+    position (several axes: time, height and width, say); None: one axis."""
+
+    def __init__(self, table, interleaved=False, sections=None):
+        import torch
+        if table.dtype != torch.float32 or not table.is_cuda or table.dim() != 2 or not table.is_contiguous():
+            raise TypeError("table must be a contiguous 2-D float32 CUDA tensor")
+        sections = [table.shape[1] // 2] if sections is None else [int(s) for s in sections]
+        if not 1 <= len(sections) <= 4:
+            raise ValueError("1 to 4 sections, got %d" % len(sections))
+        self.table = table
+        self.axes = len(sections)
+        self.spec = RopeSpec(table.data_ptr(), table.shape[0], table.shape[1], 1 if interleaved else 0, self.axes,
+                             (ctypes.c_int * 4)(*sections))
+        self._ref = ctypes.byref(self.spec)
+
+
+class KVCache:
+    """A paged cache over the caller's tensors k and v, [num_pages, kv_heads,
+    page_size, head_dim] in any memory order whose head_dim values are
+    contiguous (a [num_pages, page_size, kv_heads, head_dim] tensor's
+    transpose(1, 2), say; both the same strides): bfloat16 or float16, or
+    uint8 e4m3 codes with k_scales, v_scales fp32 [num_pages, kv_heads,
+    page_size].  It keeps references to the tensors and nothing else."""
+
+    def __init__(self, k, v, k_scales=None, v_scales=None):
+        import torch
+        dtype = {torch.bfloat16: FP8W_BF16, torch.float16: FP8W_F16, torch.uint8: FP8W_E4M3}.get(k.dtype)
+        if dtype is None or v.dtype != k.dtype or not k.is_cuda or v.device != k.device or k.dim() != 4:
+            raise TypeError("k and v must be 4-D CUDA tensors, both bfloat16, float16 or uint8 (e4m3 codes)")
+        if v.shape != k.shape or v.stride() != k.stride() or k.stride(3) != 1:
+            raise ValueError("k and v must have the same shape and strides, head_dim contiguous")
+        pages, heads, page, dim = k.shape
+        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+            if (t is None) != (dtype != FP8W_E4M3):
+                raise ValueError("%s comes with e4m3 codes, and only with them" % name)
+            if t is not None and (t.dtype != torch.float32 or t.device != k.device or not t.is_contiguous() or
+                                  t.shape != (pages, heads, page)):
+                raise TypeError("%s must be a contiguous float32 [num_pages, kv_heads, page_size] CUDA tensor" % name)
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.device, self.dtype, self.kv_heads, self.page_size, self.head_dim = k.device, k.dtype, heads, page, dim
+        self.spec = KVCacheSpec(k.data_ptr(), v.data_ptr(), None if k_scales is None else k_scales.data_ptr(),
+                                None if v_scales is None else v_scales.data_ptr(), pages, k.stride(0), k.stride(1),
+                                k.stride(2), dtype, heads, dim, page)
+        self._ref = ctypes.byref(self.spec)
+
+
+def _rows(name, x, heads=None, dim=None):
+    """x [tokens, heads, head_dim] with its heads side by side; returns the token stride."""
+    if x.dim() != 3 or not x.is_cuda:
+        raise TypeError("%s must be a 3-D [tokens, heads, head_dim] CUDA tensor" % name)
+    _, h, d = x.shape
+    s = x.stride()
+    if s[2] != 1 or (s[1] != d and h > 1) or (heads is not None and h != heads) or (dim is not None and d != dim):
+        raise ValueError("%s: shape %s with strides %s does not fit" % (name, tuple(x.shape), s))
+    return s[0] if x.shape[0] > 1 or s[0] >= h * d else h * d
+
+
+def _index(name, t, dtype, shape, device):
+    if t.dtype != dtype or t.device != device or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        raise TypeError("%s must be a contiguous %s CUDA tensor%s" % (name, dtype, "" if shape is None else " of shape %s" % (tuple(shape),)))
+    return t.data_ptr()
+
+
+def _positions(positions, rope, tokens, device):
+    import torch
+    shape = (tokens,) if positions.dim() == 1 and rope.axes == 1 else (rope.axes, tokens)
+    return _index("positions", positions, torch.int32, shape, device)
+
+
+def _out(out, x):
+    """The output tensor for rows like x's, and its token stride."""
+    import torch
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
+        raise ValueError("out must have x's shape, type and device")
+    return out, _rows("out", out)
+
+
+def rope(x, positions, rope, out=None):
+    """x[tokens, heads, head_dim] bf16/fp16 with every head rotated by its
+    token's positions: int32 [tokens], or [axes, tokens] for a Rope with
+    sections.  x may be a view of a fused projection's rows; out may be x."""
+    xs = _rows("x", x)
+    out, os_ = _out(out, x)
+    tokens, heads, dim = x.shape
+    _check(lib().fp8w_rope(x.data_ptr(), _act(x.dtype), tokens, heads, dim, xs,
+                           _positions(positions, rope, tokens, x.device), rope._ref, out.data_ptr(), os_, _stream(x)))
+    return out
+
+
+def rope_append(q, k, v, slots, cache, positions=None, rope=None, out=None):
+    """One launch for a block's new tokens: q[tokens, q_heads, head_dim]
+    rotated (returned; q None: returns None), k rotated and v as it is
+    [tokens, kv_heads, head_dim] put to slots int64 [tokens] of the cache
+    (page * page_size + offset; negative: a padded token).  rope None: no
+    rotation."""
+    import torch
+    ks, vs = _rows("k", k, cache.kv_heads, cache.head_dim), _rows("v", v, cache.kv_heads, cache.head_dim)
+    tokens = k.shape[0]
+    if v.shape[0] != tokens or v.dtype != k.dtype or (q is not None and (q.shape[0] != tokens or q.dtype != k.dtype)):
+        raise ValueError("q, k and v must have the same tokens and type")
+    if (rope is None) != (positions is None):
+        raise ValueError("positions and rope come together")
+    qs = os_ = heads = 0
+    if q is not None:
+        qs, heads = _rows("q", q, None, cache.head_dim), q.shape[1]
+        out, os_ = _out(out, q)
+    _check(lib().fp8w_rope_append(None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), _act(k.dtype), tokens,
+                                  heads, qs, ks, vs,
+                                  None if rope is None else _positions(positions, rope, tokens, k.device),
+                                  None if rope is None else rope._ref,
+                                  _index("slots", slots, torch.int64, (tokens,), k.device), cache._ref,
+                                  None if q is None else out.data_ptr(), os_, _stream(k)))
+    return None if q is None else out
+
+
+def paged_attention(q, cache, block_table, lens, starts=None, scale=None, window=0, max_new=0, max_len=0, out=None):
+    """Causal attention of each sequence's new tokens q[tokens, q_heads,
+    head_dim] over its lens[s] tokens in the cache (the new ones appended
+    before).  block_table int32 [seqs, width], lens int32 [seqs]; starts int32
+    [seqs + 1]: first token of each sequence (None: one token each).  scale
+    defaults to head_dim ** -0.5.  window: positions a token sees (0: all).
+    max_new: a bound on a sequence's new tokens, max_len: about the longest of
+    lens, where the caller knows them on the host (0: not known)."""
+    import torch
+    qs = _rows("q", q, None, cache.head_dim)
+    out, os_ = _out(out, q)
+    tokens, heads, dim = q.shape
+    if block_table.dim() != 2:
+        raise TypeError("block_table must be a 2-D int32 CUDA tensor")
+    seqs, width = block_table.shape
+    dev = q.device
+    _check(lib().fp8w_paged_attention(
+        q.data_ptr(), _act(q.dtype), tokens, heads, qs, cache._ref,
+        _index("block_table", block_table, torch.int32, None, dev), width, _index("lens", lens, torch.int32, (seqs,), dev),
+        None if starts is None else _index("starts", starts, torch.int32, (seqs + 1,), dev), seqs,
+        dim ** -0.5 if scale is None else scale, window, max_new, max_len, out.data_ptr(), os_, _stream(q)))
+    return out
+
+
 def device_error():
-    """Nonzero if a kernel gave up a bounded wait since the last call (syncs)."""
+    """Nonzero if a kernel gave up a bounded wait, or met an index out of its
+    range, since the last call (syncs)."""
     return lib().fp8w_device_error()

@@ -36,6 +36,48 @@ fp8w_status check_linear(const void* x, int act, int64_t m, int64_t k, const uin
     return FP8W_OK;
 }
 
+// Multiples of 16 bytes in elements of `bytes`.
+bool stride16(int64_t stride, int64_t bytes) { return stride % (16 / bytes) == 0; }
+
+fp8w_status check_rope_spec(const fp8w_rope_spec* s, const int32_t* positions, int head_dim) {
+    if (!s->table || !positions) return FP8W_ERR_NULL;
+    if (s->rot_dim < 16 || s->rot_dim % 16 != 0 || s->rot_dim > head_dim) return FP8W_ERR_SHAPE;
+    if (s->max_pos < 1 || s->max_pos > FP8W_MAX_DIM || s->axes < 1 || s->axes > 4) return FP8W_ERR_VALUE;
+    int64_t sum = 0;
+    for (int a = 0; a < 4; ++a) {
+        if (s->sections[a] < 0 || (a >= s->axes && s->sections[a] != 0)) return FP8W_ERR_VALUE;
+        sum += s->sections[a];
+    }
+    if (sum != s->rot_dim / 2) return FP8W_ERR_VALUE;
+    if (!aligned(s->table, 16) || !aligned(positions, 4)) return FP8W_ERR_ALIGN;
+    return FP8W_OK;
+}
+
+fp8w_status check_cache(const fp8w_kv_cache* c, int act) {
+    const bool codes = c->dtype == FP8W_E4M3;
+    if (!c->k || !c->v || (codes && (!c->k_scales || !c->v_scales))) return FP8W_ERR_NULL;
+    if (!codes && c->dtype != act) return FP8W_ERR_DTYPE;
+    if (c->num_pages < 1 || c->num_pages > FP8W_MAX_DIM - 1 || c->kv_heads < 1 || c->kv_heads > 65536 ||
+        c->head_dim < 16 || c->head_dim > 128 || c->head_dim % 16 != 0)
+        return FP8W_ERR_SHAPE;
+    if (c->page_size < 8 || c->page_size > 256 || (c->page_size & (c->page_size - 1)) != 0) return FP8W_ERR_SHAPE;
+    const int64_t bytes = codes ? 1 : 2, most = (1ll << 40) / bytes;
+    if (c->token_stride < c->head_dim || c->head_stride < c->head_dim || c->page_stride < c->head_dim ||
+        c->token_stride >= most || c->head_stride >= most || c->page_stride >= most)
+        return FP8W_ERR_VALUE;
+    if (!codes && (c->k_scales || c->v_scales)) return FP8W_ERR_VALUE;
+    if (!stride16(c->token_stride, bytes) || !stride16(c->head_stride, bytes) || !stride16(c->page_stride, bytes) ||
+        !aligned(c->k, 16) || !aligned(c->v, 16) || (codes && (!aligned(c->k_scales, 4) || !aligned(c->v_scales, 4))))
+        return FP8W_ERR_ALIGN;
+    return FP8W_OK;
+}
+
+// An operand of rows [heads, head_dim] at `stride` elements.
+fp8w_status check_rows(const void* x, int64_t heads, int64_t head_dim, int64_t stride) {
+    if (stride < heads * head_dim) return FP8W_ERR_VALUE;
+    return aligned(x, 16) && stride16(stride, 2) ? FP8W_OK : FP8W_ERR_ALIGN;
+}
+
 }  // namespace
 
 extern "C" {
@@ -219,6 +261,79 @@ fp8w_status fp8w_linear_w8a8(const uint8_t* x_codes, const float* x_scales, int6
     return cuda_status(fp8w::launch_w8a8(a, static_cast<cudaStream_t>(stream)), "fp8w_linear_w8a8 launch");
 }
 
+fp8w_status fp8w_rope(const void* x, int act_dtype, int64_t tokens, int heads, int head_dim, int64_t x_stride,
+                      const int32_t* positions, const fp8w_rope_spec* spec, void* y, int64_t y_stride, void* stream) {
+    if (!x || !y || !spec) return FP8W_ERR_NULL;
+    if (act_dtype != FP8W_BF16 && act_dtype != FP8W_F16) return FP8W_ERR_DTYPE;
+    if (tokens < 1 || tokens > FP8W_MAX_DIM || heads < 1 || heads > 65536 || head_dim < 16 || head_dim > 256 ||
+        head_dim % 16 != 0)
+        return FP8W_ERR_SHAPE;
+    fp8w_status st = check_rope_spec(spec, positions, head_dim);
+    if (st != FP8W_OK) return st;
+    if ((st = check_rows(x, heads, head_dim, x_stride)) != FP8W_OK) return st;
+    if ((st = check_rows(y, heads, head_dim, y_stride)) != FP8W_OK) return st;
+    if (x == y && x_stride != y_stride) return FP8W_ERR_VALUE;
+    fp8w::RopeArgs a = {};
+    a.q = x;
+    a.act = act_dtype;
+    a.tokens = tokens;
+    a.q_heads = heads;
+    a.head_dim = head_dim;
+    a.q_stride = x_stride;
+    a.positions = positions;
+    a.spec = spec;
+    a.q_out = y;
+    a.q_out_stride = y_stride;
+    return cuda_status(fp8w::launch_rope(a, static_cast<cudaStream_t>(stream)), "fp8w_rope launch");
+}
+
+fp8w_status fp8w_rope_append(const void* q, const void* k, const void* v, int act_dtype, int64_t tokens, int q_heads,
+                             int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t* positions,
+                             const fp8w_rope_spec* spec, const int64_t* slots, const fp8w_kv_cache* cache, void* q_out,
+                             int64_t q_out_stride, void* stream) {
+    if (!k || !v || !slots || !cache || (q && !q_out)) return FP8W_ERR_NULL;
+    if (act_dtype != FP8W_BF16 && act_dtype != FP8W_F16) return FP8W_ERR_DTYPE;
+    if (tokens < 1 || tokens > FP8W_MAX_DIM || (q && (q_heads < 1 || q_heads > 65536))) return FP8W_ERR_SHAPE;
+    fp8w_status st = check_cache(cache, act_dtype);
+    if (st != FP8W_OK) return st;
+    if (spec && (st = check_rope_spec(spec, positions, cache->head_dim)) != FP8W_OK) return st;
+    if ((st = check_rows(k, cache->kv_heads, cache->head_dim, k_stride)) != FP8W_OK) return st;
+    if ((st = check_rows(v, cache->kv_heads, cache->head_dim, v_stride)) != FP8W_OK) return st;
+    if (q) {
+        if ((st = check_rows(q, q_heads, cache->head_dim, q_stride)) != FP8W_OK) return st;
+        if ((st = check_rows(q_out, q_heads, cache->head_dim, q_out_stride)) != FP8W_OK) return st;
+        if (q == q_out && q_stride != q_out_stride) return FP8W_ERR_VALUE;
+    }
+    if (!aligned(slots, 8)) return FP8W_ERR_ALIGN;
+    const fp8w::RopeArgs a{q,        k,         v,    act_dtype, tokens, q_heads, cache->head_dim, q_stride,
+                           k_stride, v_stride,  positions, spec, slots, cache,   q_out,           q_out_stride};
+    return cuda_status(fp8w::launch_rope(a, static_cast<cudaStream_t>(stream)), "fp8w_rope_append launch");
+}
+
+fp8w_status fp8w_paged_attention(const void* q, int act_dtype, int64_t tokens, int q_heads, int64_t q_stride,
+                                 const fp8w_kv_cache* cache, const int32_t* block_table, int64_t table_width,
+                                 const int32_t* lens, const int32_t* starts, int64_t seqs, float scale, int64_t window,
+                                 int64_t max_new, int64_t max_len, void* out, int64_t out_stride, void* stream) {
+    if (!q || !cache || !block_table || !lens || !out) return FP8W_ERR_NULL;
+    if (act_dtype != FP8W_BF16 && act_dtype != FP8W_F16) return FP8W_ERR_DTYPE;
+    // positions and a sequence's rows are counted in 32 bits
+    constexpr int64_t kMost = 1 << 30;
+    if (tokens < 1 || tokens > FP8W_MAX_DIM || seqs < 1 || seqs > kMost || q_heads < 1 || table_width < 1)
+        return FP8W_ERR_SHAPE;
+    fp8w_status st = check_cache(cache, act_dtype);
+    if (st != FP8W_OK) return st;
+    if (q_heads % cache->kv_heads != 0 || tokens * (q_heads / cache->kv_heads) > kMost ||
+        table_width > kMost / cache->page_size || (!starts && tokens != seqs))
+        return FP8W_ERR_SHAPE;
+    if (!(scale > 0.0f) || !(scale <= 3.0e38f) || window < 0 || max_new < 0 || max_len < 0) return FP8W_ERR_VALUE;
+    if ((st = check_rows(q, q_heads, cache->head_dim, q_stride)) != FP8W_OK) return st;
+    if ((st = check_rows(out, q_heads, cache->head_dim, out_stride)) != FP8W_OK) return st;
+    if (!aligned(block_table, 4) || !aligned(lens, 4) || (starts && !aligned(starts, 4))) return FP8W_ERR_ALIGN;
+    const fp8w::AttentionArgs a{q,    act_dtype, tokens, q_heads, q_stride, cache,   block_table, table_width, lens,
+                                starts, seqs,    scale,  window,  max_new,  max_len, out,         out_stride};
+    return cuda_status(fp8w::launch_attention(a, static_cast<cudaStream_t>(stream)), "fp8w_paged_attention launch");
+}
+
 const char* fp8w_status_string(int status) {
     switch (status) {
         case FP8W_OK: return "ok";
@@ -228,6 +343,7 @@ const char* fp8w_status_string(int status) {
         case FP8W_ERR_DTYPE: return "activation dtype must be FP8W_BF16 or FP8W_F16";
         case FP8W_ERR_CUDA: return "CUDA call failed (see fp8w_last_cuda_error)";
         case FP8W_ERR_CONFIG: return "invalid explicit launch configuration";
+        case FP8W_ERR_VALUE: return "a scalar argument or a struct's field is out of its range";
         default: return "unknown status";
     }
 }
@@ -240,7 +356,9 @@ int fp8w_device_error(void) {
     const int b = fp8w::read_gemv_device_error();
     const int c = fp8w::read_prefill_device_error();
     const int d = fp8w::read_w8a8_device_error();
-    return a ? a : b ? b : c ? c : d;
+    const int e = fp8w::read_rope_device_error();
+    const int f = fp8w::read_attention_device_error();
+    return a ? a : b ? b : c ? c : d ? d : e ? e : f;
 }
 
 int fp8w_abi_version(void) { return FP8W_ABI_VERSION; }

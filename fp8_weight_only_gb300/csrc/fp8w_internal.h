@@ -6,6 +6,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "../../include/fp8w.h"
+
 namespace fp8w {
 
 struct LinearArgs {
@@ -96,6 +98,54 @@ struct W8A8Args {
 };
 cudaError_t launch_w8a8(const W8A8Args& a, cudaStream_t st);
 int read_w8a8_device_error();
+
+// K6: rotary positions (cache null), with the append of k and v to a paged
+// cache.  q null: keys and values only.  spec null: no rotation.
+struct RopeArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    int act;
+    int64_t tokens;
+    int q_heads, head_dim;
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t* positions;
+    const fp8w_rope_spec* spec;
+    const int64_t* slots;
+    const fp8w_kv_cache* cache;
+    void* q_out;
+    int64_t q_out_stride;
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st);
+int read_rope_device_error();
+
+// K7: attention of new tokens over the paged cache.
+struct AttentionArgs {
+    const void* q;
+    int act;
+    int64_t tokens;
+    int q_heads;
+    int64_t q_stride;
+    const fp8w_kv_cache* cache;
+    const int32_t* block_table;
+    int64_t table_width;
+    const int32_t* lens;
+    const int32_t* starts;  // null: one token a sequence
+    int64_t seqs;
+    float scale;
+    int64_t window, max_new, max_len;
+    void* out;
+    int64_t out_stride;
+};
+cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t st);
+int read_attention_device_error();
+
+// 4-D tiled tensor map over a paged cache: (value, slot, head, page) with the
+// given byte strides, boxes of box_inner values x box_slots slots; the swizzle
+// is 128 bytes, or 64 where a box row has 64 bytes.
+bool encode_pages(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t dim, uint64_t slots,
+                  uint64_t heads, uint64_t pages, uint64_t slot_bytes, uint64_t head_bytes, uint64_t page_bytes,
+                  uint32_t box_inner, uint32_t box_slots, bool swizzle64);
 
 // Kernel-recorded wait failures (0 = none); reading clears them.
 int read_skinny_device_error();

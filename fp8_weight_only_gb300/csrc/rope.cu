@@ -1,0 +1,296 @@
+// rope.cu -- kernel K6: rotary positions, and the append of keys and values to
+// a paged cache with the rotation applied on the way.
+//
+// A pair (a, b) of a head turns by its token's angle:
+//   (a cos - b sin, b cos + a sin),  products and sums in fp32, each rounded
+// once (no fused multiply-add: the result is then one function of the inputs,
+// and codes made from it are too).  Keys and values for an e4m3 cache take the
+// weight quantiser's rule on the fp32 row: scale = amax / 448 (1.0 if that is
+// 0), code = nearest-even e4m3 of the IEEE quotient.
+//
+// Memory bound: every value is read and written once, and three operations a
+// value are nothing beside that.  A thread holds 16 values of a head, the two
+// 8-value chunks that make 8 whole pairs: chunks i and i + rot_dim / 16 with
+// pairs in halves, 2 i and 2 i + 1 with interleaved ones, so one set of eight
+// cosines and sines serves either form and a thread reads what it writes
+// (in-place calls need no further order).  A CTA takes one token and walks its
+// heads: a thread keeps its item's cosines and sines in registers over the
+// heads, and the table row is read once a token.
+#include "fp8w_device.cuh"
+#include "fp8w_internal.h"
+
+namespace fp8w {
+
+__device__ int g_rope_error;
+
+namespace {
+
+constexpr int kRopeThreads = 256;
+
+struct RopeParams {
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    uint16_t* q_out;
+    int64_t q_stride, k_stride, v_stride, q_out_stride, tokens;
+    int q_heads, kv_heads, head_dim;
+    const int32_t* positions;  // null: no rotation
+    const float* table;
+    int64_t max_pos;
+    int rot_dim, interleaved, axes;
+    int bound[4];  // pairs below bound[a] belong to axes 0 .. a
+    const int64_t* slots;
+    uint8_t* kc;
+    uint8_t* vc;
+    float* ks;
+    float* vs;
+    int64_t num_pages, page_stride, head_stride, token_stride;
+    int page_size;
+};
+
+template <bool kBf16>
+__device__ __forceinline__ void widen(const uint4 v, float* f) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        f[2 * e] = kBf16 ? bf16_lo_to_f32(u[e]) : f16_lo_to_f32(u[e]);
+        f[2 * e + 1] = kBf16 ? bf16_hi_to_f32(u[e]) : f16_hi_to_f32(u[e]);
+    }
+}
+
+template <bool kBf16>
+__device__ __forceinline__ uint4 narrow(const float* f) {
+    uint32_t u[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        u[e] = static_cast<uint32_t>(round_out<kBf16>(f[2 * e])) |
+               (static_cast<uint32_t>(round_out<kBf16>(f[2 * e + 1])) << 16);
+    return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// P lanes (a power of two >= head_dim / 16) work on a head.
+template <int P, bool kBf16, bool kFp8>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+    pdl_launch_dependents();
+    constexpr int kGroups = kRopeThreads / P;
+    const int item = threadIdx.x & (P - 1);
+    const int group = threadIdx.x / P;
+    const int64_t token = blockIdx.x;
+    const bool live = item * 16 < p.head_dim;
+    const int half = p.rot_dim >> 1;
+    const bool turns = p.positions && item * 16 < p.rot_dim;
+    // the item's two chunks (first values)
+    const int c0 = turns ? (p.interleaved ? item * 16 : item * 8) : item * 16;
+    const int c1 = turns && !p.interleaved ? half + item * 8 : c0 + 8;
+    const int heads = p.q_heads + 2 * p.kv_heads;
+    const int first = static_cast<int>(blockIdx.y) * kGroups + group, step = static_cast<int>(gridDim.y) * kGroups;
+    pdl_wait();
+
+    float cs[8], sn[8];
+    if (turns) {
+        int64_t pos[4];
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            if (a >= p.axes) break;
+            int64_t at = __ldg(p.positions + a * p.tokens + token);
+            if (at < 0 || at >= p.max_pos) {
+                atomicCAS(&g_rope_error, 0, 6000 + kErrIndex);
+                at = at < 0 ? 0 : p.max_pos - 1;
+            }
+            pos[a] = at;
+        }
+        auto axis_of = [&](int pair) {
+            int a = 0;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) a += (i + 1 < p.axes && pair >= p.bound[i]) ? 1 : 0;
+            return a;
+        };
+        auto row_of = [&](int a) { return p.table + (a == 0 ? pos[0] : a == 1 ? pos[1] : a == 2 ? pos[2] : pos[3]) * p.rot_dim; };
+        const int i0 = item * 8;
+        if (axis_of(i0) == axis_of(i0 + 7)) {
+            const float* row = row_of(axis_of(i0)) + i0;
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+                const float4 c = __ldg(reinterpret_cast<const float4*>(row + e));
+                const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + e));
+                cs[e] = c.x, cs[e + 1] = c.y, cs[e + 2] = c.z, cs[e + 3] = c.w;
+                sn[e] = s.x, sn[e + 1] = s.y, sn[e + 2] = s.z, sn[e + 3] = s.w;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float* row = row_of(axis_of(i0 + e)) + i0 + e;
+                cs[e] = __ldg(row);
+                sn[e] = __ldg(row + half);
+            }
+        }
+    }
+    int64_t slot = -1, page = 0, off = 0;
+    if (p.kv_heads) {
+        slot = __ldg(p.slots + token);
+        page = slot / p.page_size;
+        off = slot - page * p.page_size;
+        if (slot >= 0 && page >= p.num_pages) {
+            atomicCAS(&g_rope_error, 0, 6000 + kErrIndex);
+            slot = -1;
+        }
+    }
+
+    // a warp's groups take consecutive heads: all of them stay in the loop
+    // until the last is done, so the exchanges below involve whole warps
+    for (int h0 = first; h0 - (group & (32 / P - 1)) < heads; h0 += step) {
+        const int h = h0;
+        const bool is_q = h < p.q_heads, is_k = !is_q && h < p.q_heads + p.kv_heads;
+        const bool work = live && h < heads && (is_q || slot >= 0);
+        const int kvh = is_q ? 0 : h - p.q_heads - (is_k ? 0 : p.kv_heads);
+        const uint16_t* src = is_q ? p.q + token * p.q_stride + static_cast<int64_t>(h) * p.head_dim
+                              : is_k ? p.k + token * p.k_stride + static_cast<int64_t>(kvh) * p.head_dim
+                                     : p.v + token * p.v_stride + static_cast<int64_t>(kvh) * p.head_dim;
+        uint4 x0 = make_uint4(0u, 0u, 0u, 0u), x1 = x0;
+        // values that do not turn go by their item's own chunks
+        const int s0 = (is_q || is_k) ? c0 : item * 16, s1 = (is_q || is_k) ? c1 : item * 16 + 8;
+        if (work) {
+            x0 = *reinterpret_cast<const uint4*>(src + s0);
+            x1 = *reinterpret_cast<const uint4*>(src + s1);
+        }
+        float f[16];
+        widen<kBf16>(x0, f);
+        widen<kBf16>(x1, f + 8);
+        if (turns && (is_q || is_k)) {
+            if (p.interleaved) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float a = f[2 * e], b = f[2 * e + 1];
+                    f[2 * e] = __fsub_rn(__fmul_rn(a, cs[e]), __fmul_rn(b, sn[e]));
+                    f[2 * e + 1] = __fadd_rn(__fmul_rn(b, cs[e]), __fmul_rn(a, sn[e]));
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float a = f[e], b = f[8 + e];
+                    f[e] = __fsub_rn(__fmul_rn(a, cs[e]), __fmul_rn(b, sn[e]));
+                    f[8 + e] = __fadd_rn(__fmul_rn(b, cs[e]), __fmul_rn(a, sn[e]));
+                }
+            }
+            x0 = narrow<kBf16>(f);
+            x1 = narrow<kBf16>(f + 8);
+        }
+        if (is_q) {
+            if (work) {
+                uint16_t* dst = p.q_out + token * p.q_out_stride + static_cast<int64_t>(h) * p.head_dim;
+                *reinterpret_cast<uint4*>(dst + s0) = x0;
+                *reinterpret_cast<uint4*>(dst + s1) = x1;
+            }
+        }
+        if constexpr (kFp8) {
+            float amax = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(f[e]));
+#pragma unroll
+            for (int d = P / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+            if (!is_q && work) {
+                float s = __fdiv_rn(amax, 448.0f);
+                s = s == 0.0f ? 1.0f : s;
+                uint32_t c[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint16_t lo = f32x2_to_e4m3x2(__fdiv_rn(f[4 * e], s), __fdiv_rn(f[4 * e + 1], s));
+                    const uint16_t hi = f32x2_to_e4m3x2(__fdiv_rn(f[4 * e + 2], s), __fdiv_rn(f[4 * e + 3], s));
+                    c[e] = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+                }
+                uint8_t* dst = (is_k ? p.kc : p.vc) + page * p.page_stride + kvh * p.head_stride + off * p.token_stride;
+                *reinterpret_cast<uint2*>(dst + s0) = make_uint2(c[0], c[1]);
+                *reinterpret_cast<uint2*>(dst + s1) = make_uint2(c[2], c[3]);
+                if (item == 0) (is_k ? p.ks : p.vs)[(page * p.kv_heads + kvh) * p.page_size + off] = s;
+            }
+        } else if (!is_q && work) {
+            uint16_t* dst = reinterpret_cast<uint16_t*>(is_k ? p.kc : p.vc) + page * p.page_stride +
+                            kvh * p.head_stride + off * p.token_stride;
+            *reinterpret_cast<uint4*>(dst + s0) = x0;
+            *reinterpret_cast<uint4*>(dst + s1) = x1;
+        }
+    }
+}
+
+template <int P>
+cudaError_t launch_p(const RopeParams& p, bool bf16, bool fp8, cudaStream_t st) {
+    int sms = 0;
+    cudaError_t e = device_sm_count(sms);
+    if (e != cudaSuccess) return e;
+    const int heads = p.q_heads + 2 * p.kv_heads;
+    // one CTA a token; with few tokens a token's heads go to several CTAs
+    constexpr int kGroups = kRopeThreads / P;
+    const int most = (heads + kGroups - 1) / kGroups;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.tokens), static_cast<unsigned>(p.tokens < 2 * sms ? most : 1));
+    cfg.blockDim = dim3(kRopeThreads);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (fp8)
+        return bf16 ? cudaLaunchKernelEx(&cfg, rope_kernel<P, true, true>, p)
+                    : cudaLaunchKernelEx(&cfg, rope_kernel<P, false, true>, p);
+    return bf16 ? cudaLaunchKernelEx(&cfg, rope_kernel<P, true, false>, p)
+                : cudaLaunchKernelEx(&cfg, rope_kernel<P, false, false>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
+    RopeParams p = {};
+    p.q = static_cast<const uint16_t*>(a.q);
+    p.q_out = static_cast<uint16_t*>(a.q_out);
+    p.q_stride = a.q_stride;
+    p.q_out_stride = a.q_out_stride;
+    p.q_heads = a.q ? a.q_heads : 0;
+    p.tokens = a.tokens;
+    p.head_dim = a.head_dim;
+    if (a.spec) {
+        p.positions = a.positions;
+        p.table = a.spec->table;
+        p.max_pos = a.spec->max_pos;
+        p.rot_dim = a.spec->rot_dim;
+        p.interleaved = a.spec->interleaved;
+        p.axes = a.spec->axes;
+        for (int i = 0, sum = 0; i < 4; ++i) p.bound[i] = sum += a.spec->sections[i];
+    }
+    bool fp8 = false;
+    if (a.cache) {
+        const fp8w_kv_cache& c = *a.cache;
+        p.k = static_cast<const uint16_t*>(a.k);
+        p.v = static_cast<const uint16_t*>(a.v);
+        p.k_stride = a.k_stride;
+        p.v_stride = a.v_stride;
+        p.kv_heads = c.kv_heads;
+        p.slots = a.slots;
+        p.kc = static_cast<uint8_t*>(c.k);
+        p.vc = static_cast<uint8_t*>(c.v);
+        p.ks = c.k_scales;
+        p.vs = c.v_scales;
+        p.num_pages = c.num_pages;
+        p.page_stride = c.page_stride;
+        p.head_stride = c.head_stride;
+        p.token_stride = c.token_stride;
+        p.page_size = c.page_size;
+        fp8 = c.dtype == FP8W_E4M3;
+    }
+    const bool bf16 = a.act == FP8W_BF16;
+    const int items = a.head_dim / 16;
+    if (items <= 1) return launch_p<1>(p, bf16, fp8, st);
+    if (items <= 2) return launch_p<2>(p, bf16, fp8, st);
+    if (items <= 4) return launch_p<4>(p, bf16, fp8, st);
+    if (items <= 8) return launch_p<8>(p, bf16, fp8, st);
+    return launch_p<16>(p, bf16, fp8, st);
+}
+
+int read_rope_device_error() {
+    int v = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&v, g_rope_error, sizeof v) != cudaSuccess) return -1;
+    if (v != 0 && cudaMemcpyToSymbol(g_rope_error, &zero, sizeof zero) != cudaSuccess) return -1;
+    return v;
+}
+
+}  // namespace fp8w

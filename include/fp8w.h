@@ -26,8 +26,9 @@
  *    outputs are untouched and no work is enqueued.  FP8W_ERR_CUDA means a
  *    CUDA runtime call failed (fp8w_last_cuda_error() names it).  Faults
  *    inside a kernel surface on the caller's next synchronisation.
- *  - A kernel that gives up a bounded wait (it never should) records a
- *    nonzero code that fp8w_device_error() returns.
+ *  - A kernel that gives up a bounded wait (it never should), or meets an
+ *    index in device memory that is out of its range, records a nonzero code
+ *    that fp8w_device_error() returns.
  *  - On its first use on a device the library sets each kernel's
  *    shared-memory attribute and reads the device's SM count and cluster
  *    capacity, and keeps them for the process (the "state" above is about
@@ -45,7 +46,7 @@
 extern "C" {
 #endif
 
-#define FP8W_ABI_VERSION 12
+#define FP8W_ABI_VERSION 13
 
 #if defined(__GNUC__)
 #define FP8W_API __attribute__((visibility("default")))
@@ -60,12 +61,13 @@ typedef enum fp8w_status {
     FP8W_ERR_ALIGN = 3,     /* a pointer breaks its alignment rule */
     FP8W_ERR_DTYPE = 4,     /* activation dtype is not FP8W_BF16 / FP8W_F16 */
     FP8W_ERR_CUDA = 5,      /* a CUDA runtime/driver call failed */
-    FP8W_ERR_CONFIG = 6     /* an explicit launch configuration is invalid */
+    FP8W_ERR_CONFIG = 6,    /* an explicit launch configuration is invalid */
+    FP8W_ERR_VALUE = 7      /* a scalar argument or a struct's field is out of its range */
 } fp8w_status;
 
 /* Activation / output dtypes (FP8W_F32: fp8w_dequantize's output and
- * fp8w_quantize_ex's weights only). */
-enum { FP8W_BF16 = 1, FP8W_F16 = 2, FP8W_F32 = 3 };
+ * fp8w_quantize_ex's weights only; FP8W_E4M3: a cache's codes only). */
+enum { FP8W_BF16 = 1, FP8W_F16 = 2, FP8W_F32 = 3, FP8W_E4M3 = 4 };
 
 /* Largest supported reduction length and row count. */
 #define FP8W_MAX_K 65536
@@ -343,14 +345,159 @@ FP8W_API fp8w_status fp8w_linear_w8a8(const uint8_t *x_codes, const float *x_sca
                              const uint8_t *w_codes, const float *w_scales, const float *bias, int64_t n,
                              void *y, int out_dtype, int flags, void *stream);
 
+/*
+ * What stands between the q, k and v linears of a decoder block and its o
+ * linear: the rotation of queries and keys by their positions, a paged cache
+ * of keys and values, and the attention of new tokens over it.  The pages
+ * have no counterpart.
+ *
+ * Rows of activations: token t, head h of a [tokens, heads, head_dim] operand
+ * starts at element t * stride + h * head_dim, so the q, k and v parts of one
+ * fused projection's output are taken where they are (stride: its columns).
+ * Strides are in elements and at least heads * head_dim; base pointers and
+ * strides are multiples of 16 bytes.
+ */
+
+/*
+ * fp8w_rope_spec -- rotary positions.  The first rot_dim values of a head are
+ * rot_dim / 2 pairs; pair i is values (i, i + rot_dim / 2), or with
+ * interleaved != 0 values (2 i, 2 i + 1).  A pair (a, b) turns to
+ *   (a * cos - b * sin, b * cos + a * sin),
+ * every product and sum in fp32, each rounded once; the values beyond rot_dim
+ * are copied.  Its cosine and sine are table[p][i] and
+ * table[p][rot_dim / 2 + i], p the token's position on the pair's axis: pairs
+ * 0 .. sections[0] - 1 belong to axis 0, the next sections[1] to axis 1 and
+ * so on (time, height and width of a video's patch, say).
+ *   table    [max_pos, rot_dim] fp32, device, 16-byte aligned.
+ *   rot_dim  a multiple of 16, at most head_dim.
+ *   axes     1..4; sections[0 .. axes - 1] >= 0 add up to rot_dim / 2, the
+ *            others are 0.
+ */
+typedef struct fp8w_rope_spec {
+    const float *table;
+    int64_t max_pos;
+    int rot_dim;
+    int interleaved;
+    int axes;
+    int sections[4];
+} fp8w_rope_spec;
+
+/*
+ * fp8w_kv_cache -- a paged cache of keys and values: num_pages pages of
+ * page_size token slots.  Slot o of page p, head h starts at element
+ *   p * page_stride + h * head_stride + o * token_stride
+ * of k and of v (head_dim contiguous values), so pages may be laid out head by
+ * head ([pages, kv_heads, page_size, head_dim]) or token by token ([pages,
+ * page_size, kv_heads, head_dim]), and may be part of larger pages.
+ *   dtype      FP8W_BF16 or FP8W_F16, then equal to the calls' act_dtype; or
+ *              FP8W_E4M3: codes with one fp32 scale per slot and head in
+ *              k_scales, v_scales [num_pages, kv_heads, page_size] (dense;
+ *              NULL for the other types), scale = amax / 448 (1.0 if that is
+ *              0), as fp8w_quantize gives a row.
+ *   head_dim   a multiple of 16, 16..128.
+ *   page_size  8, 16, 32, 64, 128 or 256.
+ * Pointers are 16-byte aligned (scales 4) and strides multiples of 16 bytes.
+ * The struct itself is read during the call only.
+ */
+typedef struct fp8w_kv_cache {
+    void *k, *v;
+    float *k_scales, *v_scales;
+    int64_t num_pages, page_stride, head_stride, token_stride;
+    int dtype, kv_heads, head_dim, page_size;
+} fp8w_kv_cache;
+
+/*
+ * fp8w_rope -- y = x with every head rotated by its token's positions, rounded
+ * once to act_dtype.  y may be x (same stride); otherwise they do not overlap.
+ *   x          [tokens, heads, head_dim] act_dtype, token stride x_stride.
+ *   head_dim   a multiple of 16, 16..256.
+ *   positions  [axes, tokens] int32, device: each in 0..max_pos - 1.  One
+ *              outside is moved to the nearer end and recorded
+ *              (fp8w_device_error).
+ *   y          like x, with y_stride (output).
+ */
+FP8W_API fp8w_status fp8w_rope(const void *x, int act_dtype, int64_t tokens, int heads, int head_dim,
+                      int64_t x_stride, const int32_t *positions, const fp8w_rope_spec *spec,
+                      void *y, int64_t y_stride, void *stream);
+
+/*
+ * fp8w_rope_append -- one launch for a decoder block's new tokens: q rotated
+ * into q_out as by fp8w_rope, k rotated and v as it is written to their slots
+ * of the cache.
+ *   q          [tokens, q_heads, head_dim] act_dtype, token stride q_stride,
+ *              or NULL: nothing is done for queries (q_out is not read).
+ *   k, v       [tokens, kv_heads, head_dim] act_dtype, k_stride, v_stride;
+ *              kv_heads and head_dim are the cache's.
+ *   positions  as fp8w_rope; NULL where spec is NULL.
+ *   spec       NULL: no rotation, keys and queries go as they are.
+ *   slots      [tokens] int64, device: page * page_size + offset of the token's
+ *              slot, pairwise different.  A negative slot writes nothing to
+ *              the cache (a padded token); one beyond the cache writes nothing
+ *              and is recorded (fp8w_device_error).
+ *   q_out      like q, with q_out_stride; may be q (same stride).
+ * A 16-bit cache gets the fp32 results rounded once (v: its own bits).  An
+ * e4m3 cache gets the codes and scales that fp8w_quantize gives the fp32 rows:
+ * the rotated key is not rounded to 16 bits in between.
+ */
+FP8W_API fp8w_status fp8w_rope_append(const void *q, const void *k, const void *v, int act_dtype,
+                             int64_t tokens, int q_heads, int64_t q_stride, int64_t k_stride,
+                             int64_t v_stride, const int32_t *positions, const fp8w_rope_spec *spec,
+                             const int64_t *slots, const fp8w_kv_cache *cache, void *q_out,
+                             int64_t q_out_stride, void *stream);
+
+/*
+ * fp8w_paged_attention -- causal attention of each sequence's new tokens over
+ * its tokens in the cache, the new ones (appended before) among them:
+ *   out[t, h] = sum_j p_j v[j, h / g],  p = softmax_j(scale * q[t, h] . k[j, h / g]),
+ * g = q_heads / kv_heads, over the positions j that token t sees: with n new
+ * tokens of len in all, new token i is at position len - n + i and sees
+ * positions 0 .. len - n + i, with window > 0 only the last `window` of them.
+ * A token that sees none (len 0, or a position below 0) gets zeros.
+ *   q            [tokens, q_heads, head_dim] act_dtype, token stride q_stride;
+ *                q_heads a multiple of the cache's kv_heads.
+ *   block_table  [seqs, table_width] int32, device: page of the sequence's
+ *                positions c * page_size ..; entries past its last position, or
+ *                of pages wholly before its window, are not used.
+ *   lens         [seqs] int32, device: tokens in the cache, at most
+ *                table_width * page_size.
+ *   starts       [seqs + 1] int32, device, not decreasing: sequence s has the
+ *                tokens starts[s] .. starts[s + 1] - 1; NULL: one token each
+ *                (tokens == seqs).  Rows of out that belong to no sequence are
+ *                not written.
+ *   scale        finite and > 0.
+ *   window       0 (all positions) or the number of positions a token sees.
+ *   max_new      no sequence has more new tokens than this; 0: not known.
+ *                Sizes the launch; more is recorded (fp8w_device_error), and
+ *                rows are then left unwritten.
+ *   max_len      about the largest of lens; 0: table_width * page_size.  Guides
+ *                how the work is split and nothing else.
+ *   out          like q, with out_stride (output); it may not overlap q.
+ * Scores, softmax and sums are fp32; the softmax weights are rounded to
+ * act_dtype for the second product, as its other operand is; e4m3 scales
+ * multiply scores and weights in fp32.  One rounding at the end.  Cached values
+ * of positions below len are finite, in act_dtype's range; slots past them may
+ * hold anything.  A table entry outside the cache, a len beyond the table or
+ * starts out of order are recorded (fp8w_device_error): the tokens concerned
+ * get unspecified finite values, and nothing outside the operands is read.
+ * One launch and no workspace: where few rows meet a long cache, the CTAs of a
+ * thread-block cluster share them and join their partial sums in distributed
+ * shared memory, in rank order.
+ */
+FP8W_API fp8w_status fp8w_paged_attention(const void *q, int act_dtype, int64_t tokens, int q_heads,
+                                 int64_t q_stride, const fp8w_kv_cache *cache, const int32_t *block_table,
+                                 int64_t table_width, const int32_t *lens, const int32_t *starts, int64_t seqs,
+                                 float scale, int64_t window, int64_t max_new, int64_t max_len, void *out,
+                                 int64_t out_stride, void *stream);
+
 /* Human-readable name of a status code (static string). */
 FP8W_API const char *fp8w_status_string(int status);
 
 /* Name of the last failing CUDA call in this thread ("" if none). */
 FP8W_API const char *fp8w_last_cuda_error(void);
 
-/* Code recorded by a kernel that gave up a bounded wait on the current
- * device (0 = none), and clears it.  Synchronises the device first. */
+/* Code recorded by a kernel that gave up a bounded wait, or met an index out
+ * of its range, on the current device (0 = none), and clears it.
+ * Synchronises the device first. */
 FP8W_API int fp8w_device_error(void);
 
 /* FP8W_ABI_VERSION of the loaded library. */
