@@ -367,54 +367,82 @@ class KVCache:
                 raise TypeError("%s must be a contiguous float32 [num_pages, kv_heads, page_size] CUDA tensor" % name)
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
         self.device, self.dtype, self.kv_heads, self.page_size, self.head_dim = k.device, k.dtype, heads, page, dim
+        self.index = k.get_device()
         self.spec = KVCacheSpec(k.data_ptr(), v.data_ptr(), None if k_scales is None else k_scales.data_ptr(),
                                 None if v_scales is None else v_scales.data_ptr(), pages, k.stride(0), k.stride(1),
                                 k.stride(2), dtype, heads, dim, page)
         self._ref = ctypes.byref(self.spec)
 
 
+# The calls below run once a layer and token, so their checks are kept to a
+# few attribute reads each.
+
+_torch = _raw_stream = None
+_ACT = {}
+
+
+def _load_torch():
+    global _torch, _raw_stream
+    import torch
+    _ACT.update({torch.bfloat16: FP8W_BF16, torch.float16: FP8W_F16})
+    # the stream's handle without a Stream object around it, where torch has it
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _torch = torch
+
+
 def _rows(name, x, heads=None, dim=None):
     """x [tokens, heads, head_dim] with its heads side by side; returns the token stride."""
-    if x.dim() != 3 or not x.is_cuda:
+    if not x.is_cuda or x.dim() != 3:
         raise TypeError("%s must be a 3-D [tokens, heads, head_dim] CUDA tensor" % name)
-    _, h, d = x.shape
-    s = x.stride()
-    if s[2] != 1 or (s[1] != d and h > 1) or (heads is not None and h != heads) or (dim is not None and d != dim):
-        raise ValueError("%s: shape %s with strides %s does not fit" % (name, tuple(x.shape), s))
-    return s[0] if x.shape[0] > 1 or s[0] >= h * d else h * d
+    tokens, h, d = x.shape
+    s0, s1, s2 = x.stride()
+    if s2 != 1 or (s1 != d and h > 1) or (heads is not None and h != heads) or (dim is not None and d != dim):
+        raise ValueError("%s: shape %s with strides %s does not fit" % (name, tuple(x.shape), x.stride()))
+    return s0 if tokens > 1 or s0 >= h * d else h * d
 
 
 def _index(name, t, dtype, shape, device):
-    if t.dtype != dtype or t.device != device or not t.is_contiguous() or (shape is not None and t.shape != shape):
-        raise TypeError("%s must be a contiguous %s CUDA tensor%s" % (name, dtype, "" if shape is None else " of shape %s" % (tuple(shape),)))
+    if t.dtype != dtype or t.get_device() != device or not t.is_contiguous() or t.shape != shape:
+        raise TypeError("%s must be a contiguous %s tensor of shape %s on the same device" % (name, dtype, tuple(shape)))
     return t.data_ptr()
 
 
 def _positions(positions, rope, tokens, device):
-    import torch
-    shape = (tokens,) if positions.dim() == 1 and rope.axes == 1 else (rope.axes, tokens)
-    return _index("positions", positions, torch.int32, shape, device)
+    shape = (tokens,) if rope.axes == 1 and positions.dim() == 1 else (rope.axes, tokens)
+    return _index("positions", positions, _torch.int32, shape, device)
 
 
 def _out(out, x):
     """The output tensor for rows like x's, and its token stride."""
-    import torch
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
+        out = _torch.empty_like(x, memory_format=_torch.contiguous_format)
+        return out, out.stride(0)
+    if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
         raise ValueError("out must have x's shape, type and device")
     return out, _rows("out", out)
+
+
+def _act_of(x):
+    act = _ACT.get(x.dtype)
+    return _act(x.dtype) if act is None else act
 
 
 def rope(x, positions, rope, out=None):
     """x[tokens, heads, head_dim] bf16/fp16 with every head rotated by its
     token's positions: int32 [tokens], or [axes, tokens] for a Rope with
     sections.  x may be a view of a fused projection's rows; out may be x."""
+    if _torch is None:
+        _load_torch()
     xs = _rows("x", x)
-    out, os_ = _out(out, x)
     tokens, heads, dim = x.shape
-    _check(lib().fp8w_rope(x.data_ptr(), _act(x.dtype), tokens, heads, dim, xs,
-                           _positions(positions, rope, tokens, x.device), rope._ref, out.data_ptr(), os_, _stream(x)))
+    dev = x.get_device()
+    out, os_ = _out(out, x)
+    st = (_lib or lib()).fp8w_rope(x.data_ptr(), _act_of(x), tokens, heads, dim, xs,
+                                   _positions(positions, rope, tokens, dev), rope._ref, out.data_ptr(), os_,
+                                   _raw_stream(dev))
+    if st:
+        _check(st)
     return out
 
 
@@ -424,23 +452,29 @@ def rope_append(q, k, v, slots, cache, positions=None, rope=None, out=None):
     [tokens, kv_heads, head_dim] put to slots int64 [tokens] of the cache
     (page * page_size + offset; negative: a padded token).  rope None: no
     rotation."""
-    import torch
-    ks, vs = _rows("k", k, cache.kv_heads, cache.head_dim), _rows("v", v, cache.kv_heads, cache.head_dim)
-    tokens = k.shape[0]
-    if v.shape[0] != tokens or v.dtype != k.dtype or (q is not None and (q.shape[0] != tokens or q.dtype != k.dtype)):
-        raise ValueError("q, k and v must have the same tokens and type")
+    if _torch is None:
+        _load_torch()
+    heads, dim = cache.kv_heads, cache.head_dim
+    ks, vs = _rows("k", k, heads, dim), _rows("v", v, heads, dim)
+    tokens, dtype, dev = k.shape[0], k.dtype, k.get_device()
+    if v.shape[0] != tokens or v.dtype != dtype or dev != cache.index or \
+            (q is not None and (q.shape[0] != tokens or q.dtype != dtype)):
+        raise ValueError("q, k and v must have the same tokens and type, on the cache's device")
     if (rope is None) != (positions is None):
         raise ValueError("positions and rope come together")
-    qs = os_ = heads = 0
+    pos = spec = qp = op = None
+    qs = os_ = q_heads = 0
+    if rope is not None:
+        pos, spec = _positions(positions, rope, tokens, dev), rope._ref
     if q is not None:
-        qs, heads = _rows("q", q, None, cache.head_dim), q.shape[1]
+        qs, q_heads, qp = _rows("q", q, None, dim), q.shape[1], q.data_ptr()
         out, os_ = _out(out, q)
-    _check(lib().fp8w_rope_append(None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), _act(k.dtype), tokens,
-                                  heads, qs, ks, vs,
-                                  None if rope is None else _positions(positions, rope, tokens, k.device),
-                                  None if rope is None else rope._ref,
-                                  _index("slots", slots, torch.int64, (tokens,), k.device), cache._ref,
-                                  None if q is None else out.data_ptr(), os_, _stream(k)))
+        op = out.data_ptr()
+    st = (_lib or lib()).fp8w_rope_append(qp, k.data_ptr(), v.data_ptr(), _act_of(k), tokens, q_heads, qs, ks, vs, pos,
+                                          spec, _index("slots", slots, _torch.int64, (tokens,), dev), cache._ref, op, os_,
+                                          _raw_stream(dev))
+    if st:
+        _check(st)
     return None if q is None else out
 
 
@@ -452,19 +486,23 @@ def paged_attention(q, cache, block_table, lens, starts=None, scale=None, window
     defaults to head_dim ** -0.5.  window: positions a token sees (0: all).
     max_new: a bound on a sequence's new tokens, max_len: about the longest of
     lens, where the caller knows them on the host (0: not known)."""
-    import torch
+    if _torch is None:
+        _load_torch()
     qs = _rows("q", q, None, cache.head_dim)
-    out, os_ = _out(out, q)
     tokens, heads, dim = q.shape
-    if block_table.dim() != 2:
-        raise TypeError("block_table must be a 2-D int32 CUDA tensor")
-    seqs, width = block_table.shape
-    dev = q.device
-    _check(lib().fp8w_paged_attention(
-        q.data_ptr(), _act(q.dtype), tokens, heads, qs, cache._ref,
-        _index("block_table", block_table, torch.int32, None, dev), width, _index("lens", lens, torch.int32, (seqs,), dev),
-        None if starts is None else _index("starts", starts, torch.int32, (seqs + 1,), dev), seqs,
-        dim ** -0.5 if scale is None else scale, window, max_new, max_len, out.data_ptr(), os_, _stream(q)))
+    dev = q.get_device()
+    if dev != cache.index or block_table.dim() != 2:
+        raise TypeError("q must be on the cache's device, and block_table a 2-D int32 tensor")
+    seqs, width = shape = block_table.shape
+    out, os_ = _out(out, q)
+    int32 = _torch.int32
+    st = (_lib or lib()).fp8w_paged_attention(
+        q.data_ptr(), _act_of(q), tokens, heads, qs, cache._ref, _index("block_table", block_table, int32, shape, dev), width,
+        _index("lens", lens, int32, (seqs,), dev),
+        None if starts is None else _index("starts", starts, int32, (seqs + 1,), dev), seqs,
+        dim ** -0.5 if scale is None else scale, window, max_new, max_len, out.data_ptr(), os_, _raw_stream(dev))
+    if st:
+        _check(st)
     return out
 
 

@@ -14,8 +14,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfp8w.so")
-SOURCES = ["api.cu", "quantize.cu", "gemv.cu", "skinny.cu", "prefill.cu", "w8a8.cu", "rope.cu", "attention.cu"]
-HEADERS = ["fp8w_device.cuh", "fp8w_internal.h"]
+SOURCES = ["api.cu", "quantize.cu", "gemv.cu", "skinny.cu", "prefill.cu", "w8a8.cu", "rope.cu", "attention.cu", "attention_few.cu"]
+HEADERS = ["fp8w_device.cuh", "fp8w_internal.h", "attention.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

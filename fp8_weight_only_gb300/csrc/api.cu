@@ -60,7 +60,7 @@ fp8w_status check_cache(const fp8w_kv_cache* c, int act) {
     if (c->num_pages < 1 || c->num_pages > FP8W_MAX_DIM - 1 || c->kv_heads < 1 || c->kv_heads > 65536 ||
         c->head_dim < 16 || c->head_dim > 128 || c->head_dim % 16 != 0)
         return FP8W_ERR_SHAPE;
-    if (c->page_size < 8 || c->page_size > 256 || (c->page_size & (c->page_size - 1)) != 0) return FP8W_ERR_SHAPE;
+    if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)) != 0) return FP8W_ERR_SHAPE;
     const int64_t bytes = codes ? 1 : 2, most = (1ll << 40) / bytes;
     if (c->token_stride < c->head_dim || c->head_stride < c->head_dim || c->page_stride < c->head_dim ||
         c->token_stride >= most || c->head_stride >= most || c->page_stride >= most)

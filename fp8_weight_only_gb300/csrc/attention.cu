@@ -17,10 +17,10 @@
 // With more than 128 rows the pipes take the two row tiles and share every key
 // tile; with fewer, both take the same rows and the key tiles in turn, and
 // their two partial results are joined at the end.
-//   warps 0-3, 4-7  softmax of pipe 0, 1: one row a thread
-//   warp 8          TMA producer of key and value tiles, a lane a page
-//   warp 9          MMA issue; owns TMEM
-//   warps 12-15     (e4m3 cache) codes -> 16-bit operand tiles
+//   warps 0-7, 8-15 softmax of pipe 0, 1: two threads a row, half its keys each
+//   warp 16         TMA producer of key and value tiles, a lane a page
+//   warp 17         MMA issue; owns TMEM
+//   warps 20-23     (e4m3 cache) codes -> 16-bit operand tiles
 // The reference m moves only when a row's maximum has grown by more than
 // 2^8 (kSlack) over it: then the row's O is rescaled, after the MMA that is
 // adding to it.  p stays below 2^8, and the sums are fp32.
@@ -34,9 +34,9 @@
 // Every wait is bounded; a CTA that gives up records a code, raises its abort
 // flag, lets its copies and MMAs land and frees TMEM.
 #include <mutex>
+#include <type_traits>
 
-#include "fp8w_device.cuh"
-#include "fp8w_internal.h"
+#include "attention.cuh"
 
 namespace fp8w {
 
@@ -47,10 +47,13 @@ namespace {
 constexpr int kKeys = 128;            // keys a tile
 constexpr int kRows = 128;            // rows a tile (TMEM lanes)
 constexpr int kMaxAttnCluster = 16;
+// Up to this many rows a key head (new tokens x its query heads) the kernel for
+// few rows reads the cache faster.
+constexpr int kFewRows = 32;
 constexpr uint32_t kAttnTmemCols = 512;
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kConvWarp = 12;
-constexpr int kBarSoftmax = 1;        // named barrier of the eight softmax warps
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kSoftmaxThreads = 512;   // sixteen warps
+constexpr int kLoadWarp = 16, kMmaWarp = 17, kConvWarp = 20;
+constexpr int kBarSoftmax = 1;        // named barrier of the softmax warps; 2..9: of the pairs that share rows
 
 template <int DP, bool kFp8>
 struct AttnSmem {
@@ -68,37 +71,21 @@ struct AttnSmem {
     static constexpr uint32_t kRawOff = kRingOff + kStages * kTileBytes;
     static constexpr uint32_t kScaleOff = kRawOff + kRaw * kRawBytes;  // [slot][k, v][128] fp32
     static constexpr uint32_t kMlOff = kScaleOff + (kFp8 ? kScaleSlots * 2 * kKeys * 4 : 0);
-    static constexpr uint32_t kBarOff = kMlOff + kRows * 8;
+    static constexpr uint32_t kJoinedOff = kMlOff + kRows * 8;   // (m, l) of the CTA's rows, for the cluster
+    static constexpr uint32_t kBarOff = kJoinedOff + kRows * 8;
     // full, empty [kStages] | rawfull, rawempty [kRaw] | sfull, pfull, ofull [2] | qfull | joinfull, joinfree | drain
     static constexpr uint32_t kNumBars = 2 * kStages + 2 * kRaw + 6 + 1 + 2 + 1;
     static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;
     static constexpr uint32_t kBytes = kMiscOff + 16;
-    static_assert(kBytes <= 227 * 1024, "shared memory");
-    static constexpr int kThreads = kFp8 ? 512 : 384;
-    // registers a thread after the split; the launch has 65536 / 512 = 128 or 65536 / 384 -> 168 a thread
-    static constexpr int kRegsSoftmax = kFp8 ? 184 : 216;
-    static constexpr int kRegsIssue = kFp8 ? 64 : 72;
-    static constexpr int kRegsConv = 80;
-    static_assert(256 * kRegsSoftmax + 128 * kRegsIssue + (kFp8 ? 128 * kRegsConv : 0) <= kThreads * (kFp8 ? 128 : 168),
-                  "register split");
-};
-
-struct AttnParams {
-    const uint16_t* q;
-    uint16_t* out;
-    int64_t q_stride, out_stride, tokens;
-    const int32_t* table;
-    const int32_t* lens;
-    const int32_t* starts;
-    int64_t table_width;
-    const float* k_scales;
-    const float* v_scales;
-    int64_t num_pages;
-    int seqs, kv_heads, group, head_dim, page_size, log_page;
-    float c;         // scale * log2(e)
-    int64_t window;  // 0: none
-    int row_tiles;   // bound on the 256-row tiles of all sequences
-    int cl;
+    static_assert(kBytes <= 227 * 1024 && kMlOff % 1024 == 0, "shared memory");
+    static constexpr int kConvGroups = kFp8 ? 1 : 0;             // converting warpgroups
+    static constexpr int kThreads = kSoftmaxThreads + 128 + 128 * kConvGroups;
+    // registers a thread at launch and after the split
+    static constexpr int kRegs = 65536 / kThreads / 8 * 8;
+    static constexpr int kRegsSoftmax = kFp8 ? 88 : 104;
+    static constexpr int kRegsIssue = kFp8 ? 56 : 64;
+    static constexpr int kRegsConv = 72;
+    static_assert(kSoftmaxThreads * kRegsSoftmax + 128 * kRegsIssue + 128 * kConvGroups * kRegsConv <= kThreads * kRegs, "register split");
 };
 
 __device__ __forceinline__ void attn_error(int code, volatile int* abort_flag) {
@@ -156,11 +143,14 @@ __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t* r) {
         : "memory");
 }
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
 }
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -183,17 +173,6 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 }
 __device__ __forceinline__ float lo2(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
 __device__ __forceinline__ float hi2(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
-
-// Two fp32 -> packed 16-bit pair (first in the low half), rounded to nearest.
-template <bool kBf16>
-__device__ __forceinline__ uint32_t pack16(float first, float second) {
-    uint32_t r;
-    if constexpr (kBf16)
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(second), "f"(first));
-    else
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(second), "f"(first));
-    return r;
-}
 
 // B operand with its N values contiguous (the value tile: rows are keys, K of
 // the product): 128-byte swizzled atoms of 8 keys x 64 values, 1024 bytes
@@ -228,20 +207,22 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
         if ((i & 63u) == 0 && (*abort_flag || cycles() - t0 > kWaitLimitCycles)) return false;
     }
 }
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+// Shared-memory accesses by address.  lds_f4 is free to move (its address
+// says after what).
+__device__ __forceinline__ float4 lds_f4(uint32_t addr) {
     float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
+    asm("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
     return v;
 }
-__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
+__device__ __forceinline__ float2 lds_f2(uint32_t addr) {
     float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
     return v;
 }
-__device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync %0, 256;" ::"n"(kBarSoftmax) : "memory"); }
+__device__ __forceinline__ void sts_f2(uint32_t addr, float x, float y) {
+    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
+}
+__device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync %0, %1;" ::"n"(kBarSoftmax), "n"(kSoftmaxThreads) : "memory"); }
 
 // What a CTA works on: rows [row0, row0 + rows) of sequence seq (rows counted
 // token * group + head), key tiles [t0, t0 + cnt), of which pipe 0 takes the
@@ -256,69 +237,17 @@ struct Work {
     bool two;
 };
 
-// The sequence of 256-row tile `tile` and the tile's number in it, by a scan
-// of the sequences' new tokens 32 at a time.  Every warp computes it alike.
 __device__ __forceinline__ bool find_work(const AttnParams& p, int tile, int head, int rank, Work& w, bool report) {
-    const int lane = threadIdx.x & 31;
-    int64_t begin = 0, count = 0;
-    int seq = -1, inner = 0;
-    if (!p.starts) {
-        const int per = (p.group + 2 * kRows - 1) / (2 * kRows);
-        seq = tile / per;
-        inner = tile - seq * per;
-        if (seq >= p.seqs) return false;
-        begin = seq;
-        count = 1;
-    } else {
-        int64_t before = 0;
-        for (int b0 = 0; b0 < p.seqs; b0 += 32) {
-            const int b = b0 + lane;
-            int64_t s = 0, n = 0, t = 0;
-            if (b < p.seqs) {
-                s = __ldg(p.starts + b);
-                n = __ldg(p.starts + b + 1) - s;
-                if (s < 0 || n < 0 || s + n > p.tokens) {
-                    if (report) atomicCAS(&g_attention_error, 0, 7000 + kErrIndex);
-                    n = 0;
-                }
-                t = (n * p.group + 2 * kRows - 1) / (2 * kRows);
-            }
-            int64_t sum = t;  // inclusive prefix over the lanes
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int64_t o = __shfl_up_sync(0xffffffffu, sum, d);
-                if (lane >= d) sum += o;
-            }
-            const unsigned hit = __ballot_sync(0xffffffffu, before + sum > tile);
-            if (hit && seq < 0) {
-                const int l = __ffs(hit) - 1;
-                seq = b0 + l;
-                inner = static_cast<int>(tile - before - __shfl_sync(0xffffffffu, sum - t, l));
-                begin = __shfl_sync(0xffffffffu, s, l);
-                count = __shfl_sync(0xffffffffu, n, l);
-                // later rows see more keys: they go first
-                inner = static_cast<int>((count * p.group + 2 * kRows - 1) / (2 * kRows)) - 1 - inner;
-                if (!report) break;
-            }
-            before += __shfl_sync(0xffffffffu, sum, 31);
-        }
-        if (report && before > p.row_tiles && lane == 0) atomicCAS(&g_attention_error, 0, 7000 + kErrIndex);
-        if (seq < 0) return false;
-    }
-    w.seq = seq;
+    SeqTile f;
+    if (!find_tile(p, 2 * kRows, tile, report, &g_attention_error, f)) return false;
+    w.seq = f.seq;
     w.head = head;
-    w.token0 = begin;
-    w.total_rows = static_cast<int>(count * p.group);
-    w.row0 = inner * 2 * kRows;
+    w.token0 = f.begin;
+    w.total_rows = static_cast<int>(f.count * p.group);
+    w.row0 = f.inner * 2 * kRows;
     w.rows = w.total_rows - w.row0 < 2 * kRows ? w.total_rows - w.row0 : 2 * kRows;
     w.two = w.rows > kRows;
-    int64_t len = __ldg(p.lens + seq);
-    if (len < 0 || len > p.table_width * p.page_size) {
-        if (report || (head == 0 && rank == 0 && inner == 0 && threadIdx.x == 0))
-            atomicCAS(&g_attention_error, 0, 7000 + kErrIndex);
-        len = 0;
-    }
-    w.pos0 = static_cast<int>(len - count);
+    w.pos0 = static_cast<int>(f.len - f.count);
     const int last = w.pos0 + (w.row0 + w.rows - 1) / p.group;    // position of the last row
     const int low = w.pos0 + w.row0 / p.group;                    // and of the first
     const int mid = w.pos0 + (w.row0 + kRows - 1) / p.group;      // and of row tile 0's last
@@ -360,6 +289,13 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // fp16 weights with e4m3 scales: p * v_scale * 2^4 keeps the products of
+    // small scales among fp16's normal numbers, and with p below 2^4 it cannot
+    // overflow (scales reach 65504 / 448 = 146.2 for fp16 values).  No slack and
+    // 2^8 would reach smaller scales, but rescales O at most of the first tiles.
+    constexpr bool kScaledF16 = kFp8 && !kBf16;
+    constexpr float kSlack = kScaledF16 ? 4.0f : 8.0f;
+    constexpr float kPScale = kScaledF16 ? 16.0f : 1.0f;
 
     if (warp == kMmaWarp) {
         tmem_alloc(smem_u32(tmem_slot), kAttnTmemCols);
@@ -367,19 +303,19 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
     } else if (warp == kLoadWarp) {
         if (lane == 0) {
             for (int s = 0; s < kStages; ++s) {
-                mbar_init(full(s), kFp8 ? 4 : 1);  // the converting warps, or the producer
+                mbar_init(full(s), kFp8 ? 4 * L::kConvGroups : 1);  // the converting warps, or the producer
                 mbar_init(empty(s), 1);            // MMA commit
             }
             for (int s = 0; s < kRaw; ++s) {
                 mbar_init(rawfull(s), 1);
-                mbar_init(rawempty(s), 4);
+                mbar_init(rawempty(s), 4 * L::kConvGroups);
             }
             for (int i = 0; i < 2; ++i) {
                 mbar_init(sfull(i), 1);
-                mbar_init(pfull(i), 4);  // the pipe's softmax warps
+                mbar_init(pfull(i), 8);  // the pipe's softmax warps
                 mbar_init(ofull(i), 1);
             }
-            mbar_init(qfull, 8);
+            mbar_init(qfull, kSoftmaxThreads / 32);
             mbar_init(joinfull, static_cast<uint32_t>(p.cl));
             mbar_init(joinfree, static_cast<uint32_t>(p.cl));
             mbar_init(drain, 1);
@@ -419,18 +355,19 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             const int box = p.page_size < kKeys ? p.page_size : kKeys;
             const int boxes = kKeys / box;
             const int32_t* row = p.table + static_cast<int64_t>(w.seq) * p.table_width;
-            auto page_of = [&](int t) -> int {  // page of this lane's box of key tile t, or one past the cache
-                const int key = t * kKeys + lane * box;
-                if (lane >= boxes || key >= w.end || key + box <= w.first_key) return static_cast<int>(p.num_pages);
-                const int pg = __ldg(row + (key >> p.log_page));
-                if (pg < 0 || pg >= p.num_pages) {
-                    atomicCAS(&g_attention_error, 0, 7000 + kErrIndex);
-                    return static_cast<int>(p.num_pages);
-                }
-                return pg;
+            // a lane's table entry is read two key tiles before its use and checked
+            // there, so the table is not waited for
+            auto wanted = [&](int j) {  // this lane's box of key tile j holds a position that some row sees
+                const int key = (w.t0 + j) * kKeys + lane * box;
+                return j < n && lane < boxes && key < w.end && key + box > w.first_key;
             };
-            // boxes past the cache read as zeros
-            int pk = page_of(w.t0), pv = pk, next = n > 1 ? page_of(w.t0 + 1) : 0;
+            auto entry_of = [&](int j) { return wanted(j) ? __ldg(row + (((w.t0 + j) * kKeys + lane * box) >> p.log_page)) : 0; };
+            auto page_of = [&](int j, int entry) -> int {  // one past the cache (which reads as zeros) for no page
+                if (wanted(j) && entry >= 0 && entry < p.num_pages) return entry;
+                if (wanted(j)) atomicCAS(&g_attention_error, 0, 7000 + kErrIndex);
+                return static_cast<int>(p.num_pages);
+            };
+            int e0 = entry_of(0), e1 = entry_of(1), e2 = 0, pk = 0, pv = 0;
             bool ok = true;
             int i = 0;
             for (; i < 2 * n; ++i) {
@@ -438,17 +375,14 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                 const bool is_k = i == 0 || (i < 2 * n - 1 && (i & 1));
                 const uint32_t fullb = kFp8 ? rawfull(s) : full(s), emptyb = kFp8 ? rawempty(s) : empty(s);
                 const int j = i == 0 ? 0 : is_k ? (i + 1) / 2 : i == 2 * n - 1 ? n - 1 : (i - 2) / 2;
-                int pg;
                 if (is_k) {
-                    if (j > 0) {
-                        pv = pk;
-                        pk = next;
-                        next = j + 1 < n ? page_of(w.t0 + j + 1) : 0;
-                    }
-                    pg = pk;
-                } else {
-                    pg = j == n - 1 ? pk : pv;
+                    e2 = entry_of(j + 2);
+                    pv = pk;
+                    pk = page_of(j, e0);
+                    e0 = e1;
+                    e1 = e2;
                 }
+                const int pg = is_k || j == n - 1 ? pk : pv;
                 if (!mbar_wait_warp(emptyb, static_cast<uint32_t>((i / kR) & 1) ^ 1u, abort_flag)) {
                     if (lane == 0) attn_error(kErrWaitSlot, abort_flag);
                     ok = false;
@@ -589,35 +523,51 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
         // --------------------------------------- codes to operand tiles --
         if constexpr (kFp8) {
             reg_down<L::kRegsConv>();
+            // One key a thread; with two warpgroups each converts half of the row.
+            // (Tiles in turn would need an even number of stages: a warpgroup that
+            // runs ahead on a stage of the other's could take one phase for another.)
+            constexpr int kGroups = L::kConvGroups, kChunks = DP / 16 / kGroups;  // 16-code chunks a thread
+            const int h = (warp - kConvWarp) >> 2;
             const int r = (warp & 3) * 32 + lane;  // key of the tile
             const uint32_t swz = static_cast<uint32_t>(r & 7);
             const int32_t* row = p.table + static_cast<int64_t>(w.seq) * p.table_width;
+            auto live_at = [&](int j) {
+                const int key = (w.t0 + j) * kKeys + r;
+                return j < n && key < w.end && key >= w.first_key;
+            };
+            // Behind a tile's page stand its scales: the page is read two key tiles
+            // ahead and the scales one, and neither is used before it is needed, so
+            // neither is waited for.
+            const int64_t head_scales = static_cast<int64_t>(w.head) * p.page_size;
+            const int64_t page_scales = static_cast<int64_t>(p.kv_heads) * p.page_size;
+            auto page_at = [&](int j) { return live_at(j) ? __ldg(row + (((w.t0 + j) * kKeys + r) >> p.log_page)) : -1; };
+            auto scales_at = [&](int j, int pg) {
+                if (pg < 0 || pg >= p.num_pages) return make_float2(0.0f, 0.0f);
+                const int64_t at = head_scales + pg * page_scales + (((w.t0 + j) * kKeys + r) & (p.page_size - 1));
+                return make_float2(__ldg(p.k_scales + at), __ldg(p.v_scales + at));
+            };
+            float2 next = scales_at(0, page_at(0));
+            int page = page_at(1);
             for (int i = 0; i < 2 * n; ++i) {
                 const bool is_k = i == 0 || (i < 2 * n - 1 && (i & 1));
                 const int j = i == 0 ? 0 : is_k ? (i + 1) / 2 : i == 2 * n - 1 ? n - 1 : (i - 2) / 2;
-                const int key = (w.t0 + j) * kKeys + r;
-                const bool live = key < w.end && key >= w.first_key;
-                // the softmax needs both scales of a tile as soon as its scores are there
-                float scale_k = 0.0f, scale_v = 0.0f;
-                if (live && is_k) {
-                    const int64_t pg = __ldg(row + (key >> p.log_page));
-                    if (pg >= 0 && pg < p.num_pages) {
-                        const int64_t at = (pg * p.kv_heads + w.head) * p.page_size + (key & (p.page_size - 1));
-                        scale_k = __ldg(p.k_scales + at);
-                        scale_v = __ldg(p.v_scales + at);
-                    }
+                const bool live = live_at(j);
+                const float2 scale = next;
+                if (is_k && h == 0) {
+                    next = scales_at(j + 1, page);
+                    page = page_at(j + 2);
                 }
                 const int s = i % kRaw, d = i % kStages;
                 if (!mbar_wait_warp(rawfull(s), static_cast<uint32_t>((i / kRaw) & 1), abort_flag)) {
                     if (lane == 0) attn_error(kErrWaitTma, abort_flag);
                     break;
                 }
-                uint4 c[DP / 16];
+                uint4 c[kChunks];
                 const uint32_t src = sbase + L::kRawOff + s * L::kRawBytes + static_cast<uint32_t>(r) * DP;
 #pragma unroll
-                for (uint32_t u = 0; u < DP / 16; ++u) {
-                    const uint32_t at = DP == 128 ? u ^ swz : u ^ (swz >> 1);  // 128- or 64-byte swizzle
-                    c[u] = lds128(src + (at << 4));
+                for (uint32_t u = 0; u < kChunks; ++u) {
+                    const uint32_t ch = h * kChunks + u;
+                    c[u] = lds128(src + ((DP == 128 ? ch ^ swz : ch ^ (swz >> 1)) << 4));  // 128- or 64-byte swizzle
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(rawempty(s));
@@ -627,7 +577,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                 }
                 const uint32_t dst = sbase + L::kRingOff + d * L::kTileBytes + static_cast<uint32_t>(r) * 128u;
 #pragma unroll
-                for (uint32_t u = 0; u < DP / 16; ++u) {
+                for (uint32_t u = 0; u < kChunks; ++u) {
                     const uint32_t w4[4] = {live ? c[u].x : 0u, live ? c[u].y : 0u, live ? c[u].z : 0u, live ? c[u].w : 0u};
                     uint32_t v[8];
 #pragma unroll
@@ -637,15 +587,16 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                         else
                             e4m3x4_to_f16x2(w4[e], v[2 * e], v[2 * e + 1]);
                     }
-                    // 16 values: 16-byte chunks 2u and 2u + 1 of the row
-                    const uint32_t sub = dst + (u >> 2) * (kKeys * 128);
-                    sts128(sub + (((2 * u) & 7) ^ swz) * 16, v[0], v[1], v[2], v[3]);
-                    sts128(sub + (((2 * u + 1) & 7) ^ swz) * 16, v[4], v[5], v[6], v[7]);
+                    // 16 values: 16-byte chunks 2 ch and 2 ch + 1 of the row
+                    const uint32_t ch = h * kChunks + u;
+                    const uint32_t sub = dst + (ch >> 2) * (kKeys * 128);
+                    sts128(sub + (((2 * ch) & 7) ^ swz) * 16, v[0], v[1], v[2], v[3]);
+                    sts128(sub + (((2 * ch + 1) & 7) ^ swz) * 16, v[4], v[5], v[6], v[7]);
                 }
-                if (is_k) {
+                if (is_k && h == 0) {  // the softmax needs both as soon as the tile's scores are there
                     float* sc = reinterpret_cast<float*>(smem + L::kScaleOff) + (j % L::kScaleSlots) * 2 * kKeys + r;
-                    sc[0] = scale_k;
-                    sc[kKeys] = scale_v;
+                    sc[0] = scale.x * p.c;
+                    sc[kKeys] = scale.y * kPScale;
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -655,30 +606,51 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
     } else {
         // ------------------------------------------------------ softmax --
         reg_up<L::kRegsSoftmax>();
-        const int pipe = warp >> 2, quarter = warp & 3;
-        const int tid = threadIdx.x;                    // 0..255
-        const int r = quarter * 32 + lane;              // row of the tile == TMEM lane
+        const int pipe = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
+        const int tid = threadIdx.x;                    // 0..511
+        const int r = quarter * 32 + lane;              // TMEM lane
         const int qtile = w.two ? pipe : 0;
-        // Q rows: the two tiles, 16 bytes a step
+        // Few rows: copies of them in the lanes' halves or quarters, each copy's
+        // threads on its own part of the keys (its P is zero elsewhere), so all
+        // warps share a tile's softmax.  The copies' results are joined.
+        const int split = w.two ? 1 : w.rows <= kRows / 4 ? 4 : w.rows <= kRows / 2 ? 2 : 1;
+        const int per_copy = kRows / split;
+        const int copy = r / per_copy, rr = r - copy * per_copy;
+        const int width = kKeys / 2 / split;            // keys of a tile for this thread
+        const int cbeg = (copy * 2 + half) * width;     // the first of them
+        // Q rows, 16 bytes a step, eight steps' reads in flight
         if (n > 0) {
-            const int chunks = DP / 8;
-            for (int u = tid; u < w.rows * chunks; u += 256) {
-                const int rr = u / chunks, ch = u - rr * chunks;
-                const int R = w.row0 + rr, t = R / p.group, g = R - t * p.group;
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (ch * 8 < p.head_dim)
-                    v = *reinterpret_cast<const uint4*>(p.q + (w.token0 + t) * p.q_stride +
-                                                        static_cast<int64_t>(w.head * p.group + g) * p.head_dim + ch * 8);
-                const uint32_t a = sbase + L::kQOff + (rr >> 7) * L::kTileBytes + (ch >> 3) * (kRows * 128) +
-                                   (rr & 127) * 128 + (((ch & 7) ^ (rr & 7)) << 4);
-                sts128(a, v.x, v.y, v.z, v.w);
+            constexpr int kChunks = DP / 8, kLines = kSoftmaxThreads / kChunks;
+            const int ch = tid % kChunks, lines = w.rows * split;
+            const bool inside = ch * 8 < p.head_dim;
+            const uint16_t* q_head = p.q + w.token0 * p.q_stride + static_cast<int64_t>(w.head * p.group) * p.head_dim + ch * 8;
+            for (int line0 = tid / kChunks; line0 < lines; line0 += 8 * kLines) {
+                uint4 v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int line = line0 + i * kLines;
+                    v[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (line < lines && inside) {
+                        const int row = w.row0 + (split > 1 ? line % w.rows : line), t = row / p.group, g = row - t * p.group;
+                        v[i] = *reinterpret_cast<const uint4*>(q_head + t * p.q_stride + g * p.head_dim);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int line = line0 + i * kLines;
+                    if (line >= lines) break;
+                    const int f = split > 1 ? line / w.rows : 0, at = f * per_copy + line - f * w.rows;  // row of the two tiles
+                    const uint32_t a = sbase + L::kQOff + (at >> 7) * L::kTileBytes + (ch >> 3) * (kRows * 128) +
+                                       (at & 127) * 128 + (((ch & 7) ^ (at & 7)) << 4);
+                    sts128(a, v[i].x, v[i].y, v[i].z, v[i].w);
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(qfull);
         }
-        const int R = w.row0 + qtile * kRows + r;
-        const bool valid = qtile * kRows + r < w.rows;
+        const int R = w.row0 + qtile * kRows + rr;
+        const bool valid = qtile * kRows + rr < w.rows;
         const int pos = w.pos0 + R / p.group;
         const int hi = valid ? pos : -1;                                     // last position seen
         const int64_t from = p.window > 0 ? static_cast<int64_t>(pos) - p.window + 1 : 0;
@@ -687,20 +659,163 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
         const int warp_hi = __reduce_min_sync(0xffffffffu, valid ? hi : 0x7fffffff);
         const int warp_lo = __reduce_max_sync(0xffffffffu, valid ? lo : 0);
         const uint32_t tq = static_cast<uint32_t>(quarter * 32) << 16;
-        const uint32_t t_s = tmem + tq + pipe * kKeys, t_o = tmem + tq + 2 * kKeys + pipe * DP;
-        // fp16 weights with e4m3 scales: p * v_scale * 2^8 keeps the products of
-        // small scales among fp16's normal numbers, and cannot overflow with p <= 1
-        // (scales reach 65504 / 448 = 146.2 for fp16 values): no slack there
-        constexpr bool kScaledF16 = kFp8 && !kBf16;
-        constexpr float kSlack = kScaledF16 ? 0.0f : 8.0f;
-        constexpr float kPScale = kScaledF16 ? 256.0f : 1.0f;
+        const uint32_t t_s = tmem + tq + pipe * kKeys, t_o = tmem + tq + 2 * kKeys + pipe * DP + half * (DP / 2);
         const float c = p.c;
         const uint64_t c2 = pack2(c, c);
-        float m = __int_as_float(0xff800000), l = 0.0f;
-        const int step = w.two ? 1 : 2, j0 = w.two ? 0 : pipe, jn = w.two && pipe == 0 ? w.cnt0 : n;
-        int done = 0;  // tiles of this pipe
+        float m = kNegInf, l = 0.0f;  // the row's reference, in exponents of two, and its sum
+        int done = 0;                 // tiles of this pipe
         bool ok = true;
-        for (int j = j0; j < jn; j += step, ++done) {
+
+        // One tile for this thread's row and W keys from cbeg: P over S, m, l and,
+        // where m moved, its half of O.  The row's other thread has the same m.
+        const uint32_t pair = 2 + pipe * 4 + quarter;   // the pair's barrier
+        const uint32_t mine = sbase + L::kMlOff + ((pipe * 2 + half) * kRows + r) * 4, theirs = mine ^ (kRows * 4);
+        auto softmax_tile = [&](auto w_tag, int j) {
+            constexpr int W = decltype(w_tag)::value;
+            constexpr int kStep = W < 32 ? W : 32;
+            const int key0 = (w.t0 + j) * kKeys + cbeg;
+            const bool masked = key0 + W - 1 > warp_hi || key0 < warp_lo;
+            // address taken after the wait, so the reads below stay behind it
+            uint32_t ksc = sbase + L::kScaleOff + (j % L::kScaleSlots) * (2 * kKeys * 4) + cbeg * 4;
+            asm volatile("" : "+r"(ksc)::"memory");
+            uint32_t o[W / 2];
+            float mx;
+            uint64_t l0, l1;
+            // o = 2^(scores - m), packed, their sums, and the largest score; 32 keys at a time
+            auto weights = [&]() {
+                const float mc = m == kNegInf ? 0.0f : -m;
+                const uint64_t mc2 = pack2(mc, mc);
+                float my = kNegInf;
+                mx = kNegInf;
+                l0 = l1 = 0ull;
+                uint32_t s[2][kStep];
+                auto read = [&](int b) {
+                    if constexpr (W == 16)
+                        tmem_ld_x16_sync(t_s + cbeg, reinterpret_cast<uint32_t(&)[16]>(s[0]));
+                    else
+                        tmem_ld_x32(t_s + cbeg + b, s[kFp8 ? 0 : (b / kStep) & 1]);
+                };
+                read(0);
+                if constexpr (!kFp8 && W == 64) read(32);
+#pragma unroll
+                for (int b = 0; b < W; b += kStep) {
+                    uint32_t* v = s[kFp8 ? 0 : (b / kStep) & 1];
+                    if constexpr (W > 16) {
+                        if (kFp8 && b > 0) read(b);
+                        tmem_wait_ld_x32(v);
+                    }
+                    if constexpr (kFp8) {  // key scales (which hold c)
+#pragma unroll
+                        for (int i = 0; i < kStep; i += 4) {
+                            const float4 f = lds_f4(ksc + (b + i) * 4);
+                            const uint64_t x = mul2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), pack2(f.x, f.y));
+                            const uint64_t y = mul2(pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), pack2(f.z, f.w));
+                            v[i] = static_cast<uint32_t>(x), v[i + 1] = static_cast<uint32_t>(x >> 32);
+                            v[i + 2] = static_cast<uint32_t>(y), v[i + 3] = static_cast<uint32_t>(y >> 32);
+                        }
+                    }
+                    if (masked) {
+                        const int top = hi - key0 - b, bot = lo - key0 - b;
+#pragma unroll
+                        for (int i = 0; i < kStep; ++i)
+                            if (i > top || i < bot) v[i] = 0xff800000u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kStep; i += 4) {
+                        mx = max3(mx, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                        my = max3(my, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+                        uint64_t x = pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                        uint64_t y = pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+                        x = kFp8 ? add2(x, mc2) : fma2(x, c2, mc2);
+                        y = kFp8 ? add2(y, mc2) : fma2(y, c2, mc2);
+                        x = pack2(ex2(lo2(x)), ex2(hi2(x)));
+                        y = pack2(ex2(lo2(y)), ex2(hi2(y)));
+                        l0 = add2(l0, x);
+                        l1 = add2(l1, y);
+                        if constexpr (kFp8) {
+                            const float4 f = lds_f4(ksc + (kKeys + b + i) * 4);
+                            x = mul2(x, pack2(f.x, f.y));
+                            y = mul2(y, pack2(f.z, f.w));
+                        }
+                        o[(b + i) / 2] = pack16<kBf16>(lo2(x), hi2(x));
+                        o[(b + i) / 2 + 1] = pack16<kBf16>(lo2(y), hi2(y));
+                    }
+                    if constexpr (kFp8) asm volatile("" : "+r"(ksc));  // scales of one part at a time
+                }
+                mx = fmaxf(mx, my);
+                if constexpr (!kFp8) mx *= c;
+            };
+            // The weights are taken with the m of the tiles before, without waiting
+            // for this one's maximum; where that turns out to lie too far above
+            // (always in the first tile), m moves and they are taken again.  Both
+            // threads of a row go on with the same m, and neither writes P before
+            // the other has read its scores.
+            weights();
+            tc_fence_before();
+            const bool moves = bar_red_or(pair, 64, done == 0 || (valid && mx - m > kSlack));  // -inf - -inf: no
+            tc_fence_after();
+            if (moves) {
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine), "f"(mx) : "memory");
+                asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+                float other;
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(theirs) : "memory");
+                mx = fmaxf(mx, other);
+                float alpha = 1.0f;
+                if (done == 0) {
+                    m = mx;
+                } else {
+                    if (valid && mx - m > kSlack) {
+                        alpha = ex2(m - mx);  // 0 while nothing was seen
+                        m = mx;
+                        l *= alpha;
+                    }
+                    // O is at rest once the last product has been added
+                    if (!mbar_wait_warp(ofull(pipe), static_cast<uint32_t>((done - 1) & 1), abort_flag)) {
+                        if (lane == 0) attn_error(kErrWaitMma, abort_flag);
+                        ok = false;
+                        return;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int b = 0; b < DP / 2; b += 16) {
+                        uint32_t v[16];
+                        tmem_ld_x16_sync(t_o + b, v);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+                        tmem_st_x16(t_o + b, v);
+                    }
+                }
+                weights();
+                // the other thread has read its scores too
+                tc_fence_before();
+                asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+                tc_fence_after();
+            }
+#pragma unroll
+            for (int b = 0; b < W / 2; b += kStep / 2) {
+                if constexpr (W == 64) {
+                    tmem_st_x16(t_s + cbeg / 2 + b, o + b);
+                } else {
+#pragma unroll
+                    for (int f = 0; f < kKeys / 2 / W; ++f) {  // zero in the other copies' keys
+                        uint32_t v[W / 2];
+#pragma unroll
+                        for (int i = 0; i < W / 2; ++i) v[i] = f == copy ? o[i] : 0u;
+                        if constexpr (W == 32)
+                            tmem_st_x16(t_s + (f * 2 + half) * (W / 2), v);
+                        else
+                            tmem_st_x8(t_s + (f * 2 + half) * (W / 2), v);
+                    }
+                }
+            }
+            l0 = add2(l0, l1);
+            l += lo2(l0) + hi2(l0);
+            tmem_wait_st();
+            tc_fence_before();
+        };
+
+        const int step = w.two ? 1 : 2, jn = w.two && pipe == 0 ? w.cnt0 : n;
+        for (int j = w.two ? 0 : pipe; j < jn; j += step, ++done) {
             if (!mbar_wait_warp(sfull(pipe), static_cast<uint32_t>(done & 1), abort_flag)) {
                 if (lane == 0) attn_error(kErrWaitMma, abort_flag);
                 ok = false;
@@ -708,94 +823,13 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             }
             tc_fence_after();
             if (busy) {
-                const int key0 = (w.t0 + j) * kKeys;
-                uint32_t s[128];
-#pragma unroll
-                for (int b = 0; b < 4; ++b) tmem_ld_x32(t_s + 32 * b, s + 32 * b);
-#pragma unroll
-                for (int b = 0; b < 4; ++b) tmem_wait_ld_x32(s + 32 * b);
-                const float* ksc = reinterpret_cast<const float*>(smem + L::kScaleOff) + (j % L::kScaleSlots) * 2 * kKeys;
-                if constexpr (kFp8) {
-#pragma unroll
-                    for (int i = 0; i < 128; i += 4) {
-                        const float4 f = *reinterpret_cast<const float4*>(ksc + i);
-                        const uint64_t a = mul2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), pack2(f.x, f.y));
-                        const uint64_t b = mul2(pack2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), pack2(f.z, f.w));
-                        s[i] = static_cast<uint32_t>(a), s[i + 1] = static_cast<uint32_t>(a >> 32);
-                        s[i + 2] = static_cast<uint32_t>(b), s[i + 3] = static_cast<uint32_t>(b >> 32);
-                    }
-                }
-                if (key0 + kKeys - 1 > warp_hi || key0 < warp_lo) {
-                    const int top = hi - key0, bot = lo - key0;
-#pragma unroll
-                    for (int i = 0; i < 128; ++i)
-                        if (i > top || i < bot) s[i] = 0xff800000u;
-                }
-                float mx = __uint_as_float(s[0]), my = __uint_as_float(s[1]);
-#pragma unroll
-                for (int i = 2; i < 126; i += 4) {
-                    mx = max3(mx, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-                    my = max3(my, __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
-                }
-                mx = max3(mx, __uint_as_float(s[126]), __uint_as_float(s[127]));
-                mx = fmaxf(mx, my);
-                if (done == 0) {
-                    m = mx;
-                } else {
-                    const bool grow = valid && (mx - m) * c > kSlack;  // -inf - -inf: no
-                    if (__any_sync(0xffffffffu, grow)) {
-                        float alpha = 1.0f;
-                        if (grow) {
-                            alpha = ex2((m - mx) * c);  // 0 while nothing was seen
-                            m = mx;
-                            l *= alpha;
-                        }
-                        // O is at rest once the last product has been added
-                        if (!mbar_wait_warp(ofull(pipe), static_cast<uint32_t>((done - 1) & 1), abort_flag)) {
-                            if (lane == 0) attn_error(kErrWaitMma, abort_flag);
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-#pragma unroll
-                        for (int b = 0; b < DP; b += 32) {
-                            uint32_t o[32];
-                            tmem_ld_x32(t_o + b, o);
-                            tmem_wait_ld_x32(o);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                            tmem_st_x32(t_o + b, o);
-                        }
-                    }
-                }
-                const float mc = m == __int_as_float(0xff800000) ? 0.0f : -m * c;
-                const uint64_t mc2 = pack2(mc, mc);
-                uint64_t l0 = 0ull, l1 = 0ull;
-                uint32_t o[32];
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-#pragma unroll
-                    for (int i = 0; i < 64; i += 4) {
-                        const int at = b * 64 + i;
-                        const uint64_t x = fma2(pack2(__uint_as_float(s[at]), __uint_as_float(s[at + 1])), c2, mc2);
-                        const uint64_t y = fma2(pack2(__uint_as_float(s[at + 2]), __uint_as_float(s[at + 3])), c2, mc2);
-                        uint64_t e = pack2(ex2(lo2(x)), ex2(hi2(x))), f = pack2(ex2(lo2(y)), ex2(hi2(y)));
-                        l0 = add2(l0, e);
-                        l1 = add2(l1, f);
-                        if constexpr (kFp8) {
-                            const float4 v = *reinterpret_cast<const float4*>(ksc + kKeys + at);
-                            e = mul2(e, pack2(v.x * kPScale, v.y * kPScale));
-                            f = mul2(f, pack2(v.z * kPScale, v.w * kPScale));
-                        }
-                        o[i / 2] = pack16<kBf16>(lo2(e), hi2(e));
-                        o[i / 2 + 1] = pack16<kBf16>(lo2(f), hi2(f));
-                    }
-                    tmem_st_x32(t_s + b * 32, o);
-                }
-                l0 = add2(l0, l1);
-                l += lo2(l0) + hi2(l0);
-                tmem_wait_st();
-                tc_fence_before();
+                if (split == 4)
+                    softmax_tile(std::integral_constant<int, 16>{}, j);
+                else if (split == 2)
+                    softmax_tile(std::integral_constant<int, 32>{}, j);
+                else
+                    softmax_tile(std::integral_constant<int, 64>{}, j);
+                if (!ok) break;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(pfull(pipe));
@@ -806,13 +840,26 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             if (!ok && lane == 0) attn_error(kErrWaitMma, abort_flag);
             tc_fence_after();
         }
+        if (busy) {  // the row's sum: both threads'
+            asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");  // the last exchange above has been read
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine), "f"(l) : "memory");
+            asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+            float other;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(theirs) : "memory");
+            l += other;
+        }
         constexpr float kUnscale = 1.0f / kPScale;
-        float* stage = reinterpret_cast<float*>(smem + L::kQOff);  // [128][DP], 16-byte chunks swizzled by the row
-        float2* ml = reinterpret_cast<float2*>(smem + L::kMlOff);
-        auto stage_at = [&](int row, int chunk) { return stage + row * DP + ((chunk ^ (row & 7)) << 2); };
+        constexpr int kHalf = DP / 2;          // output columns a thread
+        const int cout = half * kHalf;
+        const uint32_t ml = sbase + L::kMlOff, joined = sbase + L::kJoinedOff;
+        // fp32 partials [128][DP] where Q was, 16-byte chunks swizzled by the row
+        auto stage_at = [&](int row, int chunk) { return sbase + L::kQOff + static_cast<uint32_t>(row * DP + ((chunk ^ (row & 7)) << 2)) * 4u; };
+        auto out_at = [&](int row) {
+            const int t = row / p.group, g = row - t * p.group;
+            return p.out + (w.token0 + t) * p.out_stride + static_cast<int64_t>(w.head * p.group + g) * p.head_dim;
+        };
         auto write_row = [&](int b, const uint32_t* o, float inv) {  // 32 values from column b of this thread's row
-            const int t = R / p.group, g = R - t * p.group;
-            uint16_t* dst = p.out + (w.token0 + t) * p.out_stride + static_cast<int64_t>(w.head * p.group + g) * p.head_dim;
+            uint16_t* dst = out_at(R);
 #pragma unroll
             for (int i = 0; i < 32; i += 8) {
                 if (b + i >= p.head_dim) break;
@@ -827,7 +874,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             if (ok && busy) {
                 const float inv = l > 0.0f ? kUnscale / l : 0.0f;
 #pragma unroll
-                for (int b = 0; b < DP; b += 32) {
+                for (int b = 0; b < kHalf; b += 32) {
                     uint32_t o[32];
                     if (done > 0) {
                         tmem_ld_x32(t_o + b, o);
@@ -836,12 +883,12 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = 0u;
                     }
-                    if (valid) write_row(b, o, inv);
+                    if (valid) write_row(cout + b, o, inv);
                 }
             }
         } else if (have) {
-            // Partial results through shared memory: the pipes' of this CTA, then
-            // the cluster's.  Rounds: one, or one for each row tile.
+            // Partial results meet in shared memory: the pipes', the copies' and
+            // then the cluster's.  Rounds: one, or one for each row tile.
             const int rounds = w.two ? 2 : 1;
             softmax_bar();  // both pipes' products are complete: Q's place is free
             for (int round = 0; round < rounds; ++round) {
@@ -851,57 +898,96 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                     ok = __all_sync(0xffffffffu, ok);
                 }
                 if (w.two ? pipe == round : pipe == 1) {
-                    if (valid) ml[r] = make_float2(m, done > 0 ? l : 0.0f);
+                    if (valid && half == 0) sts_f2(ml + r * 8, m, done > 0 ? l : 0.0f);
                     if (ok && busy && done > 0) {
 #pragma unroll
-                        for (int b = 0; b < DP; b += 32) {
+                        for (int b = 0; b < kHalf; b += 32) {
                             uint32_t o[32];
                             tmem_ld_x32(t_o + b, o);
                             tmem_wait_ld_x32(o);
                             if (valid)
 #pragma unroll
-                                for (int i = 0; i < 32; i += 4)
-                                    *reinterpret_cast<uint4*>(stage_at(r, (b + i) / 4)) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                                for (int i = 0; i < 32; i += 4) sts128(stage_at(r, (cout + b + i) / 4), o[i], o[i + 1], o[i + 2], o[i + 3]);
                         }
                     }
                 }
                 softmax_bar();
-                if (!w.two && pipe == 0 && ok && busy) {
-                    // add pipe 1's partial to this one's
-                    float2 other = valid ? ml[r] : make_float2(0.0f, 0.0f);
-                    const float mine_l = done > 0 ? l : 0.0f;
-                    const float top = fmaxf(mine_l > 0.0f ? m : other.x, other.y > 0.0f ? other.x : m);
-                    const float a0 = mine_l > 0.0f ? ex2((m - top) * c) : 0.0f;
-                    const float a1 = other.y > 0.0f ? ex2((other.x - top) * c) : 0.0f;
-                    const float sum = a0 * mine_l + a1 * other.y;
-                    const float inv = sum > 0.0f ? kUnscale / sum : 0.0f;
+                if (!w.two) {
+                    const bool direct = split == 1 && p.cl == 1;
+                    if (pipe == 0 && ok && busy) {
+                        // add pipe 1's partial to this one's
+                        const float2 other = valid ? lds_f2(ml + r * 8) : make_float2(0.0f, 0.0f);
+                        const float mine_l = done > 0 ? l : 0.0f;
+                        const float top = fmaxf(mine_l > 0.0f ? m : other.x, other.y > 0.0f ? other.x : m);
+                        const float a0 = mine_l > 0.0f ? ex2(m - top) : 0.0f;
+                        const float a1 = other.y > 0.0f ? ex2(other.x - top) : 0.0f;
+                        const float sum = a0 * mine_l + a1 * other.y;
+                        const float inv = sum > 0.0f ? kUnscale / sum : 0.0f;
+                        // both threads of the row have read its (m, l)
+                        asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
 #pragma unroll
-                    for (int b = 0; b < DP; b += 32) {
-                        uint32_t o[32];
-                        if (done > 0) {
-                            tmem_ld_x32(t_o + b, o);
-                            tmem_wait_ld_x32(o);
-                        }
+                        for (int b = 0; b < kHalf; b += 32) {
+                            uint32_t o[32];
+                            if (done > 0) {
+                                tmem_ld_x32(t_o + b, o);
+                                tmem_wait_ld_x32(o);
+                            }
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            if (valid && a1 > 0.0f) v = *reinterpret_cast<const float4*>(stage_at(r, (b + i) / 4));
-                            const float x[4] = {v.x * a1, v.y * a1, v.z * a1, v.w * a1};
+                            for (int i = 0; i < 32; i += 4) {
+                                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                                if (valid && a1 > 0.0f) v = lds128(stage_at(r, (cout + b + i) / 4));
+                                const float x[4] = {__uint_as_float(v.x) * a1, __uint_as_float(v.y) * a1, __uint_as_float(v.z) * a1,
+                                                    __uint_as_float(v.w) * a1};
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                o[i + e] = __float_as_uint(a0 > 0.0f ? fmaf(__uint_as_float(o[i + e]), a0, x[e]) : x[e]);
-                        }
-                        if (valid) {
-                            if (p.cl == 1) {
-                                write_row(b, o, inv);
-                            } else {
+                                for (int e = 0; e < 4; ++e)
+                                    o[i + e] = __float_as_uint(a0 > 0.0f ? fmaf(__uint_as_float(o[i + e]), a0, x[e]) : x[e]);
+                            }
+                            if (valid && direct) {
+                                write_row(cout + b, o, inv);
+                            } else if (valid) {
 #pragma unroll
-                                for (int i = 0; i < 32; i += 4)
-                                    *reinterpret_cast<uint4*>(stage_at(r, (b + i) / 4)) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                                for (int i = 0; i < 32; i += 4) sts128(stage_at(r, (cout + b + i) / 4), o[i], o[i + 1], o[i + 2], o[i + 3]);
                             }
                         }
+                        if (valid && half == 0) sts_f2(ml + r * 8, top, sum);
                     }
-                    if (valid && p.cl > 1) ml[r] = make_float2(top, sum);
+                    if (direct) break;
+                    softmax_bar();
+                }
+                // the copies of a row into the first of them (its (m, l) apart: other
+                // threads of the row still read the copies')
+                const int units = rows * (DP / 4);
+                for (int u = tid; u < units; u += kSoftmaxThreads) {
+                    const int row = u / (DP / 4), ch = u - row * (DP / 4);
+                    float2 q[4];
+                    float top = kNegInf, sum = 0.0f;
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) {
+                        q[f] = f < split ? lds_f2(ml + (f * per_copy + row) * 8) : make_float2(kNegInf, 0.0f);
+                        if (q[f].y > 0.0f) top = fmaxf(top, q[f].x);
+                    }
+                    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) {
+                        if (!(q[f].y > 0.0f)) continue;
+                        const uint4 v = lds128(stage_at(f * per_copy + row, ch));
+                        const float a = ex2(q[f].x - top);
+                        sum = fmaf(q[f].y, a, sum);
+                        acc[0] = fmaf(__uint_as_float(v.x), a, acc[0]);
+                        acc[1] = fmaf(__uint_as_float(v.y), a, acc[1]);
+                        acc[2] = fmaf(__uint_as_float(v.z), a, acc[2]);
+                        acc[3] = fmaf(__uint_as_float(v.w), a, acc[3]);
+                    }
+                    if (p.cl == 1) {
+                        const float inv = sum > 0.0f ? kUnscale / sum : 0.0f;
+                        if (ch * 4 < p.head_dim)
+                            *reinterpret_cast<uint2*>(out_at(w.row0 + row) + ch * 4) =
+                                make_uint2(pack16<kBf16>(acc[0] * inv, acc[1] * inv), pack16<kBf16>(acc[2] * inv, acc[3] * inv));
+                    } else {
+                        sts128(stage_at(row, ch), __float_as_uint(acc[0]), __float_as_uint(acc[1]), __float_as_uint(acc[2]),
+                               __float_as_uint(acc[3]));
+                        if (ch == 0) sts_f2(joined + row * 8, top, sum);
+                    }
                 }
                 if (p.cl == 1) break;
                 softmax_bar();
@@ -911,35 +997,60 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                 all = __all_sync(0xffffffffu, all);
                 if (!all && lane == 0) attn_error(kErrWaitDequant, abort_flag);
                 if (all) {
-                    // each rank finishes its share of the rows' 16-byte chunks
-                    const int units = rows * (DP / 4);
-                    for (int u = rank * 256 + tid; u < units; u += p.cl * 256) {
-                        const int row = u / (DP / 4), ch = u - row * (DP / 4);
-                        const uint32_t ml_at = sbase + L::kMlOff + row * 8;
-                        const uint32_t st_at = smem_u32(stage_at(row, ch));
-                        float top = __int_as_float(0xff800000), sum = 0.0f;
+                    // each rank finishes its share of the rows' 16-byte chunks; with
+                    // few of them several lanes share one, each reading some ranks'
+                    // partials (one remote read's time instead of a rank count's)
+                    const int share = (units + p.cl - 1) / p.cl;
+                    int lanes = p.cl;
+                    while (lanes > 1 && share * lanes > kSoftmaxThreads) lanes >>= 1;
+                    const int k0 = tid & (lanes - 1);
+                    for (int b = 0; b < share; b += kSoftmaxThreads / lanes) {
+                        const int i = b + tid / lanes, u = rank * share + i;
+                        const bool live = i < share && u < units;
+                        const int row = live ? u / (DP / 4) : 0, ch = live ? u - row * (DP / 4) : 0;
+                        const uint32_t ml_at = joined + row * 8, st_at = stage_at(row, ch);
+                        float top = kNegInf, sum = 0.0f;
                         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        for (int k = 0; k < p.cl; ++k) {
-                            const float2 q = ld_cluster_f2(mapa_shared(ml_at, static_cast<uint32_t>(k)));
-                            if (!(q.y > 0.0f)) continue;
-                            const float4 v = ld_cluster_f4(mapa_shared(st_at, static_cast<uint32_t>(k)));
-                            const float to = fmaxf(top, q.x);
-                            const float a = ex2((top - to) * c), b = ex2((q.x - to) * c);
+                        for (int k = k0; k < p.cl; k += 4 * lanes) {
+                            float2 q[4];
+                            float4 v[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t from_rank = static_cast<uint32_t>(k + e * lanes < p.cl ? k + e * lanes : k);
+                                q[e] = ld_cluster_f2(mapa_shared(ml_at, from_rank));
+                                v[e] = ld_cluster_f4(mapa_shared(st_at, from_rank));
+                                if (k + e * lanes >= p.cl) q[e].y = 0.0f;
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                if (!(q[e].y > 0.0f)) continue;
+                                const float to = fmaxf(top, q[e].x);
+                                const float x = ex2(top - to), y = ex2(q[e].x - to);
+                                top = to;
+                                sum = sum * x + q[e].y * y;
+                                acc.x = acc.x * x + v[e].x * y;
+                                acc.y = acc.y * x + v[e].y * y;
+                                acc.z = acc.z * x + v[e].z * y;
+                                acc.w = acc.w * x + v[e].w * y;
+                            }
+                        }
+                        for (int d = lanes >> 1; d > 0; d >>= 1) {
+                            const float o_top = __shfl_xor_sync(0xffffffffu, top, d), o_sum = __shfl_xor_sync(0xffffffffu, sum, d);
+                            const float4 o = make_float4(__shfl_xor_sync(0xffffffffu, acc.x, d), __shfl_xor_sync(0xffffffffu, acc.y, d),
+                                                         __shfl_xor_sync(0xffffffffu, acc.z, d), __shfl_xor_sync(0xffffffffu, acc.w, d));
+                            const float to = fmaxf(top, o_top);
+                            const float x = sum > 0.0f ? ex2(top - to) : 0.0f, y = o_sum > 0.0f ? ex2(o_top - to) : 0.0f;
                             top = to;
-                            sum = sum * a + q.y * b;
-                            acc.x = acc.x * a + v.x * b;
-                            acc.y = acc.y * a + v.y * b;
-                            acc.z = acc.z * a + v.z * b;
-                            acc.w = acc.w * a + v.w * b;
+                            sum = sum * x + o_sum * y;
+                            acc.x = acc.x * x + o.x * y;
+                            acc.y = acc.y * x + o.y * y;
+                            acc.z = acc.z * x + o.z * y;
+                            acc.w = acc.w * x + o.w * y;
                         }
                         const float inv = sum > 0.0f ? kUnscale / sum : 0.0f;
-                        if (ch * 4 < p.head_dim) {
-                            const int RR = w.row0 + round * kRows + row, t = RR / p.group, g = RR - t * p.group;
-                            uint16_t* dst = p.out + (w.token0 + t) * p.out_stride +
-                                            static_cast<int64_t>(w.head * p.group + g) * p.head_dim + ch * 4;
-                            *reinterpret_cast<uint2*>(dst) =
+                        if (live && k0 == 0 && ch * 4 < p.head_dim)
+                            *reinterpret_cast<uint2*>(out_at(w.row0 + round * kRows + row) + ch * 4) =
                                 make_uint2(pack16<kBf16>(acc.x * inv, acc.y * inv), pack16<kBf16>(acc.z * inv, acc.w * inv));
-                        }
                     }
                 }
                 softmax_bar();
@@ -996,44 +1107,14 @@ cudaError_t launch_attn(const AttentionArgs& a, cudaStream_t st) {
                           static_cast<uint64_t>(c.page_stride) * es, kFp8 ? DP : 64, box, kFp8 && DP == 64))
             return cudaErrorInvalidValue;
 
-    // 256-row tiles of all sequences, at most
-    const int64_t most_new = a.max_new > 0 && a.starts ? a.max_new : a.starts ? a.tokens : 1;
-    int64_t tiles = a.seqs * ((most_new * group + 2 * kRows - 1) / (2 * kRows));
-    if (a.starts) {
-        const int64_t by_tokens = a.tokens * group / (2 * kRows) + a.seqs;
-        tiles = tiles < by_tokens ? tiles : by_tokens;
-    }
-    const int64_t items = tiles * c.kv_heads;
+    const int64_t tiles = attention_row_tiles(a, group, 2 * kRows), items = tiles * c.kv_heads;
     // CTAs a cluster: as many as fill the GPU, while each has two key tiles at least
-    int64_t longest = a.table_width * c.page_size;
-    if (a.max_len > 0 && a.max_len < longest) longest = a.max_len;
-    if (a.window > 0 && a.window + most_new < longest) longest = a.window + most_new;
-    const int64_t key_tiles = (longest + kKeys - 1) / kKeys;
+    const int64_t key_tiles = (attention_longest(a) + kKeys - 1) / kKeys;
     int cl = 1;
     while (cl < kMaxAttnCluster && items * cl * 2 <= sms && key_tiles >= cl * 4) cl *= 2;
     if (items * cl > 0x7fffffffll) return cudaErrorInvalidConfiguration;
 
-    AttnParams p = {};
-    p.q = static_cast<const uint16_t*>(a.q);
-    p.out = static_cast<uint16_t*>(a.out);
-    p.q_stride = a.q_stride;
-    p.out_stride = a.out_stride;
-    p.tokens = a.tokens;
-    p.table = a.block_table;
-    p.lens = a.lens;
-    p.starts = a.starts;
-    p.table_width = a.table_width;
-    p.k_scales = c.k_scales;
-    p.v_scales = c.v_scales;
-    p.num_pages = c.num_pages;
-    p.seqs = static_cast<int>(a.seqs);
-    p.kv_heads = c.kv_heads;
-    p.group = group;
-    p.head_dim = c.head_dim;
-    p.page_size = c.page_size;
-    while ((1 << p.log_page) < c.page_size) ++p.log_page;
-    p.c = a.scale * kLog2e;
-    p.window = a.window;
+    AttnParams p = attention_params(a);
     p.row_tiles = static_cast<int>(tiles);
     p.cl = cl;
 
@@ -1065,6 +1146,8 @@ cudaError_t launch_dim(const AttentionArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t st) {
+    const int64_t most_new = a.starts ? (a.max_new > 0 ? a.max_new : a.tokens) : 1;
+    if (most_new * (a.q_heads / a.cache->kv_heads) <= kFewRows) return launch_attention_few(a, st);
     return a.cache->head_dim <= 64 ? launch_dim<64>(a, st) : launch_dim<128>(a, st);
 }
 
@@ -1072,7 +1155,8 @@ int read_attention_device_error() {
     int v = 0, zero = 0;
     if (cudaMemcpyFromSymbol(&v, g_attention_error, sizeof v) != cudaSuccess) return -1;
     if (v != 0 && cudaMemcpyToSymbol(g_attention_error, &zero, sizeof zero) != cudaSuccess) return -1;
-    return v;
+    const int few = read_attention_few_device_error();
+    return v ? v : few;
 }
 
 }  // namespace fp8w

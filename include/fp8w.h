@@ -395,7 +395,7 @@ typedef struct fp8w_rope_spec {
  *              NULL for the other types), scale = amax / 448 (1.0 if that is
  *              0), as fp8w_quantize gives a row.
  *   head_dim   a multiple of 16, 16..128.
- *   page_size  8, 16, 32, 64, 128 or 256.
+ *   page_size  16, 32, 64, 128 or 256.
  * Pointers are 16-byte aligned (scales 4) and strides multiples of 16 bytes.
  * The struct itself is read during the call only.
  */

@@ -61,7 +61,7 @@ CACHES = [
     (dict(k=None), 1), (dict(v=None), 1), (dict(dtype=4), 1), (dict(dtype=4, ks=0x700000), 1),
     (dict(dtype=2), 4), (dict(dtype=3), 4), (dict(dtype=0), 4),
     (dict(pages=0), 2), (dict(pages=2 ** 31), 2), (dict(kv_heads=0), 2), (dict(dim=72), 2), (dict(dim=144), 2), (dict(dim=0), 2),
-    (dict(page=0), 2), (dict(page=4), 2), (dict(page=24), 2), (dict(page=512), 2),
+    (dict(page=0), 2), (dict(page=8), 2), (dict(page=24), 2), (dict(page=512), 2),
     (dict(token_stride=48), 7), (dict(head_stride=0), 7), (dict(page_stride=-2048), 7), (dict(page_stride=2 ** 40), 7),
     (dict(ks=0x700000), 7),
     (dict(token_stride=68), 3), (dict(head_stride=1028), 3), (dict(page_stride=2049), 3), (dict(k=0x500008), 3), (dict(v=0x600004), 3),

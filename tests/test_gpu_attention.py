@@ -67,7 +67,7 @@ def test_head_sizes_between_the_tile_widths(dim, codes):
     run([1, 1, 1], [300, 5, 128], 2, 4, dim, 16, "bf16", codes)
 
 
-@pytest.mark.parametrize("page", [8, 16, 32, 64, 128, 256])
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
 @pytest.mark.parametrize("codes", [False, True])
 @pytest.mark.parametrize("layout", ["heads", "tokens"])
 def test_page_sizes_and_memory_orders(page, codes, layout):
@@ -99,6 +99,12 @@ def test_the_length_hint_changes_no_result_beyond_rounding(max_len):
 @pytest.mark.parametrize("new,length", [(2, 2), (31, 31), (32, 300), (33, 33), (64, 64), (65, 1000), (257, 300), (700, 700)])
 def test_chunks(new, length, dtype, codes):
     run([new], [length], 1, 4, 128, 16, dtype, codes)
+
+
+@pytest.mark.parametrize("dtype,codes", [("bf16", False), ("f16", True)])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_long_chunks(dim, dtype, codes):
+    run([513, 300], [7000, 5001], 2, 4, dim, 32, dtype, codes)
 
 
 @pytest.mark.parametrize("group", [1, 3, 5, 8])

@@ -110,7 +110,7 @@ def make_cache(pages, kv, page, dim, dtype, codes, layout):
 @pytest.mark.parametrize("dtype,codes", [("bf16", False), ("f16", False), ("bf16", True), ("f16", True)])
 @pytest.mark.parametrize("layout", ["heads", "tokens"])
 @pytest.mark.parametrize("tokens,q_heads,kv,dim,rot,sections,interleaved,page", [
-    (1, 32, 8, 128, 128, [64], False, 16), (5, 3, 1, 16, 16, [8], True, 8), (130, 6, 3, 80, 48, [10, 14], False, 32),
+    (1, 32, 8, 128, 128, [64], False, 16), (5, 3, 1, 16, 16, [8], True, 16), (130, 6, 3, 80, 48, [10, 14], False, 32),
     (700, 8, 2, 96, 96, [16, 16, 16], True, 256), (67, 5, 5, 64, 0, None, False, 64)])
 def test_rope_append(tokens, q_heads, kv, dim, rot, sections, interleaved, page, layout, dtype, codes):
     fused = rows(11, tokens, q_heads + 2 * kv, dim, dtype)
