@@ -322,7 +322,7 @@ fp8w_status fp8w_paged_attention(const void* q, int act_dtype, int64_t tokens, i
         return FP8W_ERR_SHAPE;
     fp8w_status st = check_cache(cache, act_dtype);
     if (st != FP8W_OK) return st;
-    if (q_heads % cache->kv_heads != 0 || tokens * (q_heads / cache->kv_heads) > kMost ||
+    if (q_heads % cache->kv_heads != 0 || q_heads / cache->kv_heads > 4096 || tokens * (q_heads / cache->kv_heads) > kMost ||
         table_width > kMost / cache->page_size || (!starts && tokens != seqs))
         return FP8W_ERR_SHAPE;
     if (!(scale > 0.0f) || !(scale <= 3.0e38f) || window < 0 || max_new < 0 || max_len < 0) return FP8W_ERR_VALUE;

@@ -48,8 +48,11 @@ constexpr int kKeys = 128;            // keys a tile
 constexpr int kRows = 128;            // rows a tile (TMEM lanes)
 constexpr int kMaxAttnCluster = 16;
 // Up to this many rows a key head (new tokens x its query heads) the kernel for
-// few rows reads the cache faster.
-constexpr int kFewRows = 32;
+// few rows reads the cache faster.  It takes 16 rows at a time: with 24 a 16-bit
+// cache is read twice (a decode batch of 1.2 GB: 374 us against 323 here; 16
+// rows: 243), a cache of codes twice is still less than here (384 against 278;
+// with 48, 434 against 390).
+constexpr int kFewRows = 16, kFewRowsCodes = 48;
 constexpr uint32_t kAttnTmemCols = 512;
 constexpr int kSoftmaxThreads = 512;   // sixteen warps
 constexpr int kLoadWarp = 16, kMmaWarp = 17, kConvWarp = 20;
@@ -111,38 +114,21 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-// 32 consecutive columns of the thread's lane, without the wait.
-__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t* r) {
+// 32 consecutive columns of the thread's lane, with the wait in the same
+// statement: registers named by a load that is still in flight may be copied
+// by the compiler before a wait that stands apart.
+__device__ __forceinline__ void tmem_ld_x32_sync(uint32_t taddr, uint32_t* r) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+          "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+          "=r"(r[30]), "=r"(r[31])
         : "r"(taddr)
         : "memory");
 }
-// The wait, tied to the registers it makes valid.
-__device__ __forceinline__ void tmem_wait_ld_x32(uint32_t* r) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
-                   "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                   "+r"(r[30]), "+r"(r[31])::"memory");
-}
-__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t* r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
-
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
@@ -188,6 +174,76 @@ __device__ __forceinline__ uint64_t smem_desc_sw128_nmajor(uint32_t addr) {
 }
 constexpr uint32_t kIdescBNMajor = 1u << 16;
 
+// Eight or fewer products in a row, issued by one elected lane.  One election,
+// and descriptors that advance by an add: sixteen products a key tile have to
+// be issued beside eight busy softmax warps, and with a descriptor built for
+// each the tensor cores waited for them.
+// D[tmem] = (or +=) sum over k of A[smem] B[smem], a 16-value step of a 64-value
+// sub-tile being 32 bytes and a sub-tile 128 rows of 128 bytes.
+template <int kSteps>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+    const uint64_t da = smem_desc_sw128_kmajor(a), db = smem_desc_sw128_kmajor(b);
+    const uint32_t a_lo = static_cast<uint32_t>(da), b_lo = static_cast<uint32_t>(db), hi = static_cast<uint32_t>(da >> 32);
+    static_assert(kSteps == 4 || kSteps == 8, "64 or 128 values");
+    asm volatile(
+        "{\n\t.reg .pred e, f, t;\n\t.reg .b64 x, y;\n\t.reg .b32 u, v;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 f, 0, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, f;\n\t"
+        "add.u32 u, %1, 2;\n\tadd.u32 v, %2, 2;\n\tmov.b64 x, {u, %3};\n\tmov.b64 y, {v, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t"
+        "add.u32 u, %1, 4;\n\tadd.u32 v, %2, 4;\n\tmov.b64 x, {u, %3};\n\tmov.b64 y, {v, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t"
+        "add.u32 u, %1, 6;\n\tadd.u32 v, %2, 6;\n\tmov.b64 x, {u, %3};\n\tmov.b64 y, {v, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc)
+        : "memory");
+    if constexpr (kSteps == 8)
+        asm volatile(
+            "{\n\t.reg .pred e, t;\n\t.reg .b64 x, y;\n\t.reg .b32 u, v;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\t"
+            "setp.eq.b32 t, 0, 0;\n\t"
+            "add.u32 u, %1, 1024;\n\tadd.u32 v, %2, 1024;\n\tmov.b64 x, {u, %3};\n\tmov.b64 y, {v, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t"
+            "add.u32 u, %1, 1026;\n\tadd.u32 v, %2, 1026;\n\tmov.b64 x, {u, %3};\n\tmov.b64 y, {v, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t"
+            "add.u32 u, %1, 1028;\n\tadd.u32 v, %2, 1028;\n\tmov.b64 x, {u, %3};\n\tmov.b64 y, {v, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t"
+            "add.u32 u, %1, 1030;\n\tadd.u32 v, %2, 1030;\n\tmov.b64 x, {u, %3};\n\tmov.b64 y, {v, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t}" ::"r"(d),
+            "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc)
+            : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem] over 128 keys: 8 columns of A and 16 key rows
+// (2048 bytes) a step.
+__device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+    const uint64_t db = smem_desc_sw128_nmajor(b);
+    const uint32_t b_lo = static_cast<uint32_t>(db), hi = static_cast<uint32_t>(db >> 32);
+    asm volatile(
+        "{\n\t.reg .pred e, p, t;\n\t.reg .b64 y;\n\t.reg .b32 u, v;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "mov.b64 y, {%2, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t"
+        "add.u32 u, %1, 8;\n\tadd.u32 v, %2, 128;\n\tmov.b64 y, {v, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t"
+        "add.u32 u, %1, 16;\n\tadd.u32 v, %2, 256;\n\tmov.b64 y, {v, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t"
+        "add.u32 u, %1, 24;\n\tadd.u32 v, %2, 384;\n\tmov.b64 y, {v, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t"
+        "add.u32 u, %1, 32;\n\tadd.u32 v, %2, 512;\n\tmov.b64 y, {v, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t"
+        "add.u32 u, %1, 40;\n\tadd.u32 v, %2, 640;\n\tmov.b64 y, {v, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t"
+        "add.u32 u, %1, 48;\n\tadd.u32 v, %2, 768;\n\tmov.b64 y, {v, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t"
+        "add.u32 u, %1, 56;\n\tadd.u32 v, %2, 896;\n\tmov.b64 y, {v, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t}" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar, uint32_t rank) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(bar, rank)) : "memory");
 }
@@ -222,6 +278,8 @@ __device__ __forceinline__ float2 lds_f2(uint32_t addr) {
 __device__ __forceinline__ void sts_f2(uint32_t addr, float x, float y) {
     asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
 }
+// x / group, for x < 2^15 + group (x * group < 2^32: the rounded-up reciprocal is exact).
+__device__ __forceinline__ int by_group(const AttnParams& p, int x) { return static_cast<int>(__umulhi(static_cast<uint32_t>(x), p.group_inverse)) + (p.group == 1 ? x : 0); }
 __device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync %0, %1;" ::"n"(kBarSoftmax), "n"(kSoftmaxThreads) : "memory"); }
 
 // What a CTA works on: rows [row0, row0 + rows) of sequence seq (rows counted
@@ -265,6 +323,229 @@ __device__ __forceinline__ bool find_work(const AttnParams& p, int tile, int hea
     return true;
 }
 
+// What a softmax thread takes to the join.
+struct Join {
+    uint32_t sbase, t_o, joinfull, joinfree;
+    int rank, split, done;
+    bool ok, valid;
+    float m, l;
+};
+
+template <int DP, bool kFp8, bool kBf16>
+struct Weights {
+    // fp16 weights with e4m3 scales: p * v_scale * 2^4 keeps the products of
+    // small scales among fp16's normal numbers, and with p below 2^4 it cannot
+    // overflow (scales reach 65504 / 448 = 146.2 for fp16 values).  No slack and
+    // 2^8 would reach smaller scales, but rescales O at most of the first tiles.
+    static constexpr bool kScaledF16 = kFp8 && !kBf16;
+    static constexpr float kSlack = kScaledF16 ? 4.0f : 8.0f;
+    static constexpr float kScale = kScaledF16 ? 16.0f : 1.0f;
+};
+
+// Partial results through shared memory to the output: the pipes', the copies'
+// and then the cluster's.  Rounds: one, or one for each row tile.  A function of
+// its own: inlined, it took registers from the loop before it.  All softmax
+// threads call it.
+template <int DP, bool kBf16, bool kFp8>
+__device__ __noinline__ void join_results(const AttnParams& p, const Work& w, const Join& a, volatile int* abort_flag) {
+    using L = AttnSmem<DP, kFp8>;
+    constexpr float kUnscale = 1.0f / Weights<DP, kFp8, kBf16>::kScale;
+    const uint32_t sbase = a.sbase, t_o = a.t_o, joinfull = a.joinfull, joinfree = a.joinfree;
+    const int rank = a.rank, tid = threadIdx.x, split = a.split, done = a.done, per_copy = kRows / split;
+    constexpr int kHalf = DP / 2;          // output columns a thread
+    const int lane = tid & 31, pipe = tid >> 8, half = (tid >> 7) & 1, r = tid & 127, cout = half * kHalf;
+    const uint32_t pair = 2 + pipe * 4 + ((tid >> 5) & 3);
+    const bool valid = a.valid;
+    const float m = a.m, l = a.l;
+    bool ok = a.ok;
+    const bool busy = __any_sync(0xffffffffu, valid);
+    const uint32_t ml = sbase + L::kMlOff, joined = sbase + L::kJoinedOff;
+    // fp32 partials [128][DP] where Q was, 16-byte chunks swizzled by the row
+    auto stage_at = [&](int row, int chunk) { return sbase + L::kQOff + static_cast<uint32_t>(row * DP + ((chunk ^ (row & 7)) << 2)) * 4u; };
+    uint16_t* out = p.out + w.token0 * p.out_stride + static_cast<int64_t>(w.head * p.group) * p.head_dim;
+    auto out_at = [&](int row) {
+        const int t = row / p.group, g = row - t * p.group;
+        return out + t * p.out_stride + g * p.head_dim;
+    };
+    const int rounds = w.two ? 2 : 1;
+    softmax_bar();  // both pipes' products are complete: Q's place is free
+    for (int round = 0; round < rounds; ++round) {
+        const int rows = w.two ? (round == 0 ? kRows : w.rows - kRows) : w.rows;
+        if (round > 0) {
+            ok = ok && mbar_wait_cluster(joinfree, static_cast<uint32_t>((round - 1) & 1), abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+        }
+        if (w.two ? pipe == round : pipe == 1) {
+            if (valid && half == 0) sts_f2(ml + r * 8, m, done > 0 ? l : 0.0f);
+            if (ok && busy && done > 0) {
+#pragma unroll
+                for (int b = 0; b < kHalf; b += 32) {
+                    uint32_t o[32];
+                    tmem_ld_x32_sync(t_o + b, o);
+                    if (valid)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) sts128(stage_at(r, (cout + b + i) / 4), o[i], o[i + 1], o[i + 2], o[i + 3]);
+                }
+            }
+        }
+        softmax_bar();
+        if (!w.two) {
+            const bool direct = split == 1 && p.cl == 1;
+            if (pipe == 0 && ok && busy) {
+                // add pipe 1's partial to this one's
+                const float2 other = valid ? lds_f2(ml + r * 8) : make_float2(0.0f, 0.0f);
+                const float mine_l = done > 0 ? l : 0.0f;
+                const float top = fmaxf(mine_l > 0.0f ? m : other.x, other.y > 0.0f ? other.x : m);
+                const float a0 = mine_l > 0.0f ? ex2(m - top) : 0.0f;
+                const float a1 = other.y > 0.0f ? ex2(other.x - top) : 0.0f;
+                const float sum = a0 * mine_l + a1 * other.y;
+                const float inv = sum > 0.0f ? kUnscale / sum : 0.0f;
+                // both threads of the row have read its (m, l)
+                asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+#pragma unroll
+                for (int b = 0; b < kHalf; b += 32) {
+                    uint32_t o[32];
+                    if (done > 0) {
+                        tmem_ld_x32_sync(t_o + b, o);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                        if (valid && a1 > 0.0f) v = lds128(stage_at(r, (cout + b + i) / 4));
+                        const float x[4] = {__uint_as_float(v.x) * a1, __uint_as_float(v.y) * a1, __uint_as_float(v.z) * a1,
+                                            __uint_as_float(v.w) * a1};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[i + e] = __float_as_uint(a0 > 0.0f ? fmaf(__uint_as_float(o[i + e]), a0, x[e]) : x[e]);
+                    }
+                    if (valid && direct) {
+                        {
+                    uint16_t* dst = out_at(w.row0 + r);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        if (cout + b + i >= p.head_dim) break;
+                        uint32_t v[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            v[e] = pack16<kBf16>(__uint_as_float(o[i + 2 * e]) * inv, __uint_as_float(o[i + 2 * e + 1]) * inv);
+                        *reinterpret_cast<uint4*>(dst + cout + b + i) = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                }
+                    } else if (valid) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) sts128(stage_at(r, (cout + b + i) / 4), o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    }
+                }
+                if (valid && half == 0) sts_f2(ml + r * 8, top, sum);
+            }
+            if (direct) break;
+            softmax_bar();
+        }
+        // the copies of a row into the first of them (its (m, l) apart: other
+        // threads of the row still read the copies')
+        const int units = rows * (DP / 4);
+        for (int u = tid; u < units; u += kSoftmaxThreads) {
+            const int row = u / (DP / 4), ch = u - row * (DP / 4);
+            float2 q[4];
+            float top = kNegInf, sum = 0.0f;
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                q[f] = f < split ? lds_f2(ml + (f * per_copy + row) * 8) : make_float2(kNegInf, 0.0f);
+                if (q[f].y > 0.0f) top = fmaxf(top, q[f].x);
+            }
+            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                if (!(q[f].y > 0.0f)) continue;
+                const uint4 v = lds128(stage_at(f * per_copy + row, ch));
+                const float a = ex2(q[f].x - top);
+                sum = fmaf(q[f].y, a, sum);
+                acc[0] = fmaf(__uint_as_float(v.x), a, acc[0]);
+                acc[1] = fmaf(__uint_as_float(v.y), a, acc[1]);
+                acc[2] = fmaf(__uint_as_float(v.z), a, acc[2]);
+                acc[3] = fmaf(__uint_as_float(v.w), a, acc[3]);
+            }
+            if (p.cl == 1) {
+                const float inv = sum > 0.0f ? kUnscale / sum : 0.0f;
+                if (ch * 4 < p.head_dim)
+                    *reinterpret_cast<uint2*>(out_at(w.row0 + row) + ch * 4) =
+                        make_uint2(pack16<kBf16>(acc[0] * inv, acc[1] * inv), pack16<kBf16>(acc[2] * inv, acc[3] * inv));
+            } else {
+                sts128(stage_at(row, ch), __float_as_uint(acc[0]), __float_as_uint(acc[1]), __float_as_uint(acc[2]),
+                       __float_as_uint(acc[3]));
+                if (ch == 0) sts_f2(joined + row * 8, top, sum);
+            }
+        }
+        if (p.cl == 1) break;
+        softmax_bar();
+        if (tid < p.cl) mbar_arrive_remote(joinfull, static_cast<uint32_t>(tid));
+        __syncwarp();
+        bool all = mbar_wait_cluster(joinfull, static_cast<uint32_t>(round & 1), abort_flag);
+        all = __all_sync(0xffffffffu, all);
+        if (!all && lane == 0) attn_error(kErrWaitDequant, abort_flag);
+        if (all) {
+            // each rank finishes its share of the rows' 16-byte chunks; with
+            // few of them several lanes share one, each reading some ranks'
+            // partials (one remote read's time instead of a rank count's)
+            const int share = (units + p.cl - 1) / p.cl;
+            int lanes = p.cl;
+            while (lanes > 1 && share * lanes > kSoftmaxThreads) lanes >>= 1;
+            const int k0 = tid & (lanes - 1);
+            for (int b = 0; b < share; b += kSoftmaxThreads / lanes) {
+                const int i = b + tid / lanes, u = rank * share + i;
+                const bool live = i < share && u < units;
+                const int row = live ? u / (DP / 4) : 0, ch = live ? u - row * (DP / 4) : 0;
+                const uint32_t ml_at = joined + row * 8, st_at = stage_at(row, ch);
+                float top = kNegInf, sum = 0.0f;
+                float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int k = k0; k < p.cl; k += 4 * lanes) {
+                    float2 q[4];
+                    float4 v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t from_rank = static_cast<uint32_t>(k + e * lanes < p.cl ? k + e * lanes : k);
+                        q[e] = ld_cluster_f2(mapa_shared(ml_at, from_rank));
+                        v[e] = ld_cluster_f4(mapa_shared(st_at, from_rank));
+                        if (k + e * lanes >= p.cl) q[e].y = 0.0f;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (!(q[e].y > 0.0f)) continue;
+                        const float to = fmaxf(top, q[e].x);
+                        const float x = ex2(top - to), y = ex2(q[e].x - to);
+                        top = to;
+                        sum = sum * x + q[e].y * y;
+                        acc.x = acc.x * x + v[e].x * y;
+                        acc.y = acc.y * x + v[e].y * y;
+                        acc.z = acc.z * x + v[e].z * y;
+                        acc.w = acc.w * x + v[e].w * y;
+                    }
+                }
+                for (int d = lanes >> 1; d > 0; d >>= 1) {
+                    const float o_top = __shfl_xor_sync(0xffffffffu, top, d), o_sum = __shfl_xor_sync(0xffffffffu, sum, d);
+                    const float4 o = make_float4(__shfl_xor_sync(0xffffffffu, acc.x, d), __shfl_xor_sync(0xffffffffu, acc.y, d),
+                                                 __shfl_xor_sync(0xffffffffu, acc.z, d), __shfl_xor_sync(0xffffffffu, acc.w, d));
+                    const float to = fmaxf(top, o_top);
+                    const float x = sum > 0.0f ? ex2(top - to) : 0.0f, y = o_sum > 0.0f ? ex2(o_top - to) : 0.0f;
+                    top = to;
+                    sum = sum * x + o_sum * y;
+                    acc.x = acc.x * x + o.x * y;
+                    acc.y = acc.y * x + o.y * y;
+                    acc.z = acc.z * x + o.z * y;
+                    acc.w = acc.w * x + o.w * y;
+                }
+                const float inv = sum > 0.0f ? kUnscale / sum : 0.0f;
+                if (live && k0 == 0 && ch * 4 < p.head_dim)
+                    *reinterpret_cast<uint2*>(out_at(w.row0 + round * kRows + row) + ch * 4) =
+                        make_uint2(pack16<kBf16>(acc.x * inv, acc.y * inv), pack16<kBf16>(acc.z * inv, acc.w * inv));
+            }
+        }
+        softmax_bar();
+        if (tid < p.cl) mbar_arrive_remote(joinfree, static_cast<uint32_t>(tid));
+        __syncwarp();
+    }
+}
+
 }  // namespace
 
 template <int DP, bool kBf16, bool kFp8>
@@ -289,13 +570,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // fp16 weights with e4m3 scales: p * v_scale * 2^4 keeps the products of
-    // small scales among fp16's normal numbers, and with p below 2^4 it cannot
-    // overflow (scales reach 65504 / 448 = 146.2 for fp16 values).  No slack and
-    // 2^8 would reach smaller scales, but rescales O at most of the first tiles.
-    constexpr bool kScaledF16 = kFp8 && !kBf16;
-    constexpr float kSlack = kScaledF16 ? 4.0f : 8.0f;
-    constexpr float kPScale = kScaledF16 ? 16.0f : 1.0f;
+    constexpr float kSlack = Weights<DP, kFp8, kBf16>::kSlack, kPScale = Weights<DP, kFp8, kBf16>::kScale;
 
     if (warp == kMmaWarp) {
         tmem_alloc(smem_u32(tmem_slot), kAttnTmemCols);
@@ -425,10 +700,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             auto qk = [&](int pipe, int qtile, int i) {  // S_pipe = Q_qtile K^T
                 const uint32_t a = sbase + L::kQOff + qtile * L::kTileBytes;
                 const uint32_t b = sbase + L::kRingOff + (i % kStages) * L::kTileBytes;
-#pragma unroll
-                for (int kk = 0; kk < DP / 16; ++kk)
-                    mma_f16_ss_warp(tmem + pipe * kKeys, smem_desc_sw128_kmajor(a + (kk >> 2) * (kRows * 128) + (kk & 3) * 32),
-                                    smem_desc_sw128_kmajor(b + (kk >> 2) * (kKeys * 128) + (kk & 3) * 32), idesc_s, kk > 0);
+                mma_scores<DP / 16>(tmem + pipe * kKeys, a, b, idesc_s);
                 tc_commit_warp(sfull(pipe));
                 __syncwarp();
             };
@@ -441,10 +713,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t b = sbase + L::kRingOff + (i % kStages) * L::kTileBytes;
-#pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk)
-                    mma_f16_ts_warp(tmem + 2 * kKeys + pipe * DP, tmem + pipe * kKeys + kk * 8,
-                                    smem_desc_sw128_nmajor(b + kk * 2048), idesc_o, pv_n[pipe] > 0 || kk > 0);
+                mma_values(tmem + 2 * kKeys + pipe * DP, tmem + pipe * kKeys, b, idesc_o, pv_n[pipe] > 0);
                 tc_commit_warp(ofull(pipe));
                 __syncwarp();
                 ++pv_n[pipe];
@@ -623,7 +892,8 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             constexpr int kChunks = DP / 8, kLines = kSoftmaxThreads / kChunks;
             const int ch = tid % kChunks, lines = w.rows * split;
             const bool inside = ch * 8 < p.head_dim;
-            const uint16_t* q_head = p.q + w.token0 * p.q_stride + static_cast<int64_t>(w.head * p.group) * p.head_dim + ch * 8;
+            const int token = w.row0 / p.group, over = w.row0 - token * p.group;
+            const uint16_t* q_head = p.q + (w.token0 + token) * p.q_stride + static_cast<int64_t>(w.head * p.group) * p.head_dim + ch * 8;
             for (int line0 = tid / kChunks; line0 < lines; line0 += 8 * kLines) {
                 uint4 v[8];
 #pragma unroll
@@ -631,7 +901,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                     const int line = line0 + i * kLines;
                     v[i] = make_uint4(0u, 0u, 0u, 0u);
                     if (line < lines && inside) {
-                        const int row = w.row0 + (split > 1 ? line % w.rows : line), t = row / p.group, g = row - t * p.group;
+                        const int row = over + (split > 1 ? line % w.rows : line), t = by_group(p, row), g = row - t * p.group;
                         v[i] = *reinterpret_cast<const uint4*>(q_head + t * p.q_stride + g * p.head_dim);
                     }
                 }
@@ -669,7 +939,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
         // One tile for this thread's row and W keys from cbeg: P over S, m, l and,
         // where m moved, its half of O.  The row's other thread has the same m.
         const uint32_t pair = 2 + pipe * 4 + quarter;   // the pair's barrier
-        const uint32_t mine = sbase + L::kMlOff + ((pipe * 2 + half) * kRows + r) * 4, theirs = mine ^ (kRows * 4);
+        const uint32_t mine = sbase + L::kMlOff + ((pipe * 2 + half) * kRows + r) * 4;
         auto softmax_tile = [&](auto w_tag, int j) {
             constexpr int W = decltype(w_tag)::value;
             constexpr int kStep = W < 32 ? W : 32;
@@ -678,48 +948,66 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             // address taken after the wait, so the reads below stay behind it
             uint32_t ksc = sbase + L::kScaleOff + (j % L::kScaleSlots) * (2 * kKeys * 4) + cbeg * 4;
             asm volatile("" : "+r"(ksc)::"memory");
+            // kStep scores from the b-th on, with key scales (which hold c) and mask
+            auto scores = [&](int b, uint32_t (&v)[kStep]) {
+                if constexpr (W == 16)
+                    tmem_ld_x16_sync(t_s + cbeg, v);
+                else
+                    tmem_ld_x32_sync(t_s + cbeg + b, v);
+                if constexpr (kFp8) {
+#pragma unroll
+                    for (int i = 0; i < kStep; i += 4) {
+                        const float4 f = lds_f4(ksc + (b + i) * 4);
+                        const uint64_t x = mul2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), pack2(f.x, f.y));
+                        const uint64_t y = mul2(pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), pack2(f.z, f.w));
+                        v[i] = static_cast<uint32_t>(x), v[i + 1] = static_cast<uint32_t>(x >> 32);
+                        v[i + 2] = static_cast<uint32_t>(y), v[i + 3] = static_cast<uint32_t>(y >> 32);
+                    }
+                }
+                if (masked) {
+                    const int top = hi - key0 - b, bot = lo - key0 - b;
+#pragma unroll
+                    for (int i = 0; i < kStep; ++i)
+                        if (i > top || i < bot) v[i] = 0xff800000u;
+                }
+            };
+            // m of the larger of both threads' maxima
+            auto exchange = [&](float x) {
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine), "f"(x) : "memory");
+                asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+                float other;
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(mine ^ (kRows * 4)) : "memory");
+                return fmaxf(x, other);
+            };
+            float mx = kNegInf, my = kNegInf;
+            if (done == 0) {  // the first tile's maximum is the first m
+#pragma unroll 1
+                for (int b = 0; b < W; b += kStep) {
+                    uint32_t v[kStep];
+                    scores(b, v);
+#pragma unroll
+                    for (int i = 0; i < kStep; i += 4) {
+                        mx = max3(mx, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                        my = max3(my, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+                    }
+                }
+                m = exchange(fmaxf(mx, my) * (kFp8 ? 1.0f : c));
+            }
             uint32_t o[W / 2];
-            float mx;
             uint64_t l0, l1;
-            // o = 2^(scores - m), packed, their sums, and the largest score; 32 keys at a time
-            auto weights = [&]() {
+            // The weights are taken with the m of the tiles before, without waiting
+            // for this one's maximum; where that turns out to lie too far above, m
+            // moves and they are taken again.  Both threads of a row go on with the
+            // same m, and neither writes P before the other has read its scores.
+            for (;;) {
                 const float mc = m == kNegInf ? 0.0f : -m;
                 const uint64_t mc2 = pack2(mc, mc);
-                float my = kNegInf;
-                mx = kNegInf;
+                mx = my = kNegInf;
                 l0 = l1 = 0ull;
-                uint32_t s[2][kStep];
-                auto read = [&](int b) {
-                    if constexpr (W == 16)
-                        tmem_ld_x16_sync(t_s + cbeg, reinterpret_cast<uint32_t(&)[16]>(s[0]));
-                    else
-                        tmem_ld_x32(t_s + cbeg + b, s[kFp8 ? 0 : (b / kStep) & 1]);
-                };
-                read(0);
-                if constexpr (!kFp8 && W == 64) read(32);
 #pragma unroll
                 for (int b = 0; b < W; b += kStep) {
-                    uint32_t* v = s[kFp8 ? 0 : (b / kStep) & 1];
-                    if constexpr (W > 16) {
-                        if (kFp8 && b > 0) read(b);
-                        tmem_wait_ld_x32(v);
-                    }
-                    if constexpr (kFp8) {  // key scales (which hold c)
-#pragma unroll
-                        for (int i = 0; i < kStep; i += 4) {
-                            const float4 f = lds_f4(ksc + (b + i) * 4);
-                            const uint64_t x = mul2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), pack2(f.x, f.y));
-                            const uint64_t y = mul2(pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), pack2(f.z, f.w));
-                            v[i] = static_cast<uint32_t>(x), v[i + 1] = static_cast<uint32_t>(x >> 32);
-                            v[i + 2] = static_cast<uint32_t>(y), v[i + 3] = static_cast<uint32_t>(y >> 32);
-                        }
-                    }
-                    if (masked) {
-                        const int top = hi - key0 - b, bot = lo - key0 - b;
-#pragma unroll
-                        for (int i = 0; i < kStep; ++i)
-                            if (i > top || i < bot) v[i] = 0xff800000u;
-                    }
+                    uint32_t v[kStep];
+                    scores(b, v);
 #pragma unroll
                     for (int i = 0; i < kStep; i += 4) {
                         mx = max3(mx, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
@@ -744,52 +1032,33 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                 }
                 mx = fmaxf(mx, my);
                 if constexpr (!kFp8) mx *= c;
-            };
-            // The weights are taken with the m of the tiles before, without waiting
-            // for this one's maximum; where that turns out to lie too far above
-            // (always in the first tile), m moves and they are taken again.  Both
-            // threads of a row go on with the same m, and neither writes P before
-            // the other has read its scores.
-            weights();
-            tc_fence_before();
-            const bool moves = bar_red_or(pair, 64, done == 0 || (valid && mx - m > kSlack));  // -inf - -inf: no
-            tc_fence_after();
-            if (moves) {
-                asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine), "f"(mx) : "memory");
-                asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
-                float other;
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(theirs) : "memory");
-                mx = fmaxf(mx, other);
-                float alpha = 1.0f;
-                if (done == 0) {
-                    m = mx;
-                } else {
-                    if (valid && mx - m > kSlack) {
-                        alpha = ex2(m - mx);  // 0 while nothing was seen
-                        m = mx;
-                        l *= alpha;
-                    }
-                    // O is at rest once the last product has been added
-                    if (!mbar_wait_warp(ofull(pipe), static_cast<uint32_t>((done - 1) & 1), abort_flag)) {
-                        if (lane == 0) attn_error(kErrWaitMma, abort_flag);
-                        ok = false;
-                        return;
-                    }
-                    tc_fence_after();
-#pragma unroll
-                    for (int b = 0; b < DP / 2; b += 16) {
-                        uint32_t v[16];
-                        tmem_ld_x16_sync(t_o + b, v);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
-                        tmem_st_x16(t_o + b, v);
-                    }
-                }
-                weights();
-                // the other thread has read its scores too
                 tc_fence_before();
-                asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+                const bool moves = bar_red_or(pair, 64, valid && mx - m > kSlack);  // -inf - -inf: no
                 tc_fence_after();
+                if (!moves) break;
+                mx = exchange(mx);
+                float alpha = 1.0f;
+                if (valid && mx - m > kSlack) {
+                    alpha = ex2(m - mx);  // 0 while nothing was seen
+                    m = mx;
+                    l *= alpha;
+                }
+                if (done == 0) continue;
+                // O is at rest once the last product has been added
+                if (!mbar_wait_warp(ofull(pipe), static_cast<uint32_t>((done - 1) & 1), abort_flag)) {
+                    if (lane == 0) attn_error(kErrWaitMma, abort_flag);
+                    ok = false;
+                    return;
+                }
+                tc_fence_after();
+#pragma unroll 1
+                for (int b = 0; b < DP / 2; b += 16) {
+                    uint32_t v[16];
+                    tmem_ld_x16_sync(t_o + b, v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+                    tmem_st_x16(t_o + b, v);
+                }
             }
 #pragma unroll
             for (int b = 0; b < W / 2; b += kStep / 2) {
@@ -845,218 +1114,63 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine), "f"(l) : "memory");
             asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
             float other;
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(theirs) : "memory");
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(mine ^ (kRows * 4)) : "memory");
             l += other;
         }
-        constexpr float kUnscale = 1.0f / kPScale;
-        constexpr int kHalf = DP / 2;          // output columns a thread
-        const int cout = half * kHalf;
-        const uint32_t ml = sbase + L::kMlOff, joined = sbase + L::kJoinedOff;
-        // fp32 partials [128][DP] where Q was, 16-byte chunks swizzled by the row
-        auto stage_at = [&](int row, int chunk) { return sbase + L::kQOff + static_cast<uint32_t>(row * DP + ((chunk ^ (row & 7)) << 2)) * 4u; };
-        auto out_at = [&](int row) {
-            const int t = row / p.group, g = row - t * p.group;
-            return p.out + (w.token0 + t) * p.out_stride + static_cast<int64_t>(w.head * p.group + g) * p.head_dim;
-        };
-        auto write_row = [&](int b, const uint32_t* o, float inv) {  // 32 values from column b of this thread's row
-            uint16_t* dst = out_at(R);
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-                if (b + i >= p.head_dim) break;
-                uint32_t v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    v[e] = pack16<kBf16>(__uint_as_float(o[i + 2 * e]) * inv, __uint_as_float(o[i + 2 * e + 1]) * inv);
-                *reinterpret_cast<uint4*>(dst + b + i) = make_uint4(v[0], v[1], v[2], v[3]);
-            }
-        };
         if (w.two && p.cl == 1) {
             if (ok && busy) {
-                const float inv = l > 0.0f ? kUnscale / l : 0.0f;
+                // Each warp through its own rows of this pipe's Q tile, which no product
+                // reads any more (half a row a warp): 16-byte chunks swizzled by the row,
+                // then 16 bytes a lane along the rows to memory.
+                constexpr int kHalf = DP / 2, kChunks = kHalf / 8, kRowsAtOnce = 32 / kChunks;
+                const float inv = l > 0.0f ? 1.0f / (kPScale * l) : 0.0f;
+                const uint32_t mine = sbase + L::kQOff + pipe * L::kTileBytes + (half * 4 + quarter) * (32 * kHalf * 2);
 #pragma unroll
                 for (int b = 0; b < kHalf; b += 32) {
                     uint32_t o[32];
                     if (done > 0) {
-                        tmem_ld_x32(t_o + b, o);
-                        tmem_wait_ld_x32(o);
+                        tmem_ld_x32_sync(t_o + b, o);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = 0u;
                     }
-                    if (valid) write_row(cout + b, o, inv);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            v[e] = pack16<kBf16>(__uint_as_float(o[i + 2 * e]) * inv, __uint_as_float(o[i + 2 * e + 1]) * inv);
+                        sts128(mine + lane * (kHalf * 2) + ((((b + i) / 8) ^ (lane & (kChunks - 1))) << 4), v[0], v[1], v[2], v[3]);
+                    }
+                }
+                __syncwarp();
+                const int row0 = w.row0 + qtile * kRows + quarter * 32, token = row0 / p.group, over = row0 - token * p.group;
+                const int left = w.rows - qtile * kRows - quarter * 32, ch = lane % kChunks, col = half * kHalf + ch * 8;
+                uint16_t* out = p.out + (w.token0 + token) * p.out_stride + static_cast<int64_t>(w.head * p.group) * p.head_dim + col;
+                if (col < p.head_dim) {
+#pragma unroll 4
+                    for (int i = lane / kChunks; i < 32; i += kRowsAtOnce) {
+                        if (i >= left) break;
+                        const uint4 v = lds128(mine + i * (kHalf * 2) + ((ch ^ (i & (kChunks - 1))) << 4));
+                        const int t = by_group(p, over + i), g = over + i - t * p.group;
+                        *reinterpret_cast<uint4*>(out + t * p.out_stride + g * p.head_dim) = v;
+                    }
                 }
             }
         } else if (have) {
-            // Partial results meet in shared memory: the pipes', the copies' and
-            // then the cluster's.  Rounds: one, or one for each row tile.
-            const int rounds = w.two ? 2 : 1;
-            softmax_bar();  // both pipes' products are complete: Q's place is free
-            for (int round = 0; round < rounds; ++round) {
-                const int rows = w.two ? (round == 0 ? kRows : w.rows - kRows) : w.rows;
-                if (round > 0) {
-                    ok = ok && mbar_wait_cluster(joinfree, static_cast<uint32_t>((round - 1) & 1), abort_flag);
-                    ok = __all_sync(0xffffffffu, ok);
-                }
-                if (w.two ? pipe == round : pipe == 1) {
-                    if (valid && half == 0) sts_f2(ml + r * 8, m, done > 0 ? l : 0.0f);
-                    if (ok && busy && done > 0) {
-#pragma unroll
-                        for (int b = 0; b < kHalf; b += 32) {
-                            uint32_t o[32];
-                            tmem_ld_x32(t_o + b, o);
-                            tmem_wait_ld_x32(o);
-                            if (valid)
-#pragma unroll
-                                for (int i = 0; i < 32; i += 4) sts128(stage_at(r, (cout + b + i) / 4), o[i], o[i + 1], o[i + 2], o[i + 3]);
-                        }
-                    }
-                }
-                softmax_bar();
-                if (!w.two) {
-                    const bool direct = split == 1 && p.cl == 1;
-                    if (pipe == 0 && ok && busy) {
-                        // add pipe 1's partial to this one's
-                        const float2 other = valid ? lds_f2(ml + r * 8) : make_float2(0.0f, 0.0f);
-                        const float mine_l = done > 0 ? l : 0.0f;
-                        const float top = fmaxf(mine_l > 0.0f ? m : other.x, other.y > 0.0f ? other.x : m);
-                        const float a0 = mine_l > 0.0f ? ex2(m - top) : 0.0f;
-                        const float a1 = other.y > 0.0f ? ex2(other.x - top) : 0.0f;
-                        const float sum = a0 * mine_l + a1 * other.y;
-                        const float inv = sum > 0.0f ? kUnscale / sum : 0.0f;
-                        // both threads of the row have read its (m, l)
-                        asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
-#pragma unroll
-                        for (int b = 0; b < kHalf; b += 32) {
-                            uint32_t o[32];
-                            if (done > 0) {
-                                tmem_ld_x32(t_o + b, o);
-                                tmem_wait_ld_x32(o);
-                            }
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                                if (valid && a1 > 0.0f) v = lds128(stage_at(r, (cout + b + i) / 4));
-                                const float x[4] = {__uint_as_float(v.x) * a1, __uint_as_float(v.y) * a1, __uint_as_float(v.z) * a1,
-                                                    __uint_as_float(v.w) * a1};
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    o[i + e] = __float_as_uint(a0 > 0.0f ? fmaf(__uint_as_float(o[i + e]), a0, x[e]) : x[e]);
-                            }
-                            if (valid && direct) {
-                                write_row(cout + b, o, inv);
-                            } else if (valid) {
-#pragma unroll
-                                for (int i = 0; i < 32; i += 4) sts128(stage_at(r, (cout + b + i) / 4), o[i], o[i + 1], o[i + 2], o[i + 3]);
-                            }
-                        }
-                        if (valid && half == 0) sts_f2(ml + r * 8, top, sum);
-                    }
-                    if (direct) break;
-                    softmax_bar();
-                }
-                // the copies of a row into the first of them (its (m, l) apart: other
-                // threads of the row still read the copies')
-                const int units = rows * (DP / 4);
-                for (int u = tid; u < units; u += kSoftmaxThreads) {
-                    const int row = u / (DP / 4), ch = u - row * (DP / 4);
-                    float2 q[4];
-                    float top = kNegInf, sum = 0.0f;
-#pragma unroll
-                    for (int f = 0; f < 4; ++f) {
-                        q[f] = f < split ? lds_f2(ml + (f * per_copy + row) * 8) : make_float2(kNegInf, 0.0f);
-                        if (q[f].y > 0.0f) top = fmaxf(top, q[f].x);
-                    }
-                    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int f = 0; f < 4; ++f) {
-                        if (!(q[f].y > 0.0f)) continue;
-                        const uint4 v = lds128(stage_at(f * per_copy + row, ch));
-                        const float a = ex2(q[f].x - top);
-                        sum = fmaf(q[f].y, a, sum);
-                        acc[0] = fmaf(__uint_as_float(v.x), a, acc[0]);
-                        acc[1] = fmaf(__uint_as_float(v.y), a, acc[1]);
-                        acc[2] = fmaf(__uint_as_float(v.z), a, acc[2]);
-                        acc[3] = fmaf(__uint_as_float(v.w), a, acc[3]);
-                    }
-                    if (p.cl == 1) {
-                        const float inv = sum > 0.0f ? kUnscale / sum : 0.0f;
-                        if (ch * 4 < p.head_dim)
-                            *reinterpret_cast<uint2*>(out_at(w.row0 + row) + ch * 4) =
-                                make_uint2(pack16<kBf16>(acc[0] * inv, acc[1] * inv), pack16<kBf16>(acc[2] * inv, acc[3] * inv));
-                    } else {
-                        sts128(stage_at(row, ch), __float_as_uint(acc[0]), __float_as_uint(acc[1]), __float_as_uint(acc[2]),
-                               __float_as_uint(acc[3]));
-                        if (ch == 0) sts_f2(joined + row * 8, top, sum);
-                    }
-                }
-                if (p.cl == 1) break;
-                softmax_bar();
-                if (tid < p.cl) mbar_arrive_remote(joinfull, static_cast<uint32_t>(tid));
-                __syncwarp();
-                bool all = mbar_wait_cluster(joinfull, static_cast<uint32_t>(round & 1), abort_flag);
-                all = __all_sync(0xffffffffu, all);
-                if (!all && lane == 0) attn_error(kErrWaitDequant, abort_flag);
-                if (all) {
-                    // each rank finishes its share of the rows' 16-byte chunks; with
-                    // few of them several lanes share one, each reading some ranks'
-                    // partials (one remote read's time instead of a rank count's)
-                    const int share = (units + p.cl - 1) / p.cl;
-                    int lanes = p.cl;
-                    while (lanes > 1 && share * lanes > kSoftmaxThreads) lanes >>= 1;
-                    const int k0 = tid & (lanes - 1);
-                    for (int b = 0; b < share; b += kSoftmaxThreads / lanes) {
-                        const int i = b + tid / lanes, u = rank * share + i;
-                        const bool live = i < share && u < units;
-                        const int row = live ? u / (DP / 4) : 0, ch = live ? u - row * (DP / 4) : 0;
-                        const uint32_t ml_at = joined + row * 8, st_at = stage_at(row, ch);
-                        float top = kNegInf, sum = 0.0f;
-                        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        for (int k = k0; k < p.cl; k += 4 * lanes) {
-                            float2 q[4];
-                            float4 v[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t from_rank = static_cast<uint32_t>(k + e * lanes < p.cl ? k + e * lanes : k);
-                                q[e] = ld_cluster_f2(mapa_shared(ml_at, from_rank));
-                                v[e] = ld_cluster_f4(mapa_shared(st_at, from_rank));
-                                if (k + e * lanes >= p.cl) q[e].y = 0.0f;
-                            }
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                if (!(q[e].y > 0.0f)) continue;
-                                const float to = fmaxf(top, q[e].x);
-                                const float x = ex2(top - to), y = ex2(q[e].x - to);
-                                top = to;
-                                sum = sum * x + q[e].y * y;
-                                acc.x = acc.x * x + v[e].x * y;
-                                acc.y = acc.y * x + v[e].y * y;
-                                acc.z = acc.z * x + v[e].z * y;
-                                acc.w = acc.w * x + v[e].w * y;
-                            }
-                        }
-                        for (int d = lanes >> 1; d > 0; d >>= 1) {
-                            const float o_top = __shfl_xor_sync(0xffffffffu, top, d), o_sum = __shfl_xor_sync(0xffffffffu, sum, d);
-                            const float4 o = make_float4(__shfl_xor_sync(0xffffffffu, acc.x, d), __shfl_xor_sync(0xffffffffu, acc.y, d),
-                                                         __shfl_xor_sync(0xffffffffu, acc.z, d), __shfl_xor_sync(0xffffffffu, acc.w, d));
-                            const float to = fmaxf(top, o_top);
-                            const float x = sum > 0.0f ? ex2(top - to) : 0.0f, y = o_sum > 0.0f ? ex2(o_top - to) : 0.0f;
-                            top = to;
-                            sum = sum * x + o_sum * y;
-                            acc.x = acc.x * x + o.x * y;
-                            acc.y = acc.y * x + o.y * y;
-                            acc.z = acc.z * x + o.z * y;
-                            acc.w = acc.w * x + o.w * y;
-                        }
-                        const float inv = sum > 0.0f ? kUnscale / sum : 0.0f;
-                        if (live && k0 == 0 && ch * 4 < p.head_dim)
-                            *reinterpret_cast<uint2*>(out_at(w.row0 + round * kRows + row) + ch * 4) =
-                                make_uint2(pack16<kBf16>(acc.x * inv, acc.y * inv), pack16<kBf16>(acc.z * inv, acc.w * inv));
-                    }
-                }
-                softmax_bar();
-                if (tid < p.cl) mbar_arrive_remote(joinfree, static_cast<uint32_t>(tid));
-                __syncwarp();
-            }
+            Join j;
+            j.sbase = sbase;
+            j.t_o = t_o;
+            j.joinfull = joinfull;
+            j.joinfree = joinfree;
+            j.rank = rank;
+            j.split = split;
+            j.done = done;
+            j.ok = ok;
+            j.valid = valid;
+            j.m = m;
+            j.l = l;
+            join_results<DP, kBf16, kFp8>(p, w, j, abort_flag);
         }
     }
 
@@ -1073,6 +1187,42 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
 }
 
 namespace {
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled() {
+    static std::once_flag once;
+    static EncodeTiledFn fn = nullptr;
+    std::call_once(once, [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(f);
+    });
+    return fn;
+}
+
+// Tensor map over one half of a paged cache: (value, slot, head, page), boxes of
+// box_inner values x box_slots slots, 128-byte swizzle (64 for 64-byte boxes).
+bool encode_pages(CUtensorMap* map, const fp8w_kv_cache& c, const void* base, uint32_t box_inner, uint32_t box_slots) {
+    EncodeTiledFn fn = encode_tiled();
+    if (!fn) return false;
+    const bool codes = c.dtype == FP8W_E4M3;
+    const cuuint64_t es = codes ? 1 : 2;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.page_size),
+                                static_cast<cuuint64_t>(c.kv_heads), static_cast<cuuint64_t>(c.num_pages)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.token_stride) * es, static_cast<cuuint64_t>(c.head_stride) * es,
+                                   static_cast<cuuint64_t>(c.page_stride) * es};
+    const cuuint32_t box[4] = {box_inner, box_slots, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(base), dims,
+              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              box_inner * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 template <int DP, bool kBf16, bool kFp8>
 cudaError_t launch_attn(const AttentionArgs& a, cudaStream_t st) {
@@ -1096,16 +1246,10 @@ cudaError_t launch_attn(const AttentionArgs& a, cudaStream_t st) {
 
     const fp8w_kv_cache& c = *a.cache;
     const int group = a.q_heads / c.kv_heads;
-    const uint64_t es = kFp8 ? 1 : 2;
     CUtensorMap map_k, map_v;
     const uint32_t box = static_cast<uint32_t>(c.page_size < kKeys ? c.page_size : kKeys);
-    for (int i = 0; i < 2; ++i)
-        if (!encode_pages(i ? &map_v : &map_k, kFp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
-                          i ? c.v : c.k, static_cast<uint64_t>(c.head_dim), static_cast<uint64_t>(c.page_size),
-                          static_cast<uint64_t>(c.kv_heads), static_cast<uint64_t>(c.num_pages),
-                          static_cast<uint64_t>(c.token_stride) * es, static_cast<uint64_t>(c.head_stride) * es,
-                          static_cast<uint64_t>(c.page_stride) * es, kFp8 ? DP : 64, box, kFp8 && DP == 64))
-            return cudaErrorInvalidValue;
+    if (!encode_pages(&map_k, c, c.k, kFp8 ? DP : 64, box) || !encode_pages(&map_v, c, c.v, kFp8 ? DP : 64, box))
+        return cudaErrorInvalidValue;
 
     const int64_t tiles = attention_row_tiles(a, group, 2 * kRows), items = tiles * c.kv_heads;
     // CTAs a cluster: as many as fill the GPU, while each has two key tiles at least
@@ -1147,7 +1291,8 @@ cudaError_t launch_dim(const AttentionArgs& a, cudaStream_t st) {
 
 cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t st) {
     const int64_t most_new = a.starts ? (a.max_new > 0 ? a.max_new : a.tokens) : 1;
-    if (most_new * (a.q_heads / a.cache->kv_heads) <= kFewRows) return launch_attention_few(a, st);
+    if (most_new * (a.q_heads / a.cache->kv_heads) <= (a.cache->dtype == FP8W_E4M3 ? kFewRowsCodes : kFewRows))
+        return launch_attention_few(a, st);
     return a.cache->head_dim <= 64 ? launch_dim<64>(a, st) : launch_dim<128>(a, st);
 }
 

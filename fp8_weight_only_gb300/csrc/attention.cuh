@@ -26,6 +26,7 @@ struct AttnParams {
     const float* v_scales;
     int64_t num_pages;
     int seqs, kv_heads, group, head_dim, page_size, log_page;
+    uint32_t group_inverse;  // 2^32 / group rounded up (0 for 1)
     float c;         // scale * log2(e)
     int64_t window;  // 0: none
     int row_tiles;   // bound on the row tiles of all sequences
@@ -138,6 +139,7 @@ inline AttnParams attention_params(const AttentionArgs& a) {
     p.seqs = static_cast<int>(a.seqs);
     p.kv_heads = c.kv_heads;
     p.group = a.q_heads / c.kv_heads;
+    p.group_inverse = static_cast<uint32_t>(((1ull << 32) + p.group - 1) / p.group);
     p.head_dim = c.head_dim;
     p.page_size = c.page_size;
     while ((1 << p.log_page) < c.page_size) ++p.log_page;

@@ -28,8 +28,7 @@ enum DeviceError : int {
     kErrWaitMma = 2,      // waiting for tensor-core completion
     kErrWaitDequant = 3,  // MMA issuer gave up waiting for a dequantised stage
     kErrWaitSlot = 4,     // producer gave up waiting for a free stage
-    kErrWaitDrain = 5,    // giving up on in-flight copies at exit
-    kErrIndex = 6         // an index in device memory is out of its range
+    kErrWaitDrain = 5     // giving up on in-flight copies at exit
 };
 
 // ---------------------------------------------------------------- loads --

@@ -99,6 +99,10 @@ struct W8A8Args {
 cudaError_t launch_w8a8(const W8A8Args& a, cudaStream_t st);
 int read_w8a8_device_error();
 
+// Recorded where an index in device memory is out of its range (beside the
+// wait failures' codes).
+constexpr int kErrIndex = 6;
+
 // K6: rotary positions (cache null), with the append of k and v to a paged
 // cache.  q null: keys and values only.  spec null: no rotation.
 struct RopeArgs {
@@ -139,13 +143,6 @@ struct AttentionArgs {
 };
 cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t st);
 int read_attention_device_error();
-
-// 4-D tiled tensor map over a paged cache: (value, slot, head, page) with the
-// given byte strides, boxes of box_inner values x box_slots slots; the swizzle
-// is 128 bytes, or 64 where a box row has 64 bytes.
-bool encode_pages(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t dim, uint64_t slots,
-                  uint64_t heads, uint64_t pages, uint64_t slot_bytes, uint64_t head_bytes, uint64_t page_bytes,
-                  uint32_t box_inner, uint32_t box_slots, bool swizzle64);
 
 // Kernel-recorded wait failures (0 = none); reading clears them.
 int read_skinny_device_error();

@@ -1113,20 +1113,6 @@ bool encode_3d_blocks(CUtensorMap* map, const void* base, uint64_t rows, uint64_
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool encode_pages(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t dim, uint64_t slots,
-                  uint64_t heads, uint64_t pages, uint64_t slot_bytes, uint64_t head_bytes, uint64_t page_bytes,
-                  uint32_t box_inner, uint32_t box_slots, bool swizzle64) {
-    EncodeTiledFn fn = get_encode_fn();
-    if (!fn) return false;
-    const cuuint64_t dims[4] = {dim, slots, heads, pages};
-    const cuuint64_t strides[3] = {slot_bytes, head_bytes, page_bytes};
-    const cuuint32_t box[4] = {box_inner, box_slots, 1, 1};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
-    return fn(map, dt, 4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              swizzle64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 cudaError_t device_sm_count(int& sms) {
     static int cache[64];
     static std::mutex mu;

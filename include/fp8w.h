@@ -454,7 +454,7 @@ FP8W_API fp8w_status fp8w_rope_append(const void *q, const void *k, const void *
  * positions 0 .. len - n + i, with window > 0 only the last `window` of them.
  * A token that sees none (len 0, or a position below 0) gets zeros.
  *   q            [tokens, q_heads, head_dim] act_dtype, token stride q_stride;
- *                q_heads a multiple of the cache's kv_heads.
+ *                q_heads a multiple of the cache's kv_heads, at most 4096 times them.
  *   block_table  [seqs, table_width] int32, device: page of the sequence's
  *                positions c * page_size ..; entries past its last position, or
  *                of pages wholly before its window, are not used.
