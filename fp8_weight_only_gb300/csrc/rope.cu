@@ -9,13 +9,14 @@
 // 0), code = nearest-even e4m3 of the IEEE quotient.
 //
 // Memory bound: every value is read and written once, and three operations a
-// value are nothing beside that.  A thread holds 16 values of a head, the two
+// value are nothing beside that.  A lane holds 16 values of a head, the two
 // 8-value chunks that make 8 whole pairs: chunks i and i + rot_dim / 16 with
 // pairs in halves, 2 i and 2 i + 1 with interleaved ones, so one set of eight
-// cosines and sines serves either form and a thread reads what it writes
-// (in-place calls need no further order).  A CTA takes one token and walks its
-// heads: a thread keeps its item's cosines and sines in registers over the
-// heads, and the table row is read once a token.
+// cosines and sines serves either form and a lane writes what it has read
+// (in-place calls need no further order).  A warp takes a token, or with few
+// tokens a part of its heads: 32 / P heads a step (P lanes a head), kAhead
+// steps' loads in flight, the first before the position and the table row are
+// asked for, and its cosines and sines stay in registers over the heads.
 #include "fp8w_device.cuh"
 #include "fp8w_internal.h"
 
@@ -25,7 +26,9 @@ __device__ int g_rope_error;
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeWarps = 4;
+constexpr int kRopeFill = 16;  // warps an SM up to which a token's heads are divided
+constexpr int kAhead = 2;  // steps of a warp in flight: 2 KB (4 steps: 77 us against 68 for 344 MB, the registers leave fewer warps)
 
 struct RopeParams {
     const uint16_t* q;
@@ -46,6 +49,7 @@ struct RopeParams {
     float* vs;
     int64_t num_pages, page_stride, head_stride, token_stride;
     int page_size;
+    int parts, per_part;  // warps a token, steps of each
 };
 
 template <bool kBf16>
@@ -70,21 +74,44 @@ __device__ __forceinline__ uint4 narrow(const float* f) {
 
 // P lanes (a power of two >= head_dim / 16) work on a head.
 template <int P, bool kBf16, bool kFp8>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_constant__ RopeParams p) {
     pdl_launch_dependents();
-    constexpr int kGroups = kRopeThreads / P;
-    const int item = threadIdx.x & (P - 1);
-    const int group = threadIdx.x / P;
-    const int64_t token = blockIdx.x;
+    constexpr int kHeads = 32 / P;  // heads a step
+    const int lane = threadIdx.x & 31, item = lane & (P - 1);
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kRopeWarps + (threadIdx.x >> 5);
+    const int64_t token = unit / p.parts;
+    if (token >= p.tokens) return;
+    const int part = static_cast<int>(unit - token * p.parts);
     const bool live = item * 16 < p.head_dim;
     const int half = p.rot_dim >> 1;
     const bool turns = p.positions && item * 16 < p.rot_dim;
     // the item's two chunks (first values)
     const int c0 = turns ? (p.interleaved ? item * 16 : item * 8) : item * 16;
     const int c1 = turns && !p.interleaved ? half + item * 8 : c0 + 8;
-    const int heads = p.q_heads + 2 * p.kv_heads;
-    const int first = static_cast<int>(blockIdx.y) * kGroups + group, step = static_cast<int>(gridDim.y) * kGroups;
+    const int heads = p.q_heads + 2 * p.kv_heads, steps = (heads + kHeads - 1) / kHeads;
+    const int first = part * p.per_part, last = min(first + p.per_part, steps);
     pdl_wait();
+
+    int64_t slot = 0;
+    if (p.kv_heads) slot = __ldg(p.slots + token);
+    uint4 x[kAhead][2];
+    auto head_of = [&](int step) { return step * kHeads + lane / P; };
+    auto load = [&](int step, uint4 (&y)[2]) {
+        const int h = head_of(step);
+        const bool is_q = h < p.q_heads, is_k = !is_q && h < p.q_heads + p.kv_heads;
+        const int kvh = h - p.q_heads - (is_k ? 0 : p.kv_heads);
+        const uint16_t* src = is_q ? p.q + token * p.q_stride + static_cast<int64_t>(h) * p.head_dim
+                              : is_k ? p.k + token * p.k_stride + static_cast<int64_t>(kvh) * p.head_dim
+                                     : p.v + token * p.v_stride + static_cast<int64_t>(kvh) * p.head_dim;
+        y[0] = y[1] = make_uint4(0u, 0u, 0u, 0u);
+        if (live && step < last && h < heads) {
+            // values that do not turn go by their item's own chunks
+            y[0] = *reinterpret_cast<const uint4*>(src + (is_q || is_k ? c0 : item * 16));
+            y[1] = *reinterpret_cast<const uint4*>(src + (is_q || is_k ? c1 : item * 16 + 8));
+        }
+    };
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) load(first + u, x[u]);
 
     float cs[8], sn[8];
     if (turns) {
@@ -125,34 +152,19 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
             }
         }
     }
-    int64_t slot = -1, page = 0, off = 0;
-    if (p.kv_heads) {
-        slot = __ldg(p.slots + token);
-        page = slot / p.page_size;
-        off = slot - page * p.page_size;
-        if (slot >= 0 && page >= p.num_pages) {
-            atomicCAS(&g_rope_error, 0, 6000 + kErrIndex);
-            slot = -1;
-        }
+    const int64_t page = slot >= 0 ? slot / p.page_size : 0, off = slot - page * p.page_size;
+    bool kept = p.kv_heads && slot >= 0;  // the token goes into the cache
+    if (kept && page >= p.num_pages) {
+        atomicCAS(&g_rope_error, 0, 6000 + kErrIndex);
+        kept = false;
     }
 
-    // a warp's groups take consecutive heads: all of them stay in the loop
-    // until the last is done, so the exchanges below involve whole warps
-    for (int h0 = first; h0 - (group & (32 / P - 1)) < heads; h0 += step) {
-        const int h = h0;
+    auto finish = [&](int step, uint4 x0, uint4 x1) {
+        const int h = head_of(step);
         const bool is_q = h < p.q_heads, is_k = !is_q && h < p.q_heads + p.kv_heads;
-        const bool work = live && h < heads && (is_q || slot >= 0);
+        const bool work = live && h < heads && (is_q || kept);
         const int kvh = is_q ? 0 : h - p.q_heads - (is_k ? 0 : p.kv_heads);
-        const uint16_t* src = is_q ? p.q + token * p.q_stride + static_cast<int64_t>(h) * p.head_dim
-                              : is_k ? p.k + token * p.k_stride + static_cast<int64_t>(kvh) * p.head_dim
-                                     : p.v + token * p.v_stride + static_cast<int64_t>(kvh) * p.head_dim;
-        uint4 x0 = make_uint4(0u, 0u, 0u, 0u), x1 = x0;
-        // values that do not turn go by their item's own chunks
         const int s0 = (is_q || is_k) ? c0 : item * 16, s1 = (is_q || is_k) ? c1 : item * 16 + 8;
-        if (work) {
-            x0 = *reinterpret_cast<const uint4*>(src + s0);
-            x1 = *reinterpret_cast<const uint4*>(src + s1);
-        }
         float f[16];
         widen<kBf16>(x0, f);
         widen<kBf16>(x1, f + 8);
@@ -175,14 +187,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
             x0 = narrow<kBf16>(f);
             x1 = narrow<kBf16>(f + 8);
         }
-        if (is_q) {
-            if (work) {
-                uint16_t* dst = p.q_out + token * p.q_out_stride + static_cast<int64_t>(h) * p.head_dim;
-                *reinterpret_cast<uint4*>(dst + s0) = x0;
-                *reinterpret_cast<uint4*>(dst + s1) = x1;
-            }
+        if (is_q && work) {
+            uint16_t* dst = p.q_out + token * p.q_out_stride + static_cast<int64_t>(h) * p.head_dim;
+            *reinterpret_cast<uint4*>(dst + s0) = x0;
+            *reinterpret_cast<uint4*>(dst + s1) = x1;
         }
         if constexpr (kFp8) {
+            if (__all_sync(0xffffffffu, is_q)) return;  // a step of queries only
             float amax = 0.0f;
 #pragma unroll
             for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(f[e]));
@@ -209,24 +220,38 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
             *reinterpret_cast<uint4*>(dst + s0) = x0;
             *reinterpret_cast<uint4*>(dst + s1) = x1;
         }
+    };
+    for (int step = first; step < last; step += kAhead) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (step + u >= last) break;
+            const uint4 x0 = x[u][0], x1 = x[u][1];
+            load(step + u + kAhead, x[u]);
+            finish(step + u, x0, x1);
+        }
     }
 }
 
 template <int P>
-cudaError_t launch_p(const RopeParams& p, bool bf16, bool fp8, cudaStream_t st) {
+cudaError_t launch_p(RopeParams p, bool bf16, bool fp8, cudaStream_t st) {
     int sms = 0;
     cudaError_t e = device_sm_count(sms);
     if (e != cudaSuccess) return e;
-    const int heads = p.q_heads + 2 * p.kv_heads;
-    // one CTA a token; with few tokens a token's heads go to several CTAs
-    constexpr int kGroups = kRopeThreads / P;
-    const int most = (heads + kGroups - 1) / kGroups;
+    // one warp a token; with few tokens a token's heads go to several
+    const int steps = (p.q_heads + 2 * p.kv_heads + 32 / P - 1) / (32 / P);
+    const int64_t want = (static_cast<int64_t>(sms) * kRopeFill + p.tokens - 1) / p.tokens;
+    const int parts = static_cast<int>(want < steps ? want : steps);
+    p.per_part = (((steps + parts - 1) / parts + kAhead - 1) / kAhead) * kAhead;  // whole rounds
+    if (p.tokens * steps <= static_cast<int64_t>(sms) * kRopeFill) p.per_part = 1;  // a warp for each step
+    p.parts = (steps + p.per_part - 1) / p.per_part;
+    const int64_t blocks = (p.tokens * p.parts + kRopeWarps - 1) / kRopeWarps;
+    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.tokens), static_cast<unsigned>(p.tokens < 2 * sms ? most : 1));
-    cfg.blockDim = dim3(kRopeThreads);
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(kRopeWarps * 32);
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
