@@ -374,58 +374,60 @@ class KVCache:
         self._ref = ctypes.byref(self.spec)
 
 
-# The calls below run once a layer and token, so their checks are kept to a
-# few attribute reads each.
+# The calls below run once a layer and token, where a few microseconds of the
+# host count: they read each attribute once and compare in place; _refuse finds
+# out what was wrong.
 
-_torch = _raw_stream = None
+_torch = _stream_of = _empty_like = _dense = _int32 = _int64 = None
 _ACT = {}
 
 
 def _load_torch():
-    global _torch, _raw_stream
+    global _torch, _stream_of, _empty_like, _dense, _int32, _int64
     import torch
     _ACT.update({torch.bfloat16: FP8W_BF16, torch.float16: FP8W_F16})
     # the stream's handle without a Stream object around it, where torch has it
-    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _empty_like, _dense, _int32, _int64 = torch.empty_like, torch.contiguous_format, torch.int32, torch.int64
+    lib()
     _torch = torch
 
 
-def _rows(name, x, heads=None, dim=None):
-    """x [tokens, heads, head_dim] with its heads side by side; returns the token stride."""
-    if not x.is_cuda or x.dim() != 3:
-        raise TypeError("%s must be a 3-D [tokens, heads, head_dim] CUDA tensor" % name)
+def _refuse(name, x, index, dtype=None, shape=None, dense=False):
+    """Raises for what is wrong with an operand; returns the token stride of
+    rows [tokens, heads, head_dim] that are right after all (a stride of a
+    dimension of one)."""
+    if x.get_device() != index or index < 0:
+        raise TypeError("%s must be a CUDA tensor on the operands' device" % name)
+    if (x.dtype not in _ACT) if dtype is None else x.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, "bfloat16 or float16" if dtype is None else dtype, x.dtype))
+    if (x.dim() != 3) if shape is None else x.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" %
+                         (name, "[tokens, heads, head_dim]" if shape is None else tuple(shape), tuple(x.shape)))
+    if dense:
+        raise TypeError("%s must be contiguous" % name)
     tokens, h, d = x.shape
     s0, s1, s2 = x.stride()
-    if s2 != 1 or (s1 != d and h > 1) or (heads is not None and h != heads) or (dim is not None and d != dim):
-        raise ValueError("%s: shape %s with strides %s does not fit" % (name, tuple(x.shape), x.stride()))
+    if (s2 != 1 and d > 1) or (s1 != d and h > 1):
+        raise ValueError("%s: the heads of a token must be side by side, got shape %s with strides %s" %
+                         (name, tuple(x.shape), x.stride()))
     return s0 if tokens > 1 or s0 >= h * d else h * d
 
 
-def _index(name, t, dtype, shape, device):
-    if t.dtype != dtype or t.get_device() != device or not t.is_contiguous() or t.shape != shape:
-        raise TypeError("%s must be a contiguous %s tensor of shape %s on the same device" % (name, dtype, tuple(shape)))
+def _rows(name, x, index, dtype, shape):
+    """The token stride of an operand that has to have this type and shape."""
+    s = x.stride()
+    if x.shape != shape or x.dtype is not dtype or x.get_device() != index or s[-1] != 1 or s[-2] != shape[2] or \
+            s[0] < shape[1] * shape[2]:
+        return _refuse(name, x, index, dtype, shape)
+    return s[0]
+
+
+def _index(name, t, dtype, shape, index):
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        _refuse(name, t, index, dtype, shape, True)
     return t.data_ptr()
-
-
-def _positions(positions, rope, tokens, device):
-    shape = (tokens,) if rope.axes == 1 and positions.dim() == 1 else (rope.axes, tokens)
-    return _index("positions", positions, _torch.int32, shape, device)
-
-
-def _out(out, x):
-    """The output tensor for rows like x's, and its token stride."""
-    if out is None:
-        out = _torch.empty_like(x, memory_format=_torch.contiguous_format)
-        return out, out.stride(0)
-    if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
-        raise ValueError("out must have x's shape, type and device")
-    return out, _rows("out", out)
-
-
-def _act_of(x):
-    act = _ACT.get(x.dtype)
-    return _act(x.dtype) if act is None else act
 
 
 def rope(x, positions, rope, out=None):
@@ -434,13 +436,19 @@ def rope(x, positions, rope, out=None):
     sections.  x may be a view of a fused projection's rows; out may be x."""
     if _torch is None:
         _load_torch()
-    xs = _rows("x", x)
-    tokens, heads, dim = x.shape
-    dev = x.get_device()
-    out, os_ = _out(out, x)
-    st = (_lib or lib()).fp8w_rope(x.data_ptr(), _act_of(x), tokens, heads, dim, xs,
-                                   _positions(positions, rope, tokens, dev), rope._ref, out.data_ptr(), os_,
-                                   _raw_stream(dev))
+    dev, dtype, shape, s = x.get_device(), x.dtype, x.shape, x.stride()
+    act = _ACT.get(dtype)
+    if act is None or dev < 0 or len(shape) != 3:
+        _refuse("x", x, dev)
+    tokens, heads, dim = shape
+    xs = s[0] if s[2] == 1 and s[1] == dim and s[0] >= heads * dim else _refuse("x", x, dev)
+    if out is None:
+        out, os_ = _empty_like(x, memory_format=_dense), heads * dim
+    else:
+        os_ = _rows("out", out, dev, dtype, shape)
+    axes = rope.axes
+    pos = _index("positions", positions, _int32, (tokens,) if axes == 1 and positions.dim() == 1 else (axes, tokens), dev)
+    st = _lib.fp8w_rope(x.data_ptr(), act, tokens, heads, dim, xs, pos, rope._ref, out.data_ptr(), os_, _stream_of(dev))
     if st:
         _check(st)
     return out
@@ -454,25 +462,33 @@ def rope_append(q, k, v, slots, cache, positions=None, rope=None, out=None):
     rotation."""
     if _torch is None:
         _load_torch()
-    heads, dim = cache.kv_heads, cache.head_dim
-    ks, vs = _rows("k", k, heads, dim), _rows("v", v, heads, dim)
-    tokens, dtype, dev = k.shape[0], k.dtype, k.get_device()
-    if v.shape[0] != tokens or v.dtype != dtype or dev != cache.index or \
-            (q is not None and (q.shape[0] != tokens or q.dtype != dtype)):
-        raise ValueError("q, k and v must have the same tokens and type, on the cache's device")
+    dev, dim, dtype = cache.index, cache.head_dim, k.dtype
+    act = _ACT.get(dtype)
+    if act is None or k.dim() != 3:
+        _refuse("k", k, dev)
+    tokens = k.shape[0]
+    shape = (tokens, cache.kv_heads, dim)
+    ks, vs = _rows("k", k, dev, dtype, shape), _rows("v", v, dev, dtype, shape)
+    pos = spec = qp = op = None
+    qs = os_ = heads = 0
     if (rope is None) != (positions is None):
         raise ValueError("positions and rope come together")
-    pos = spec = qp = op = None
-    qs = os_ = q_heads = 0
     if rope is not None:
-        pos, spec = _positions(positions, rope, tokens, dev), rope._ref
+        axes, spec = rope.axes, rope._ref
+        pos = _index("positions", positions, _int32, (tokens,) if axes == 1 and positions.dim() == 1 else (axes, tokens), dev)
     if q is not None:
-        qs, q_heads, qp = _rows("q", q, None, dim), q.shape[1], q.data_ptr()
-        out, os_ = _out(out, q)
+        if q.dim() != 3:
+            _refuse("q", q, dev)
+        heads = q.shape[1]
+        shape = (tokens, heads, dim)
+        qs, qp = _rows("q", q, dev, dtype, shape), q.data_ptr()
+        if out is None:
+            out, os_ = _empty_like(q, memory_format=_dense), heads * dim
+        else:
+            os_ = _rows("out", out, dev, dtype, shape)
         op = out.data_ptr()
-    st = (_lib or lib()).fp8w_rope_append(qp, k.data_ptr(), v.data_ptr(), _act_of(k), tokens, q_heads, qs, ks, vs, pos,
-                                          spec, _index("slots", slots, _torch.int64, (tokens,), dev), cache._ref, op, os_,
-                                          _raw_stream(dev))
+    st = _lib.fp8w_rope_append(qp, k.data_ptr(), v.data_ptr(), act, tokens, heads, qs, ks, vs, pos, spec,
+                               _index("slots", slots, _int64, (tokens,), dev), cache._ref, op, os_, _stream_of(dev))
     if st:
         _check(st)
     return None if q is None else out
@@ -488,19 +504,23 @@ def paged_attention(q, cache, block_table, lens, starts=None, scale=None, window
     lens, where the caller knows them on the host (0: not known)."""
     if _torch is None:
         _load_torch()
-    qs = _rows("q", q, None, cache.head_dim)
-    tokens, heads, dim = q.shape
-    dev = q.get_device()
-    if dev != cache.index or block_table.dim() != 2:
-        raise TypeError("q must be on the cache's device, and block_table a 2-D int32 tensor")
-    seqs, width = shape = block_table.shape
-    out, os_ = _out(out, q)
-    int32 = _torch.int32
-    st = (_lib or lib()).fp8w_paged_attention(
-        q.data_ptr(), _act_of(q), tokens, heads, qs, cache._ref, _index("block_table", block_table, int32, shape, dev), width,
-        _index("lens", lens, int32, (seqs,), dev),
-        None if starts is None else _index("starts", starts, int32, (seqs + 1,), dev), seqs,
-        dim ** -0.5 if scale is None else scale, window, max_new, max_len, out.data_ptr(), os_, _raw_stream(dev))
+    dev, dim, dtype = cache.index, cache.head_dim, q.dtype
+    act = _ACT.get(dtype)
+    if act is None or q.dim() != 3 or block_table.dim() != 2:
+        _refuse("q", q, dev)
+        raise ValueError("block_table must have two dimensions")
+    tokens, heads, d = q.shape
+    seqs, width = pages = block_table.shape
+    shape = (tokens, heads, dim)
+    qs = _rows("q", q, dev, dtype, shape)
+    if out is None:
+        out, os_ = _empty_like(q, memory_format=_dense), heads * dim
+    else:
+        os_ = _rows("out", out, dev, dtype, shape)
+    st = _lib.fp8w_paged_attention(
+        q.data_ptr(), act, tokens, heads, qs, cache._ref, _index("block_table", block_table, _int32, pages, dev), width,
+        _index("lens", lens, _int32, (seqs,), dev), None if starts is None else _index("starts", starts, _int32, (seqs + 1,), dev),
+        seqs, dim ** -0.5 if scale is None else scale, window, max_new, max_len, out.data_ptr(), os_, _stream_of(dev))
     if st:
         _check(st)
     return out
