@@ -472,11 +472,12 @@ FP8W_API fp8w_status fp8w_rope_append(const void *q, const void *k, const void *
  *   max_len      about the largest of lens; 0: table_width * page_size.  Guides
  *                how the work is split and nothing else.
  *   out          like q, with out_stride (output); it may not overlap q.
- * Scores, softmax and sums are fp32; the softmax weights are rounded to
- * act_dtype for the second product, as its other operand is; e4m3 scales
- * multiply scores and weights in fp32.  One rounding at the end.  Cached values
- * of positions below len are finite, in act_dtype's range; slots past them may
- * hold anything.  A table entry outside the cache, a len beyond the table or
+ * Scores, softmax and sums are fp32; the softmax weights are rounded to 16 bits
+ * for the second product: to act_dtype, or with codes and few rows to fp16.
+ * e4m3 scales multiply scores and weights in fp32.  One rounding at the end.
+ * Cached values of positions below len are finite, in act_dtype's range (a
+ * value that is not may reach other tokens of its sequence, none of another);
+ * slots past them may hold anything.  A table entry outside the cache, a len beyond the table or
  * starts out of order are recorded (fp8w_device_error): the tokens concerned
  * get unspecified finite values, and nothing outside the operands is read.
  * One launch and no workspace: where few rows meet a long cache, the CTAs of a
