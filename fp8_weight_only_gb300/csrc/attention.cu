@@ -56,6 +56,7 @@ constexpr int kFewRows = 16, kFewRowsCodes = 48;
 constexpr uint32_t kAttnTmemCols = 512;
 constexpr int kSoftmaxThreads = 512;   // sixteen warps
 constexpr int kLoadWarp = 16, kMmaWarp = 17, kConvWarp = 20;
+constexpr int kLoaders = 2;           // warps that load: kLoadWarp and the one after kMmaWarp
 constexpr int kBarSoftmax = 1;        // named barrier of the softmax warps; 2..9: of the pairs that share rows
 
 template <int DP, bool kFp8>
@@ -578,11 +579,11 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
     } else if (warp == kLoadWarp) {
         if (lane == 0) {
             for (int s = 0; s < kStages; ++s) {
-                mbar_init(full(s), kFp8 ? 4 * L::kConvGroups : 1);  // the converting warps, or the producer
+                mbar_init(full(s), kFp8 ? 4 * L::kConvGroups : kLoaders);  // the converting warps, or the producers
                 mbar_init(empty(s), 1);            // MMA commit
             }
             for (int s = 0; s < kRaw; ++s) {
-                mbar_init(rawfull(s), 1);
+                mbar_init(rawfull(s), kLoaders);
                 mbar_init(rawempty(s), 4 * L::kConvGroups);
             }
             for (int i = 0; i < 2; ++i) {
@@ -624,19 +625,25 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
 
     if (warp >= kLoadWarp && warp < kLoadWarp + 4) {
         reg_down<L::kRegsIssue>();
-        if (warp == kLoadWarp && n > 0) {
+        if (warp != kMmaWarp && warp < kLoadWarp + kLoaders + 1 && n > 0) {
             // ------------------------------------------------- producer --
             constexpr int kR = kFp8 ? kRaw : kStages;
+            // A tile is up to 16 copies of a page's 64-value sub-tile (a page's codes),
+            // one a lane, of two warps in turn: a warp alone issues them too slowly.
+            constexpr int kCopies = kFp8 ? 1 : static_cast<int>(L::kSubs);  // of a box
+            const int loader = warp == kLoadWarp ? 0 : 1;
             const int box = p.page_size < kKeys ? p.page_size : kKeys;
-            const int boxes = kKeys / box;
+            const int mine = lane * kLoaders + loader, sub = mine % kCopies, at = mine / kCopies * box;
+            const bool lives = at < kKeys;
+            const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, lives)) * box) * (kFp8 ? DP : 128);
             const int32_t* row = p.table + static_cast<int64_t>(w.seq) * p.table_width;
             // a lane's table entry is read two key tiles before its use and checked
             // there, so the table is not waited for
             auto wanted = [&](int j) {  // this lane's box of key tile j holds a position that some row sees
-                const int key = (w.t0 + j) * kKeys + lane * box;
-                return j < n && lane < boxes && key < w.end && key + box > w.first_key;
+                const int key = (w.t0 + j) * kKeys + at;
+                return j < n && lives && key < w.end && key + box > w.first_key;
             };
-            auto entry_of = [&](int j) { return wanted(j) ? __ldg(row + (((w.t0 + j) * kKeys + lane * box) >> p.log_page)) : 0; };
+            auto entry_of = [&](int j) { return wanted(j) ? __ldg(row + (((w.t0 + j) * kKeys + at) >> p.log_page)) : 0; };
             auto page_of = [&](int j, int entry) -> int {  // one past the cache (which reads as zeros) for no page
                 if (wanted(j) && entry >= 0 && entry < p.num_pages) return entry;
                 if (wanted(j)) atomicCAS(&g_attention_error, 0, 7000 + kErrIndex);
@@ -663,19 +670,14 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                     ok = false;
                     break;
                 }
-                if (lane == 0) mbar_arrive_expect_tx(fullb, kFp8 ? L::kRawBytes : L::kTileBytes);
+                if (lane == 0) mbar_arrive_expect_tx(fullb, bytes);
                 __syncwarp();
-                if (lane < boxes) {
+                if (lives) {
                     const CUtensorMap* map = is_k ? &map_k : &map_v;
-                    const int slot = ((w.t0 + j) * kKeys + lane * box) & (p.page_size - 1);
-                    if constexpr (kFp8) {
-                        tma_load_4d(sbase + L::kRawOff + s * L::kRawBytes + lane * box * DP, map, 0, slot, w.head, pg, fullb);
-                    } else {
-#pragma unroll
-                        for (uint32_t u = 0; u < L::kSubs; ++u)
-                            tma_load_4d(sbase + L::kRingOff + s * L::kTileBytes + u * (kKeys * 128) + lane * box * 128, map,
-                                        static_cast<int>(u) * 64, slot, w.head, pg, fullb);
-                    }
+                    const int slot = ((w.t0 + j) * kKeys + at) & (p.page_size - 1);
+                    const uint32_t dst = kFp8 ? L::kRawOff + s * L::kRawBytes + at * DP
+                                              : L::kRingOff + s * L::kTileBytes + sub * (kKeys * 128) + at * 128;
+                    tma_load_4d(sbase + dst, map, sub * 64, slot, w.head, pg, fullb);
                 }
                 __syncwarp();
             }

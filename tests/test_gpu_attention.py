@@ -140,6 +140,39 @@ def test_many_short_sequences():
     run(new, [n + (i * 13) % 90 for i, n in enumerate(new)], 1, 2, 64, 16)
 
 
+# Long prompts of many heads: a sequence's rows, 512 at a time, to a pair of
+# CTAs that share every key tile.
+
+@pytest.mark.parametrize("dtype,codes", [("bf16", False), ("f16", False), ("bf16", True), ("f16", True)])
+@pytest.mark.parametrize("page", [16, 64, 256])
+def test_long_prompts(page, dtype, codes):
+    # tiles of 512 rows full, by one row more, of a pipe's rows alone, of few
+    run([1100, 512, 513, 1700, 3, 0, 256], [1100, 2000, 513, 1701, 5, 40, 300], 26, 1, 128, page, dtype, codes)
+
+
+@pytest.mark.parametrize("dim", [80, 96, 112])
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("group", [3, 5])
+def test_long_prompts_of_other_heads(group, codes, dim):
+    run([399, 260, 129], [399, 1001, 640], 20, group, dim, 32, "bf16", codes, layout="tokens")
+
+
+@pytest.mark.parametrize("window", [1, 100, 128, 700])
+@pytest.mark.parametrize("codes", [False, True])
+def test_long_prompts_in_a_window(window, codes):
+    run([700, 600], [1500, 900], 32, 1, 128, 16, "bf16", codes, window=window)
+
+
+@pytest.mark.parametrize("dtype,codes", [("bf16", False), ("f16", False), ("bf16", True), ("f16", True)])
+def test_long_prompts_growing_maximum(dtype, codes):
+    run([600, 650], [1500, 1300], 26, 1, 128, 16, dtype, codes, growth=6.0, q_scale=2.0)
+
+
+def test_long_prompts_before_the_first_position():
+    _, _, out = run([600, 700], [100, 660], 26, 1, 128, 16)
+    assert not out[:500].any() and out[500:600].any() and not out[600:640].any() and out[640:].any()
+
+
 # ------------------------------------------------------------------- masks --
 
 @pytest.mark.parametrize("window", [1, 2, 100, 128, 129, 1000, 2 ** 40])
