@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
         if (lane == 0) {
             for (int s = 0; s < kStages; ++s) {
                 mbar_init(full(s), kFp8 ? 4 * L::kConvGroups : kLoaders);  // the converting warps, or the producers
-                mbar_init(empty(s), 1);            // MMA commit
+                mbar_init(empty(s), 1);  // MMA commit
             }
             for (int s = 0; s < kRaw; ++s) {
                 mbar_init(rawfull(s), kLoaders);
@@ -622,6 +622,13 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
     // ring position of key tile j and value tile j: K0 K1 V0 K2 V1 ...
     auto kpos = [&](int j) { return j == 0 ? 0 : 2 * j - 1; };
     auto vpos = [&](int j) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; };
+    // Release e is of positions 2 e - 1 and 2 e: key tile e and value tile e - 1,
+    // which one commit gives back.  Whether position i may be filled again: the
+    // last release lies less than kStages after the one that is waited for.
+    auto wait_free = [&](int i, const volatile int* abort_flag) {
+        const int e = (i - kStages + 1) / 2;
+        return i < kStages || mbar_wait_warp(empty(e % kStages), static_cast<uint32_t>((e / kStages) & 1), abort_flag);
+    };
 
     if (warp >= kLoadWarp && warp < kLoadWarp + 4) {
         reg_down<L::kRegsIssue>();
@@ -655,7 +662,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             for (; i < 2 * n; ++i) {
                 const int s = i % kR;
                 const bool is_k = i == 0 || (i < 2 * n - 1 && (i & 1));
-                const uint32_t fullb = kFp8 ? rawfull(s) : full(s), emptyb = kFp8 ? rawempty(s) : empty(s);
+                const uint32_t fullb = kFp8 ? rawfull(s) : full(s);
                 const int j = i == 0 ? 0 : is_k ? (i + 1) / 2 : i == 2 * n - 1 ? n - 1 : (i - 2) / 2;
                 if (is_k) {
                     e2 = entry_of(j + 2);
@@ -665,7 +672,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                     e1 = e2;
                 }
                 const int pg = is_k || j == n - 1 ? pk : pv;
-                if (!mbar_wait_warp(emptyb, static_cast<uint32_t>((i / kR) & 1) ^ 1u, abort_flag)) {
+                if (!(kFp8 ? mbar_wait_warp(rawempty(s), static_cast<uint32_t>((i / kR) & 1) ^ 1u, abort_flag) : wait_free(i, abort_flag))) {
                     if (lane == 0) attn_error(kErrWaitSlot, abort_flag);
                     ok = false;
                     break;
@@ -698,7 +705,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                 if (!ok && lane == 0) attn_error(kErrWaitTma, abort_flag);
                 tc_fence_after();
             };
-            auto release = [&](int i) { tc_commit_warp(empty(i % kStages)); };
+            auto release = [&](int e) { tc_commit_warp(empty(e % kStages)); };
             auto qk = [&](int pipe, int qtile, int i) {  // S_pipe = Q_qtile K^T
                 const uint32_t a = sbase + L::kQOff + qtile * L::kTileBytes;
                 const uint32_t b = sbase + L::kRingOff + (i % kStages) * L::kTileBytes;
@@ -707,7 +714,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                 __syncwarp();
             };
             int pv_n[2] = {0, 0};  // products P V of each pipe
-            auto pv = [&](int pipe, int i) {  // O_pipe (+)= P_pipe V
+            auto pv = [&](int pipe, int i, bool last) {  // O_pipe (+)= P_pipe V
                 if (!mbar_wait_warp(pfull(pipe), static_cast<uint32_t>(pv_n[pipe] & 1), abort_flag)) {
                     if (lane == 0) attn_error(kErrWaitMma, abort_flag);
                     ok = false;
@@ -716,7 +723,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                 tc_fence_after();
                 const uint32_t b = sbase + L::kRingOff + (i % kStages) * L::kTileBytes;
                 mma_values(tmem + 2 * kKeys + pipe * DP, tmem + pipe * kKeys, b, idesc_o, pv_n[pipe] > 0);
-                tc_commit_warp(ofull(pipe));
+                if (last) tc_commit_warp(ofull(pipe));
                 __syncwarp();
                 ++pv_n[pipe];
             };
@@ -742,25 +749,24 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                 if (ok) {
                     if (w.cnt0 > 0) qk(0, 0, kpos(0));
                     qk(1, 1, kpos(0));
-                    release(kpos(0));
+                    release(0);
                 }
                 for (int j = 0; j < n && ok; ++j) {
                     wait_full(vpos(j));
                     if (!ok) break;
                     clear_tail(j);
                     if (j < w.cnt0) {
-                        pv(0, vpos(j));
+                        pv(0, vpos(j), j == w.cnt0 - 1);
                         if (!ok) break;
                     }
                     if (j + 1 < n) wait_full(kpos(j + 1));
                     if (!ok) break;
                     if (j + 1 < w.cnt0) qk(0, 0, kpos(j + 1));
-                    pv(1, vpos(j));
+                    pv(1, vpos(j), j == n - 1);
                     if (!ok) break;
-                    release(vpos(j));
                     if (j + 1 < n) {
                         qk(1, 1, kpos(j + 1));
-                        release(kpos(j + 1));
+                        release(j + 1);
                     }
                 }
             } else {
@@ -768,20 +774,19 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                     wait_full(kpos(j));
                     if (!ok) break;
                     qk(j, 0, kpos(j));
-                    release(kpos(j));
+                    if (j == 0) release(0);
                 }
                 for (int j = 0; j < n && ok; ++j) {
                     wait_full(vpos(j));
                     if (!ok) break;
                     clear_tail(j);
-                    pv(j & 1, vpos(j));
+                    pv(j & 1, vpos(j), j >= n - 2);
                     if (!ok) break;
-                    release(vpos(j));
+                    release(j + 1);
                     if (j + 2 < n) {
                         wait_full(kpos(j + 2));
                         if (!ok) break;
                         qk(j & 1, 0, kpos(j + 2));
-                        release(kpos(j + 2));
                     }
                 }
             }
@@ -842,7 +847,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(rawempty(s));
-                if (!mbar_wait_warp(empty(d), static_cast<uint32_t>((i / kStages) & 1) ^ 1u, abort_flag)) {
+                if (!wait_free(i, abort_flag)) {
                     if (lane == 0) attn_error(kErrWaitMma, abort_flag);
                     break;
                 }
@@ -1046,13 +1051,8 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                     l *= alpha;
                 }
                 if (done == 0) continue;
-                // O is at rest once the last product has been added
-                if (!mbar_wait_warp(ofull(pipe), static_cast<uint32_t>((done - 1) & 1), abort_flag)) {
-                    if (lane == 0) attn_error(kErrWaitMma, abort_flag);
-                    ok = false;
-                    return;
-                }
-                tc_fence_after();
+                // O is at rest: the product of the tile before was issued before
+                // these scores, whose commit stands for it too
 #pragma unroll 1
                 for (int b = 0; b < DP / 2; b += 16) {
                     uint32_t v[16];
@@ -1107,7 +1107,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
         }
         // --------------------------------------------------- the result --
         if (ok && done > 0) {
-            ok = mbar_wait_warp(ofull(pipe), static_cast<uint32_t>((done - 1) & 1), abort_flag);
+            ok = mbar_wait_warp(ofull(pipe), 0, abort_flag);
             if (!ok && lane == 0) attn_error(kErrWaitMma, abort_flag);
             tc_fence_after();
         }
