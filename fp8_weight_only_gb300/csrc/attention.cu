@@ -77,8 +77,8 @@ struct AttnSmem {
     static constexpr uint32_t kMlOff = kScaleOff + (kFp8 ? kScaleSlots * 2 * kKeys * 4 : 0);
     static constexpr uint32_t kJoinedOff = kMlOff + kRows * 8;   // (m, l) of the CTA's rows, for the cluster
     static constexpr uint32_t kBarOff = kJoinedOff + kRows * 8;
-    // full, empty [kStages] | rawfull, rawempty [kRaw] | sfull, pfull, ofull [2] | qfull | joinfull, joinfree | drain
-    static constexpr uint32_t kNumBars = 2 * kStages + 2 * kRaw + 6 + 1 + 2 + 1;
+    // full, empty [kStages] | rawfull, rawempty [kRaw] | sfull, pfull, ofull [2] | qfull | joinfull, joinfree | drain | tail
+    static constexpr uint32_t kNumBars = 2 * kStages + 2 * kRaw + 6 + 1 + 2 + 1 + 1;
     static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;
     static constexpr uint32_t kBytes = kMiscOff + 16;
     static_assert(kBytes <= 227 * 1024 && kMlOff % 1024 == 0, "shared memory");
@@ -175,72 +175,53 @@ __device__ __forceinline__ uint64_t smem_desc_sw128_nmajor(uint32_t addr) {
 }
 constexpr uint32_t kIdescBNMajor = 1u << 16;
 
-// Eight or fewer products in a row, issued by one elected lane.  One election,
-// and descriptors that advance by an add: sixteen products a key tile have to
-// be issued beside eight busy softmax warps, and with a descriptor built for
-// each the tensor cores waited for them.
-// D[tmem] = (or +=) sum over k of A[smem] B[smem], a 16-value step of a 64-value
-// sub-tile being 32 bytes and a sub-tile 128 rows of 128 bytes.
-template <int kSteps>
-__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
-    const uint64_t da = smem_desc_sw128_kmajor(a), db = smem_desc_sw128_kmajor(b);
-    const uint32_t a_lo = static_cast<uint32_t>(da), b_lo = static_cast<uint32_t>(db), hi = static_cast<uint32_t>(da >> 32);
-    static_assert(kSteps == 4 || kSteps == 8, "64 or 128 values");
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// Products in a row, issued by one thread.  Sixteen a key tile have to be issued
+// beside sixteen busy softmax warps, so descriptors advance by an add.
+// D[tmem] = (or +=) sum of A[smem] B[smem] over the 64 values of a sub-tile, a
+// 16-value step being 32 bytes.
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool accumulate) {
     asm volatile(
-        "{\n\t.reg .pred e, f, t;\n\t.reg .b64 x, y;\n\t.reg .b32 u, v;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.b32 f, 0, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "{\n\t.reg .pred p, t;\n\t.reg .b64 x, y;\n\t.reg .b32 u, v;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
         "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, f;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t"
         "add.u32 u, %1, 2;\n\tadd.u32 v, %2, 2;\n\tmov.b64 x, {u, %3};\n\tmov.b64 y, {v, %3};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t"
         "add.u32 u, %1, 4;\n\tadd.u32 v, %2, 4;\n\tmov.b64 x, {u, %3};\n\tmov.b64 y, {v, %3};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t"
         "add.u32 u, %1, 6;\n\tadd.u32 v, %2, 6;\n\tmov.b64 x, {u, %3};\n\tmov.b64 y, {v, %3};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t}" ::"r"(d),
-        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate ? 1u : 0u)
         : "memory");
-    if constexpr (kSteps == 8)
-        asm volatile(
-            "{\n\t.reg .pred e, t;\n\t.reg .b64 x, y;\n\t.reg .b32 u, v;\n\t"
-            "elect.sync _|e, 0xffffffff;\n\t"
-            "setp.eq.b32 t, 0, 0;\n\t"
-            "add.u32 u, %1, 1024;\n\tadd.u32 v, %2, 1024;\n\tmov.b64 x, {u, %3};\n\tmov.b64 y, {v, %3};\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t"
-            "add.u32 u, %1, 1026;\n\tadd.u32 v, %2, 1026;\n\tmov.b64 x, {u, %3};\n\tmov.b64 y, {v, %3};\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t"
-            "add.u32 u, %1, 1028;\n\tadd.u32 v, %2, 1028;\n\tmov.b64 x, {u, %3};\n\tmov.b64 y, {v, %3};\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t"
-            "add.u32 u, %1, 1030;\n\tadd.u32 v, %2, 1030;\n\tmov.b64 x, {u, %3};\n\tmov.b64 y, {v, %3};\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t}" ::"r"(d),
-            "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc)
-            : "memory");
 }
 // D[tmem] (+)= A[tmem] B[smem] over 128 keys: 8 columns of A and 16 key rows
 // (2048 bytes) a step.
-__device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
-    const uint64_t db = smem_desc_sw128_nmajor(b);
-    const uint32_t b_lo = static_cast<uint32_t>(db), hi = static_cast<uint32_t>(db >> 32);
+__device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool accumulate) {
     asm volatile(
-        "{\n\t.reg .pred e, p, t;\n\t.reg .b64 y;\n\t.reg .b32 u, v;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
+        "{\n\t.reg .pred p, t;\n\t.reg .b64 y;\n\t.reg .b32 u, v;\n\t"
         "setp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
         "mov.b64 y, {%2, %3};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t"
         "add.u32 u, %1, 8;\n\tadd.u32 v, %2, 128;\n\tmov.b64 y, {v, %3};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t"
         "add.u32 u, %1, 16;\n\tadd.u32 v, %2, 256;\n\tmov.b64 y, {v, %3};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t"
         "add.u32 u, %1, 24;\n\tadd.u32 v, %2, 384;\n\tmov.b64 y, {v, %3};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t"
         "add.u32 u, %1, 32;\n\tadd.u32 v, %2, 512;\n\tmov.b64 y, {v, %3};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t"
         "add.u32 u, %1, 40;\n\tadd.u32 v, %2, 640;\n\tmov.b64 y, {v, %3};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t"
         "add.u32 u, %1, 48;\n\tadd.u32 v, %2, 768;\n\tmov.b64 y, {v, %3};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t"
         "add.u32 u, %1, 56;\n\tadd.u32 v, %2, 896;\n\tmov.b64 y, {v, %3};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t}" ::"r"(d),
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t}" ::"r"(d),
         "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate ? 1u : 0u)
         : "memory");
 }
@@ -567,7 +548,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
     auto pfull = [&](int i) { return bar0 + 8u * (kB + 2 + i); };
     auto ofull = [&](int i) { return bar0 + 8u * (kB + 4 + i); };
     const uint32_t qfull = bar0 + 8u * (kB + 6), joinfull = bar0 + 8u * (kB + 7), joinfree = bar0 + 8u * (kB + 8),
-                   drain = bar0 + 8u * (kB + 9);
+                   drain = bar0 + 8u * (kB + 9), tail = bar0 + 8u * (kB + 10);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -595,6 +576,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             mbar_init(joinfull, static_cast<uint32_t>(p.cl));
             mbar_init(joinfree, static_cast<uint32_t>(p.cl));
             mbar_init(drain, 1);
+            mbar_init(tail, 1);
             *abort_flag = (sbase & 1023u) ? 1 : 0;  // the swizzled tiles need this alignment
             tma_prefetch_desc(&map_k);
             tma_prefetch_desc(&map_v);
@@ -619,9 +601,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                                                 blockIdx.x == 0 && warp == 0);
     if (!have) w = Work{};
     const int n = w.cnt;
-    // ring position of key tile j and value tile j: K0 K1 V0 K2 V1 ...
-    auto kpos = [&](int j) { return j == 0 ? 0 : 2 * j - 1; };
-    auto vpos = [&](int j) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; };
+    // Ring positions: K0 K1 V0 K2 V1 .. K(n-1) V(n-2) V(n-1).
     // Release e is of positions 2 e - 1 and 2 e: key tile e and value tile e - 1,
     // which one commit gives back.  Whether position i may be filled again: the
     // last release lies less than kStages after the one that is waited for.
@@ -688,6 +668,26 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                 }
                 __syncwarp();
             }
+            // Slots past the sequence's end hold anything, a NaN perhaps, and
+            // 0 * NaN is no zero: those rows of the last value tile are cleared
+            // (pages past the end were never read; codes are cleared as they convert)
+            const int keep = w.end - (w.t0 + n - 1) * kKeys;
+            if (!kFp8 && ok && loader == 0 && keep < kKeys) {
+                const int s = (2 * n - 1) % kStages;
+                ok = mbar_wait_warp(full(s), static_cast<uint32_t>(((2 * n - 1) / kStages) & 1), abort_flag);
+                if (ok) {
+                    const uint32_t b = sbase + L::kRingOff + s * L::kTileBytes;
+                    for (int u = keep * 8 + lane; u < kKeys * 8; u += 32) {
+#pragma unroll
+                        for (uint32_t v = 0; v < L::kSubs; ++v) sts128(b + v * (kKeys * 128) + u * 16, 0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(tail);
+                } else if (lane == 0) {
+                    attn_error(kErrWaitTma, abort_flag);
+                }
+            }
             if (!ok || *abort_flag) {
                 // let the copies still in flight land before the CTA exits
                 for (int c = i > kR ? i - kR : 0; c < i; ++c)
@@ -696,103 +696,97 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             }
         } else if (warp == kMmaWarp && n > 0) {
             // ------------------------------------------------ MMA issue --
-            constexpr uint32_t idesc_s = idesc_f16(kBf16, kKeys);
-            constexpr uint32_t idesc_o = idesc_f16(kBf16, DP) | kIdescBNMajor;
-            bool ok = true;
-            auto wait_full = [&](int i) {
-                if (!ok) return;
-                ok = mbar_wait_warp(full(i % kStages), static_cast<uint32_t>((i / kStages) & 1), abort_flag);
-                if (!ok && lane == 0) attn_error(kErrWaitTma, abort_flag);
-                tc_fence_after();
-            };
-            auto release = [&](int e) { tc_commit_warp(empty(e % kStages)); };
-            auto qk = [&](int pipe, int qtile, int i) {  // S_pipe = Q_qtile K^T
-                const uint32_t a = sbase + L::kQOff + qtile * L::kTileBytes;
-                const uint32_t b = sbase + L::kRingOff + (i % kStages) * L::kTileBytes;
-                mma_scores<DP / 16>(tmem + pipe * kKeys, a, b, idesc_s);
-                tc_commit_warp(sfull(pipe));
-                __syncwarp();
-            };
-            int pv_n[2] = {0, 0};  // products P V of each pipe
-            auto pv = [&](int pipe, int i, bool last) {  // O_pipe (+)= P_pipe V
-                if (!mbar_wait_warp(pfull(pipe), static_cast<uint32_t>(pv_n[pipe] & 1), abort_flag)) {
-                    if (lane == 0) attn_error(kErrWaitMma, abort_flag);
-                    ok = false;
-                    return;
-                }
-                tc_fence_after();
-                const uint32_t b = sbase + L::kRingOff + (i % kStages) * L::kTileBytes;
-                mma_values(tmem + 2 * kKeys + pipe * DP, tmem + pipe * kKeys, b, idesc_o, pv_n[pipe] > 0);
-                if (last) tc_commit_warp(ofull(pipe));
-                __syncwarp();
-                ++pv_n[pipe];
-            };
-            // Slots past the sequence's end hold anything, a NaN perhaps, and
-            // 0 * NaN is no zero: those rows of the last value tile are cleared
-            // (pages past the end were never read; codes are cleared as they convert)
-            auto clear_tail = [&](int j) {
-                const int keep = w.end - (w.t0 + j) * kKeys;
-                if (kFp8 || keep >= kKeys) return;
-                const uint32_t b = sbase + L::kRingOff + (vpos(j) % kStages) * L::kTileBytes;
-                for (int u = keep * 8 + lane; u < kKeys * 8; u += 32) {
+            // One thread, and no more instructions than it needs: it shares its
+            // scheduler with four softmax warps, and the tensor cores wait for it
+            // (the loop of a whole warp with an election a product took 447 us for
+            // 8192 tokens).
+            if (elect_one()) {
+                constexpr uint32_t idesc_s = idesc_f16(kBf16, kKeys);
+                constexpr uint32_t idesc_o = idesc_f16(kBf16, DP) | kIdescBNMajor;
+                const uint64_t qd = smem_desc_sw128_kmajor(sbase + L::kQOff), kd = smem_desc_sw128_kmajor(sbase + L::kRingOff),
+                               vd = smem_desc_sw128_nmajor(sbase + L::kRingOff);
+                const uint32_t q_lo = static_cast<uint32_t>(qd), k_lo = static_cast<uint32_t>(kd), v_lo = static_cast<uint32_t>(vd);
+                const uint32_t k_hi = static_cast<uint32_t>(kd >> 32), v_hi = static_cast<uint32_t>(vd >> 32);
+                bool ok = true;
+                auto wait = [&](uint32_t bar, uint32_t parity, int code) {
+                    ok = mbar_wait(bar, parity, abort_flag);
+                    if (!ok) attn_error(code, abort_flag);
+                    return ok;
+                };
+                auto qk = [&](int pipe, int qtile, uint32_t stage) {  // S_pipe = Q_qtile K^T
 #pragma unroll
-                    for (uint32_t sub = 0; sub < L::kSubs; ++sub) sts128(b + sub * (kKeys * 128) + u * 16, 0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-            };
-            ok = mbar_wait_warp(qfull, 0, abort_flag);
-            if (!ok && lane == 0) attn_error(kErrWaitDequant, abort_flag);
-            tc_fence_after();
-            if (w.two) {
-                wait_full(kpos(0));
-                if (ok) {
-                    if (w.cnt0 > 0) qk(0, 0, kpos(0));
-                    qk(1, 1, kpos(0));
-                    release(0);
-                }
-                for (int j = 0; j < n && ok; ++j) {
-                    wait_full(vpos(j));
-                    if (!ok) break;
-                    clear_tail(j);
-                    if (j < w.cnt0) {
-                        pv(0, vpos(j), j == w.cnt0 - 1);
-                        if (!ok) break;
+                    for (uint32_t u = 0; u < L::kSubs; ++u)
+                        mma_scores(tmem + pipe * kKeys, q_lo + qtile * (L::kTileBytes >> 4) + u * (kRows * 128 >> 4),
+                                   k_lo + stage * (L::kTileBytes >> 4) + u * (kKeys * 128 >> 4), k_hi, idesc_s, u > 0);
+                    tc_commit(sfull(pipe));
+                };
+                auto pv = [&](int pipe, uint32_t done, uint32_t stage, bool last) {  // O_pipe (+)= P_pipe V, the pipe's product number `done`
+                    if (!wait(pfull(pipe), done & 1, kErrWaitMma)) return false;
+                    tc_fence_after();
+                    mma_values(tmem + 2 * kKeys + pipe * DP, tmem + pipe * kKeys, v_lo + stage * (L::kTileBytes >> 4), v_hi, idesc_o,
+                               done > 0);
+                    if (last) tc_commit(ofull(pipe));
+                    return true;
+                };
+                // the last value tile: a producer clears what lies past the end
+                auto wait_tail = [&] { return kFp8 || w.end - (w.t0 + n - 1) * kKeys >= kKeys || wait(tail, 0, kErrWaitTma); };
+                // ring stage and phase of position 2 j + 1, and of the one behind it
+                uint32_t a = 1, a_ph = 0;
+                auto behind = [&](uint32_t& stage, uint32_t& phase) { stage = a + 1 == kStages ? 0 : a + 1, phase = a_ph ^ (a + 1 == kStages); };
+                auto advance = [&] {
+                    a += 2;
+                    if (a >= kStages) a -= kStages, a_ph ^= 1;
+                };
+                ok = wait(qfull, 0, kErrWaitDequant) && wait(full(0), 0, kErrWaitTma);
+                if (ok) tc_fence_after();
+                if (ok && w.two) {
+                    if (w.cnt0 > 0) qk(0, 0, 0);
+                    qk(1, 1, 0);
+                    tc_commit(empty(0));
+                    uint32_t free_at = 1;  // barrier of release j + 1
+                    for (int j = 0; j < n; ++j, advance()) {
+                        const bool last = j == n - 1;
+                        uint32_t b, b_ph;
+                        behind(b, b_ph);
+                        if (last) b = a, b_ph = a_ph;  // no key tile between
+                        if (!wait(full(b), b_ph, kErrWaitTma) || (last && !wait_tail())) break;
+                        if (j < w.cnt0 && !pv(0, j, b, j == w.cnt0 - 1)) break;
+                        if (!last) {
+                            if (!wait(full(a), a_ph, kErrWaitTma)) break;
+                            if (j + 1 < w.cnt0) qk(0, 0, a);
+                        }
+                        if (!pv(1, j, b, last)) break;
+                        if (!last) {
+                            qk(1, 1, a);
+                            tc_commit(empty(free_at));
+                            free_at = free_at + 1 == kStages ? 0 : free_at + 1;
+                        }
                     }
-                    if (j + 1 < n) wait_full(kpos(j + 1));
-                    if (!ok) break;
-                    if (j + 1 < w.cnt0) qk(0, 0, kpos(j + 1));
-                    pv(1, vpos(j), j == n - 1);
-                    if (!ok) break;
-                    if (j + 1 < n) {
-                        qk(1, 1, kpos(j + 1));
-                        release(j + 1);
+                } else if (ok) {
+                    qk(0, 0, 0);
+                    tc_commit(empty(0));
+                    if (n > 1 && wait(full(1), 0, kErrWaitTma)) qk(1, 0, 1);
+                    uint32_t free_at = 1;
+                    for (int j = 0; j < n && ok; ++j) {
+                        const bool last = j == n - 1;
+                        uint32_t b, b_ph;
+                        behind(b, b_ph);
+                        if (last) b = a, b_ph = a_ph;
+                        if (!wait(full(b), b_ph, kErrWaitTma) || (last && !wait_tail())) break;
+                        if (!pv(j & 1, j >> 1, b, j >= n - 2)) break;
+                        tc_commit(empty(free_at));
+                        free_at = free_at + 1 == kStages ? 0 : free_at + 1;
+                        advance();
+                        if (j + 2 < n) {
+                            if (!wait(full(a), a_ph, kErrWaitTma)) break;
+                            qk(j & 1, 0, a);
+                        }
                     }
                 }
-            } else {
-                for (int j = 0; j < 2 && j < n; ++j) {
-                    wait_full(kpos(j));
-                    if (!ok) break;
-                    qk(j, 0, kpos(j));
-                    if (j == 0) release(0);
-                }
-                for (int j = 0; j < n && ok; ++j) {
-                    wait_full(vpos(j));
-                    if (!ok) break;
-                    clear_tail(j);
-                    pv(j & 1, vpos(j), j >= n - 2);
-                    if (!ok) break;
-                    release(j + 1);
-                    if (j + 2 < n) {
-                        wait_full(kpos(j + 2));
-                        if (!ok) break;
-                        qk(j & 1, 0, kpos(j + 2));
-                    }
-                }
+                // every MMA issued above completes before TMEM is released
+                tc_commit(drain);
+                if (!mbar_wait_drain(drain, 0)) atomicCAS(&g_attention_error, 0, 7000 + kErrWaitDrain);
             }
-            // every MMA issued above completes before TMEM is released
-            tc_commit_warp(drain);
-            if (!mbar_wait_drain(drain, 0) && lane == 0) atomicCAS(&g_attention_error, 0, 7000 + kErrWaitDrain);
             __syncwarp();
         }
     } else if (kFp8 && warp >= kConvWarp) {
