@@ -56,7 +56,6 @@ constexpr int kFewRows = 16, kFewRowsCodes = 48;
 constexpr uint32_t kAttnTmemCols = 512;
 constexpr int kSoftmaxThreads = 512;   // sixteen warps
 constexpr int kLoadWarp = 16, kMmaWarp = 17, kConvWarp = 20;
-constexpr int kLoaders = 2;           // warps that load: kLoadWarp and the one after kMmaWarp
 constexpr int kBarSoftmax = 1;        // named barrier of the softmax warps; 2..9: of the pairs that share rows
 
 template <int DP, bool kFp8>
@@ -69,6 +68,7 @@ struct AttnSmem {
     // Key tile m is converted once ring position 2 m - 1 - kStages is free.  With
     // 3 stages that is value tile m - 3, so the softmax is done with tile m - 3;
     // with 6 it is key tile m - 3, multiplied after value tile m - 5 was.
+    static constexpr int kLoaders = kFp8 ? 2 : 3;                // warps that load: kLoadWarp and those after kMmaWarp
     static constexpr int kScaleSlots = DP == 128 ? 4 : 8;
     static constexpr uint32_t kQOff = 0;                         // two row tiles; later a 128 x DP fp32 partial
     static constexpr uint32_t kRingOff = 2 * kTileBytes;
@@ -82,14 +82,13 @@ struct AttnSmem {
     static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;
     static constexpr uint32_t kBytes = kMiscOff + 16;
     static_assert(kBytes <= 227 * 1024 && kMlOff % 1024 == 0, "shared memory");
-    static constexpr int kConvGroups = kFp8 ? 1 : 0;             // converting warpgroups
-    static constexpr int kThreads = kSoftmaxThreads + 128 + 128 * kConvGroups;
+    static constexpr int kThreads = kSoftmaxThreads + 128 + (kFp8 ? 128 : 0);
     // registers a thread at launch and after the split
     static constexpr int kRegs = 65536 / kThreads / 8 * 8;
     static constexpr int kRegsSoftmax = kFp8 ? 88 : 104;
     static constexpr int kRegsIssue = kFp8 ? 56 : 64;
     static constexpr int kRegsConv = 72;
-    static_assert(kSoftmaxThreads * kRegsSoftmax + 128 * kRegsIssue + 128 * kConvGroups * kRegsConv <= kThreads * kRegs, "register split");
+    static_assert(kSoftmaxThreads * kRegsSoftmax + 128 * kRegsIssue + (kFp8 ? 128 * kRegsConv : 0) <= kThreads * kRegs, "register split");
 };
 
 __device__ __forceinline__ void attn_error(int code, volatile int* abort_flag) {
@@ -560,12 +559,12 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
     } else if (warp == kLoadWarp) {
         if (lane == 0) {
             for (int s = 0; s < kStages; ++s) {
-                mbar_init(full(s), kFp8 ? 4 * L::kConvGroups : kLoaders);  // the converting warps, or the producers
+                mbar_init(full(s), kFp8 ? 4 : L::kLoaders);  // the converting warps, or the producers
                 mbar_init(empty(s), 1);  // MMA commit
             }
             for (int s = 0; s < kRaw; ++s) {
-                mbar_init(rawfull(s), kLoaders);
-                mbar_init(rawempty(s), 4 * L::kConvGroups);
+                mbar_init(rawfull(s), L::kLoaders);
+                mbar_init(rawempty(s), 4);
             }
             for (int i = 0; i < 2; ++i) {
                 mbar_init(sfull(i), 1);
@@ -603,77 +602,81 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
     const int n = w.cnt;
     // Ring positions: K0 K1 V0 K2 V1 .. K(n-1) V(n-2) V(n-1).
     // Release e is of positions 2 e - 1 and 2 e: key tile e and value tile e - 1,
-    // which one commit gives back.  Whether position i may be filled again: the
-    // last release lies less than kStages after the one that is waited for.
-    auto wait_free = [&](int i, const volatile int* abort_flag) {
-        const int e = (i - kStages + 1) / 2;
-        return i < kStages || mbar_wait_warp(empty(e % kStages), static_cast<uint32_t>((e / kStages) & 1), abort_flag);
-    };
+    // which one commit gives back; position i may be filled again after release
+    // (i - kStages + 1) / 2.  Those who fill wait for each release in turn; the last
+    // one lies less than kStages after the one that is waited for.
 
     if (warp >= kLoadWarp && warp < kLoadWarp + 4) {
         reg_down<L::kRegsIssue>();
-        if (warp != kMmaWarp && warp < kLoadWarp + kLoaders + 1 && n > 0) {
+        if (warp != kMmaWarp && warp < kLoadWarp + L::kLoaders + 1 && n > 0) {
             // ------------------------------------------------- producer --
             constexpr int kR = kFp8 ? kRaw : kStages;
             // A tile is up to 16 copies of a page's 64-value sub-tile (a page's codes),
-            // one a lane, of two warps in turn: a warp alone issues them too slowly.
+            // one a lane, of three warps in turn: a warp alone issues them too slowly,
+            // and each instruction here waits behind the softmax warps' (8192 tokens on
+            // 16-slot pages: 543 us with one warp, 434 with two, 415 with three).
             constexpr int kCopies = kFp8 ? 1 : static_cast<int>(L::kSubs);  // of a box
-            const int loader = warp == kLoadWarp ? 0 : 1;
+            const int loader = warp == kLoadWarp ? 0 : warp - kMmaWarp;
             const int box = p.page_size < kKeys ? p.page_size : kKeys;
-            const int mine = lane * kLoaders + loader, sub = mine % kCopies, at = mine / kCopies * box;
+            const int mine = lane * L::kLoaders + loader, sub = mine % kCopies, at = mine / kCopies * box;
             const bool lives = at < kKeys;
             const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, lives)) * box) * (kFp8 ? DP : 128);
+            const uint32_t dst0 = sbase + (kFp8 ? L::kRawOff + at * DP : L::kRingOff + sub * (kKeys * 128) + at * 128);
             const int32_t* row = p.table + static_cast<int64_t>(w.seq) * p.table_width;
-            // a lane's table entry is read two key tiles before its use and checked
-            // there, so the table is not waited for
-            auto wanted = [&](int j) {  // this lane's box of key tile j holds a position that some row sees
-                const int key = (w.t0 + j) * kKeys + at;
+            // A lane's table entry is read two key tiles before its use and checked
+            // there, so the table is not waited for.  One past the cache (which reads as
+            // zeros) stands for no page, and for positions that no row sees.
+            const int none = static_cast<int>(p.num_pages), key0 = w.t0 * kKeys + at;
+            auto wanted = [&](int j) {
+                const int key = key0 + j * kKeys;
                 return j < n && lives && key < w.end && key + box > w.first_key;
             };
-            auto entry_of = [&](int j) { return wanted(j) ? __ldg(row + (((w.t0 + j) * kKeys + at) >> p.log_page)) : 0; };
-            auto page_of = [&](int j, int entry) -> int {  // one past the cache (which reads as zeros) for no page
-                if (wanted(j) && entry >= 0 && entry < p.num_pages) return entry;
+            auto entry_of = [&](int j) { return wanted(j) ? __ldg(row + ((key0 + j * kKeys) >> p.log_page)) : none; };
+            auto page_of = [&](int j, int entry) {
+                if (static_cast<uint32_t>(entry) < static_cast<uint32_t>(none)) return entry;
                 if (wanted(j)) atomicCAS(&g_attention_error, 0, 7000 + kErrIndex);
-                return static_cast<int>(p.num_pages);
+                return none;
             };
-            int e0 = entry_of(0), e1 = entry_of(1), e2 = 0, pk = 0, pv = 0;
+            uint32_t s = 0, phase = 0;               // stage of the position, use of it
+            uint32_t freed = 0, fs = 0, fphase = 0;  // releases waited for; the next one's barrier and phase
+            int e0 = entry_of(0), e1 = entry_of(1), now = none, before = none;  // now: the newest key tile's page
             bool ok = true;
             int i = 0;
-            for (; i < 2 * n; ++i) {
-                const int s = i % kR;
+#pragma unroll 1
+            for (; i < 2 * n; ++i) {  // one body: a small loop fetches its instructions faster
                 const bool is_k = i == 0 || (i < 2 * n - 1 && (i & 1));
-                const uint32_t fullb = kFp8 ? rawfull(s) : full(s);
-                const int j = i == 0 ? 0 : is_k ? (i + 1) / 2 : i == 2 * n - 1 ? n - 1 : (i - 2) / 2;
+                const int j = (i + (is_k ? 1 : i == 2 * n - 1 ? -1 : -2)) / 2;
                 if (is_k) {
-                    e2 = entry_of(j + 2);
-                    pv = pk;
-                    pk = page_of(j, e0);
+                    before = now;
+                    now = page_of(j, e0);
                     e0 = e1;
-                    e1 = e2;
+                    e1 = entry_of(j + 2);
                 }
-                const int pg = is_k || j == n - 1 ? pk : pv;
-                if (!(kFp8 ? mbar_wait_warp(rawempty(s), static_cast<uint32_t>((i / kR) & 1) ^ 1u, abort_flag) : wait_free(i, abort_flag))) {
+                if constexpr (kFp8) {
+                    ok = mbar_wait_warp(rawempty(s), phase ^ 1u, abort_flag);
+                } else if (i >= kStages && i + 1 >= kStages + 2 * static_cast<int>(freed)) {
+                    ok = mbar_wait_warp(empty(fs), fphase, abort_flag);
+                    ++freed;
+                    if (++fs == kStages) fs = 0, fphase ^= 1u;
+                }
+                if (!ok) {
                     if (lane == 0) attn_error(kErrWaitSlot, abort_flag);
-                    ok = false;
                     break;
                 }
-                if (lane == 0) mbar_arrive_expect_tx(fullb, bytes);
+                const uint32_t bar = kFp8 ? rawfull(s) : full(s);
+                if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                if (lives)
+                    tma_load_4d(dst0 + s * (kFp8 ? L::kRawBytes : L::kTileBytes), is_k ? &map_k : &map_v, sub * 64,
+                                (key0 + j * kKeys) & (p.page_size - 1), w.head, is_k || j == n - 1 ? now : before, bar);
                 __syncwarp();
-                if (lives) {
-                    const CUtensorMap* map = is_k ? &map_k : &map_v;
-                    const int slot = ((w.t0 + j) * kKeys + at) & (p.page_size - 1);
-                    const uint32_t dst = kFp8 ? L::kRawOff + s * L::kRawBytes + at * DP
-                                              : L::kRingOff + s * L::kTileBytes + sub * (kKeys * 128) + at * 128;
-                    tma_load_4d(sbase + dst, map, sub * 64, slot, w.head, pg, fullb);
-                }
-                __syncwarp();
+                if (++s == kR) s = 0, phase ^= 1u;
             }
             // Slots past the sequence's end hold anything, a NaN perhaps, and
             // 0 * NaN is no zero: those rows of the last value tile are cleared
             // (pages past the end were never read; codes are cleared as they convert)
             const int keep = w.end - (w.t0 + n - 1) * kKeys;
             if (!kFp8 && ok && loader == 0 && keep < kKeys) {
-                const int s = (2 * n - 1) % kStages;
+                const int s = (2 * n - 1) % kStages;  // the stage filled last
                 ok = mbar_wait_warp(full(s), static_cast<uint32_t>(((2 * n - 1) / kStages) & 1), abort_flag);
                 if (ok) {
                     const uint32_t b = sbase + L::kRingOff + s * L::kTileBytes;
@@ -793,11 +796,9 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
         // --------------------------------------- codes to operand tiles --
         if constexpr (kFp8) {
             reg_down<L::kRegsConv>();
-            // One key a thread; with two warpgroups each converts half of the row.
-            // (Tiles in turn would need an even number of stages: a warpgroup that
-            // runs ahead on a stage of the other's could take one phase for another.)
-            constexpr int kGroups = L::kConvGroups, kChunks = DP / 16 / kGroups;  // 16-code chunks a thread
-            const int h = (warp - kConvWarp) >> 2;
+            // One key a thread.  (Two warpgroups, half a key a thread each: 769 us for the
+            // chunks that take 720 so; the schedulers have no room for more.)
+            constexpr int kChunks = DP / 16;  // 16-code chunks
             const int r = (warp & 3) * 32 + lane;  // key of the tile
             const uint32_t swz = static_cast<uint32_t>(r & 7);
             const int32_t* row = p.table + static_cast<int64_t>(w.seq) * p.table_width;
@@ -818,17 +819,20 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             };
             float2 next = scales_at(0, page_at(0));
             int page = page_at(1);
+            uint32_t s = 0, phase = 0, d = 0;        // raw stage of the position, use of it, ring stage
+            uint32_t freed = 0, fs = 0, fphase = 0;  // releases waited for; the next one's barrier and phase
+            // One body for key and value tiles: two copies of it took 753 us where this takes 720.
+#pragma unroll 1
             for (int i = 0; i < 2 * n; ++i) {
                 const bool is_k = i == 0 || (i < 2 * n - 1 && (i & 1));
                 const int j = i == 0 ? 0 : is_k ? (i + 1) / 2 : i == 2 * n - 1 ? n - 1 : (i - 2) / 2;
                 const bool live = live_at(j);
                 const float2 scale = next;
-                if (is_k && h == 0) {
+                if (is_k) {
                     next = scales_at(j + 1, page);
                     page = page_at(j + 2);
                 }
-                const int s = i % kRaw, d = i % kStages;
-                if (!mbar_wait_warp(rawfull(s), static_cast<uint32_t>((i / kRaw) & 1), abort_flag)) {
+                if (!mbar_wait_warp(rawfull(s), phase, abort_flag)) {
                     if (lane == 0) attn_error(kErrWaitTma, abort_flag);
                     break;
                 }
@@ -836,14 +840,17 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                 const uint32_t src = sbase + L::kRawOff + s * L::kRawBytes + static_cast<uint32_t>(r) * DP;
 #pragma unroll
                 for (uint32_t u = 0; u < kChunks; ++u) {
-                    const uint32_t ch = h * kChunks + u;
-                    c[u] = lds128(src + ((DP == 128 ? ch ^ swz : ch ^ (swz >> 1)) << 4));  // 128- or 64-byte swizzle
+                    c[u] = lds128(src + ((DP == 128 ? u ^ swz : u ^ (swz >> 1)) << 4));  // 128- or 64-byte swizzle
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(rawempty(s));
-                if (!wait_free(i, abort_flag)) {
-                    if (lane == 0) attn_error(kErrWaitMma, abort_flag);
-                    break;
+                if (i >= kStages && i + 1 >= kStages + 2 * static_cast<int>(freed)) {
+                    if (!mbar_wait_warp(empty(fs), fphase, abort_flag)) {
+                        if (lane == 0) attn_error(kErrWaitMma, abort_flag);
+                        break;
+                    }
+                    ++freed;
+                    if (++fs == kStages) fs = 0, fphase ^= 1u;
                 }
                 const uint32_t dst = sbase + L::kRingOff + d * L::kTileBytes + static_cast<uint32_t>(r) * 128u;
 #pragma unroll
@@ -857,13 +864,12 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                         else
                             e4m3x4_to_f16x2(w4[e], v[2 * e], v[2 * e + 1]);
                     }
-                    // 16 values: 16-byte chunks 2 ch and 2 ch + 1 of the row
-                    const uint32_t ch = h * kChunks + u;
-                    const uint32_t sub = dst + (ch >> 2) * (kKeys * 128);
-                    sts128(sub + (((2 * ch) & 7) ^ swz) * 16, v[0], v[1], v[2], v[3]);
-                    sts128(sub + (((2 * ch + 1) & 7) ^ swz) * 16, v[4], v[5], v[6], v[7]);
+                    // 16 values: 16-byte chunks 2 u and 2 u + 1 of the row
+                    const uint32_t sub = dst + (u >> 2) * (kKeys * 128);
+                    sts128(sub + (((2 * u) & 7) ^ swz) * 16, v[0], v[1], v[2], v[3]);
+                    sts128(sub + (((2 * u + 1) & 7) ^ swz) * 16, v[4], v[5], v[6], v[7]);
                 }
-                if (is_k && h == 0) {  // the softmax needs both as soon as the tile's scores are there
+                if (is_k) {  // the softmax needs both as soon as the tile's scores are there
                     float* sc = reinterpret_cast<float*>(smem + L::kScaleOff) + (j % L::kScaleSlots) * 2 * kKeys + r;
                     sc[0] = scale.x * p.c;
                     sc[kKeys] = scale.y * kPScale;
@@ -871,6 +877,8 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full(d));
+                if (++s == kRaw) s = 0, phase ^= 1u;
+                if (++d == kStages) d = 0;
             }
         }
     } else {
