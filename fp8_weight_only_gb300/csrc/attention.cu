@@ -951,27 +951,33 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
         const uint32_t mine = sbase + L::kMlOff + ((pipe * 2 + half) * kRows + r) * 4;
         auto softmax_tile = [&](auto w_tag, int j) {
             constexpr int W = decltype(w_tag)::value;
-            constexpr int kStep = W < 32 ? W : 32;
+            constexpr int kStep = W < 32 ? W : !kFp8 && DP == 128 ? 16 : 32;
             const int key0 = (w.t0 + j) * kKeys + cbeg;
             const bool masked = key0 + W - 1 > warp_hi || key0 < warp_lo;
             // address taken after the wait, so the reads below stay behind it
             uint32_t ksc = sbase + L::kScaleOff + (j % L::kScaleSlots) * (2 * kKeys * 4) + cbeg * 4;
             asm volatile("" : "+r"(ksc)::"memory");
-            // kStep scores from the b-th on, with key scales (which hold c) and mask
-            auto scores = [&](int b, uint32_t (&v)[kStep]) {
-                if constexpr (W == 16)
-                    tmem_ld_x16_sync(t_s + cbeg, v);
+            // kStep exponents from the b-th on: scores times c (with codes, times key
+            // scales that hold it) less m, masked
+            auto exponents = [&](int b, uint64_t less_m, uint32_t (&v)[kStep]) {
+                if constexpr (kStep == 16)
+                    tmem_ld_x16_sync(t_s + cbeg + b, v);
                 else
                     tmem_ld_x32_sync(t_s + cbeg + b, v);
-                if constexpr (kFp8) {
 #pragma unroll
-                    for (int i = 0; i < kStep; i += 4) {
+                for (int i = 0; i < kStep; i += 4) {
+                    uint64_t x = pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                    uint64_t y = pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+                    if constexpr (kFp8) {
                         const float4 f = lds_f4(ksc + (b + i) * 4);
-                        const uint64_t x = mul2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), pack2(f.x, f.y));
-                        const uint64_t y = mul2(pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), pack2(f.z, f.w));
-                        v[i] = static_cast<uint32_t>(x), v[i + 1] = static_cast<uint32_t>(x >> 32);
-                        v[i + 2] = static_cast<uint32_t>(y), v[i + 3] = static_cast<uint32_t>(y >> 32);
+                        x = fma2(x, pack2(f.x, f.y), less_m);
+                        y = fma2(y, pack2(f.z, f.w), less_m);
+                    } else {
+                        x = fma2(x, c2, less_m);
+                        y = fma2(y, c2, less_m);
                     }
+                    v[i] = static_cast<uint32_t>(x), v[i + 1] = static_cast<uint32_t>(x >> 32);
+                    v[i + 2] = static_cast<uint32_t>(y), v[i + 3] = static_cast<uint32_t>(y >> 32);
                 }
                 if (masked) {
                     const int top = hi - key0 - b, bot = lo - key0 - b;
@@ -993,14 +999,14 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
 #pragma unroll 1
                 for (int b = 0; b < W; b += kStep) {
                     uint32_t v[kStep];
-                    scores(b, v);
+                    exponents(b, 0ull, v);
 #pragma unroll
                     for (int i = 0; i < kStep; i += 4) {
                         mx = max3(mx, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
                         my = max3(my, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
                     }
                 }
-                m = exchange(fmaxf(mx, my) * (kFp8 ? 1.0f : c));
+                m = exchange(fmaxf(mx, my));
             }
             uint32_t o[W / 2];
             uint64_t l0, l1;
@@ -1009,22 +1015,20 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             // moves and they are taken again.  Both threads of a row go on with the
             // same m, and neither writes P before the other has read its scores.
             for (;;) {
-                const float mc = m == kNegInf ? 0.0f : -m;
+                const float mc = m == kNegInf ? 0.0f : -m;  // while nothing was seen, exponents are not reduced
                 const uint64_t mc2 = pack2(mc, mc);
                 mx = my = kNegInf;
                 l0 = l1 = 0ull;
 #pragma unroll
                 for (int b = 0; b < W; b += kStep) {
                     uint32_t v[kStep];
-                    scores(b, v);
+                    exponents(b, mc2, v);
 #pragma unroll
                     for (int i = 0; i < kStep; i += 4) {
                         mx = max3(mx, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
                         my = max3(my, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
                         uint64_t x = pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
                         uint64_t y = pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
-                        x = kFp8 ? add2(x, mc2) : fma2(x, c2, mc2);
-                        y = kFp8 ? add2(y, mc2) : fma2(y, c2, mc2);
                         x = pack2(ex2(lo2(x)), ex2(hi2(x)));
                         y = pack2(ex2(lo2(y)), ex2(hi2(y)));
                         l0 = add2(l0, x);
@@ -1040,14 +1044,13 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                     if constexpr (kFp8) asm volatile("" : "+r"(ksc));  // scales of one part at a time
                 }
                 mx = fmaxf(mx, my);
-                if constexpr (!kFp8) mx *= c;
                 tc_fence_before();
-                const bool moves = bar_red_or(pair, 64, valid && mx - m > kSlack);  // -inf - -inf: no
+                const bool moves = bar_red_or(pair, 64, valid && mx > (m == kNegInf ? kNegInf : kSlack));
                 tc_fence_after();
                 if (!moves) break;
-                mx = exchange(mx);
+                mx = exchange(mx) - mc;
                 float alpha = 1.0f;
-                if (valid && mx - m > kSlack) {
+                if (valid && mx - m > kSlack) {  // -inf - -inf: no
                     alpha = ex2(m - mx);  // 0 while nothing was seen
                     m = mx;
                     l *= alpha;
@@ -1065,7 +1068,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                 }
             }
 #pragma unroll
-            for (int b = 0; b < W / 2; b += kStep / 2) {
+            for (int b = 0; b < (W == 64 ? 32 : 1); b += 16) {
                 if constexpr (W == 64) {
                     tmem_st_x16(t_s + cbeg / 2 + b, o + b);
                 } else {
