@@ -17,6 +17,8 @@
 // tokens a part of its heads: 32 / P heads a step (P lanes a head), kAhead
 // steps' loads in flight, the first before the position and the table row are
 // asked for, and its cosines and sines stay in registers over the heads.
+// 16384 tokens of 40 heads of 128, three axes: 60.8 us, 5.7 TB/s (84% of the
+// measured copy rate); one axis 55.7 us; 8192 tokens appended: 35.9 us (83%).
 #include "fp8w_device.cuh"
 #include "fp8w_internal.h"
 
@@ -28,7 +30,14 @@ namespace {
 
 constexpr int kRopeWarps = 4;
 constexpr int kRopeFill = 16;  // warps an SM up to which a token's heads are divided
-constexpr int kAhead = 2;  // steps of a warp in flight: 2 KB (4 steps: 77 us against 68 for 344 MB, the registers leave fewer warps)
+constexpr int kAhead = 2;  // steps of a warp in flight: 2 KB
+// Blocks an SM where a warp takes a whole token: the warps in flight count, and
+// for them the registers (344 MB: 5 blocks 67.5 us, 6 62.9, 7 60.8, 8 62.8;
+// codes, whose divisions take more of them: 8192 tokens 5 blocks 44.1 us, 6
+// 47.1, 7 47.9, no bound 50.5).
+// With fewer tokens a block's own time counts, and all registers help it (1161
+// tokens: 5.9 us, with the bound 7.6).
+constexpr int kDenseBlocks = 7, kDenseBlocksCodes = 5;
 
 struct RopeParams {
     const uint16_t* q;
@@ -73,8 +82,8 @@ __device__ __forceinline__ uint4 narrow(const float* f) {
 }
 
 // P lanes (a power of two >= head_dim / 16) work on a head.
-template <int P, bool kBf16, bool kFp8>
-__global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_constant__ RopeParams p) {
+template <int P, bool kBf16, bool kFp8, bool kDense>
+__global__ void __launch_bounds__(kRopeWarps * 32, !kDense ? 1 : kFp8 ? kDenseBlocksCodes : kDenseBlocks) rope_kernel(const __grid_constant__ RopeParams p) {
     pdl_launch_dependents();
     constexpr int kHeads = 32 / P;  // heads a step
     const int lane = threadIdx.x & 31, item = lane & (P - 1);
@@ -232,6 +241,15 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_cons
     }
 }
 
+template <int P, bool kDense>
+cudaError_t launch_form(const cudaLaunchConfig_t& cfg, const RopeParams& p, bool bf16, bool fp8) {
+    if (fp8)
+        return bf16 ? cudaLaunchKernelEx(&cfg, rope_kernel<P, true, true, kDense>, p)
+                    : cudaLaunchKernelEx(&cfg, rope_kernel<P, false, true, kDense>, p);
+    return bf16 ? cudaLaunchKernelEx(&cfg, rope_kernel<P, true, false, kDense>, p)
+                : cudaLaunchKernelEx(&cfg, rope_kernel<P, false, false, kDense>, p);
+}
+
 template <int P>
 cudaError_t launch_p(RopeParams p, bool bf16, bool fp8, cudaStream_t st) {
     int sms = 0;
@@ -255,11 +273,8 @@ cudaError_t launch_p(RopeParams p, bool bf16, bool fp8, cudaStream_t st) {
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (fp8)
-        return bf16 ? cudaLaunchKernelEx(&cfg, rope_kernel<P, true, true>, p)
-                    : cudaLaunchKernelEx(&cfg, rope_kernel<P, false, true>, p);
-    return bf16 ? cudaLaunchKernelEx(&cfg, rope_kernel<P, true, false>, p)
-                : cudaLaunchKernelEx(&cfg, rope_kernel<P, false, false>, p);
+    if (p.parts > 1) return launch_form<P, false>(cfg, p, bf16, fp8);
+    return launch_form<P, true>(cfg, p, bf16, fp8);
 }
 
 }  // namespace
