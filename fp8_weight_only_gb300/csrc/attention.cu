@@ -18,9 +18,24 @@
 // tile; with fewer, both take the same rows and the key tiles in turn, and
 // their two partial results are joined at the end.
 //   warps 0-7, 8-15 softmax of pipe 0, 1: two threads a row, half its keys each
-//   warp 16         TMA producer of key and value tiles, a lane a page
-//   warp 17         MMA issue; owns TMEM
+//   warps 16, 18, 19 (with codes 16, 18) TMA producers of key and value tiles
+//   warp 17         MMA issue, one thread; owns TMEM
 //   warps 20-23     (e4m3 cache) codes -> 16-bit operand tiles
+// What bounds it: 8192 new tokens, 32 query heads of 128, 16-slot pages take 390
+// us, 1410 TFLOP/s, 76% of the measured rate.  Per key tile of 256 rows the
+// products need 2048 cycles of the 3100 it takes; without the softmax's work 2700,
+// without products and work 1900: a pipe's scores, weights and products wait for
+// one another, and every instruction of the one thread that issues and of the
+// producers waits behind sixteen softmax warps, so these loops are kept short.
+// Heads of 64: 343 us, 43%: the softmax is the same for half the products.
+// Codes: 705 us for chunks of 500 to 1030 tokens over 9000 to 16000, 46%: the
+// softmax multiplies both scales too, and the conversion shares its schedulers;
+// 17% is the last wave (352 row tiles on 152 SMs).
+// Measured and not kept for the prompt: a pair of CTAs sharing products of 256
+// rows (cta_group::2, half of each key and value tile a CTA): 537 us when one CTA
+// took 455, each product waiting for both CTAs' softmax; scores of 64 keys at a
+// time in four buffers: 664; a persistent grid: 520 to 540 when this took 543, and
+// 52 instead of 39 for mixed lengths; two CTAs a tile's keys, joined: 782.
 // The reference m moves only when a row's maximum has grown by more than
 // 2^8 (kSlack) over it: then the row's O is rescaled, after the MMA that is
 // adding to it.  p stays below 2^8, and the sums are fp32.
@@ -48,10 +63,10 @@ constexpr int kKeys = 128;            // keys a tile
 constexpr int kRows = 128;            // rows a tile (TMEM lanes)
 constexpr int kMaxAttnCluster = 16;
 // Up to this many rows a key head (new tokens x its query heads) the kernel for
-// few rows reads the cache faster.  It takes 16 rows at a time: with 24 a 16-bit
-// cache is read twice (a decode batch of 1.2 GB: 374 us against 323 here; 16
-// rows: 243), a cache of codes twice is still less than here (384 against 278;
-// with 48, 434 against 390).
+// few rows reads the cache faster.  It takes 16 rows at a time: with more a 16-bit
+// cache is read twice (a decode batch of 1.2 GB, 16 rows: 244 us against 251 here,
+// 24: 373 against 254), a cache of codes twice or thrice is still less than here
+// (24: 275 against 395; 48: 378 against 410; 64: 478 against 414).
 constexpr int kFewRows = 16, kFewRowsCodes = 48;
 constexpr uint32_t kAttnTmemCols = 512;
 constexpr int kSoftmaxThreads = 512;   // sixteen warps
@@ -614,7 +629,8 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             // A tile is up to 16 copies of a page's 64-value sub-tile (a page's codes),
             // one a lane, of three warps in turn: a warp alone issues them too slowly,
             // and each instruction here waits behind the softmax warps' (8192 tokens on
-            // 16-slot pages: 543 us with one warp, 434 with two, 415 with three).
+            // 16-slot pages: 543 us with one warp when two took 455; 434 with two when
+            // three took 415).  Codes are half the copies: two warps, 707 us against 709.
             constexpr int kCopies = kFp8 ? 1 : static_cast<int>(L::kSubs);  // of a box
             const int loader = warp == kLoadWarp ? 0 : warp - kMmaWarp;
             const int box = p.page_size < kKeys ? p.page_size : kKeys;
@@ -701,8 +717,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             // ------------------------------------------------ MMA issue --
             // One thread, and no more instructions than it needs: it shares its
             // scheduler with four softmax warps, and the tensor cores wait for it
-            // (the loop of a whole warp with an election a product took 447 us for
-            // 8192 tokens).
+            // (8192 tokens: a whole warp that elects for each statement 447 us, this 434).
             if (elect_one()) {
                 constexpr uint32_t idesc_s = idesc_f16(kBf16, kKeys);
                 constexpr uint32_t idesc_o = idesc_f16(kBf16, DP) | kIdescBNMajor;
@@ -951,6 +966,8 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
         const uint32_t mine = sbase + L::kMlOff + ((pipe * 2 + half) * kRows + r) * 4;
         auto softmax_tile = [&](auto w_tag, int j) {
             constexpr int W = decltype(w_tag)::value;
+            // columns a load: 16 leave registers where the head is wide (8192 tokens 390
+            // us against 406; heads of 64 356 against 343, codes 720 against 705)
             constexpr int kStep = W < 32 ? W : !kFp8 && DP == 128 ? 16 : 32;
             const int key0 = (w.t0 + j) * kKeys + cbeg;
             const bool masked = key0 + W - 1 > warp_hi || key0 < warp_lo;
