@@ -17,8 +17,9 @@
 // tokens a part of its heads: 32 / P heads a step (P lanes a head), kAhead
 // steps' loads in flight, the first before the position and the table row are
 // asked for, and its cosines and sines stay in registers over the heads.
-// 16384 tokens of 40 heads of 128, three axes: 60.8 us, 5.7 TB/s (84% of the
-// measured copy rate); one axis 55.7 us; 8192 tokens appended: 35.9 us (83%).
+// 16384 tokens of 40 heads of 128, three axes: 58.5 us, 5.9 TB/s (87% of the
+// measured copy rate), one axis 53.6 us; 8192 tokens appended 33.9 us (88%), as
+// codes 41.6 us (66%: sixteen IEEE divisions a lane); one token 1.8 us.
 #include "fp8w_device.cuh"
 #include "fp8w_internal.h"
 
@@ -32,11 +33,10 @@ constexpr int kRopeWarps = 4;
 constexpr int kRopeFill = 16;  // warps an SM up to which a token's heads are divided
 constexpr int kAhead = 2;  // steps of a warp in flight: 2 KB
 // Blocks an SM where a warp takes a whole token: the warps in flight count, and
-// for them the registers (344 MB: 5 blocks 67.5 us, 6 62.9, 7 60.8, 8 62.8;
-// codes, whose divisions take more of them: 8192 tokens 5 blocks 44.1 us, 6
-// 47.1, 7 47.9, no bound 50.5).
-// With fewer tokens a block's own time counts, and all registers help it (1161
-// tokens: 5.9 us, with the bound 7.6).
+// for them the registers (344 MB: 6 blocks 63.1 us, 7 58.5, 8 59.1; 8192 tokens
+// appended 35.2, 33.9, 37.5; as codes, whose divisions take more of them, 4 blocks
+// 47.1 us, 5 41.6, 6 43.1).  With fewer tokens a block's own time counts, and all
+// registers help it (1161 tokens: 5.9 us when with the bound it was 7.6).
 constexpr int kDenseBlocks = 7, kDenseBlocksCodes = 5;
 
 struct RopeParams {
@@ -57,7 +57,7 @@ struct RopeParams {
     float* ks;
     float* vs;
     int64_t num_pages, page_stride, head_stride, token_stride;
-    int page_size;
+    int page_size, log_page;
     int parts, per_part;  // warps a token, steps of each
 };
 
@@ -75,43 +75,52 @@ template <bool kBf16>
 __device__ __forceinline__ uint4 narrow(const float* f) {
     uint32_t u[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        u[e] = static_cast<uint32_t>(round_out<kBf16>(f[2 * e])) |
-               (static_cast<uint32_t>(round_out<kBf16>(f[2 * e + 1])) << 16);
+    for (int e = 0; e < 4; ++e) {
+        if constexpr (kBf16)
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[e]) : "f"(f[2 * e + 1]), "f"(f[2 * e]));
+        else
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(u[e]) : "f"(f[2 * e + 1]), "f"(f[2 * e]));
+    }
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
+// What a call does: rotate, or also append to a 16-bit cache or one of codes.
+constexpr int kRotate = 0, kAppend16 = 1, kAppendCodes = 2;
+
 // P lanes (a power of two >= head_dim / 16) work on a head.
-template <int P, bool kBf16, bool kFp8, bool kDense>
-__global__ void __launch_bounds__(kRopeWarps * 32, !kDense ? 1 : kFp8 ? kDenseBlocksCodes : kDenseBlocks) rope_kernel(const __grid_constant__ RopeParams p) {
+template <int P, bool kBf16, int kKind, bool kDense>
+__global__ void __launch_bounds__(kRopeWarps * 32, !kDense ? 1 : kKind == kAppendCodes ? kDenseBlocksCodes : kDenseBlocks) rope_kernel(const __grid_constant__ RopeParams p) {
     pdl_launch_dependents();
     constexpr int kHeads = 32 / P;  // heads a step
+    constexpr bool kAppend = kKind != kRotate, kFp8 = kKind == kAppendCodes;
     const int lane = threadIdx.x & 31, item = lane & (P - 1);
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * kRopeWarps + (threadIdx.x >> 5);
-    const int64_t token = unit / p.parts;
+    // a token's parts are few where there are more than one: 32 bits
+    const int64_t token = kDense ? unit : static_cast<int64_t>(static_cast<uint32_t>(unit) / static_cast<uint32_t>(p.parts));
     if (token >= p.tokens) return;
-    const int part = static_cast<int>(unit - token * p.parts);
+    const int part = kDense ? 0 : static_cast<int>(unit - token * p.parts);
     const bool live = item * 16 < p.head_dim;
     const int half = p.rot_dim >> 1;
     const bool turns = p.positions && item * 16 < p.rot_dim;
     // the item's two chunks (first values)
     const int c0 = turns ? (p.interleaved ? item * 16 : item * 8) : item * 16;
     const int c1 = turns && !p.interleaved ? half + item * 8 : c0 + 8;
-    const int heads = p.q_heads + 2 * p.kv_heads, steps = (heads + kHeads - 1) / kHeads;
+    const int heads = p.q_heads + (kAppend ? 2 * p.kv_heads : 0), steps = (heads + kHeads - 1) / kHeads;
     const int first = part * p.per_part, last = min(first + p.per_part, steps);
     pdl_wait();
 
     int64_t slot = 0;
-    if (p.kv_heads) slot = __ldg(p.slots + token);
+    if constexpr (kAppend) slot = __ldg(p.slots + token);
     uint4 x[kAhead][2];
     auto head_of = [&](int step) { return step * kHeads + lane / P; };
+    const uint16_t* const q_row = p.q + token * p.q_stride;
+    const uint16_t* const k_row = p.k + token * p.k_stride;
+    const uint16_t* const v_row = p.v + token * p.v_stride;
     auto load = [&](int step, uint4 (&y)[2]) {
         const int h = head_of(step);
-        const bool is_q = h < p.q_heads, is_k = !is_q && h < p.q_heads + p.kv_heads;
+        const bool is_q = !kAppend || h < p.q_heads, is_k = !is_q && h < p.q_heads + p.kv_heads;
         const int kvh = h - p.q_heads - (is_k ? 0 : p.kv_heads);
-        const uint16_t* src = is_q ? p.q + token * p.q_stride + static_cast<int64_t>(h) * p.head_dim
-                              : is_k ? p.k + token * p.k_stride + static_cast<int64_t>(kvh) * p.head_dim
-                                     : p.v + token * p.v_stride + static_cast<int64_t>(kvh) * p.head_dim;
+        const uint16_t* src = (is_q ? q_row : is_k ? k_row : v_row) + static_cast<int64_t>(is_q ? h : kvh) * p.head_dim;
         y[0] = y[1] = make_uint4(0u, 0u, 0u, 0u);
         if (live && step < last && h < heads) {
             // values that do not turn go by their item's own chunks
@@ -161,16 +170,17 @@ __global__ void __launch_bounds__(kRopeWarps * 32, !kDense ? 1 : kFp8 ? kDenseBl
             }
         }
     }
-    const int64_t page = slot >= 0 ? slot / p.page_size : 0, off = slot - page * p.page_size;
-    bool kept = p.kv_heads && slot >= 0;  // the token goes into the cache
-    if (kept && page >= p.num_pages) {
+    const int64_t page = kAppend && slot >= 0 ? slot >> p.log_page : 0, off = slot - page * p.page_size;
+    bool kept = kAppend && slot >= 0;  // the token goes into the cache
+    if (kAppend && kept && page >= p.num_pages) {
         atomicCAS(&g_rope_error, 0, 6000 + kErrIndex);
         kept = false;
     }
 
+    uint16_t* const q_out_row = p.q_out + token * p.q_out_stride;
     auto finish = [&](int step, uint4 x0, uint4 x1) {
         const int h = head_of(step);
-        const bool is_q = h < p.q_heads, is_k = !is_q && h < p.q_heads + p.kv_heads;
+        const bool is_q = !kAppend || h < p.q_heads, is_k = !is_q && h < p.q_heads + p.kv_heads;
         const bool work = live && h < heads && (is_q || kept);
         const int kvh = is_q ? 0 : h - p.q_heads - (is_k ? 0 : p.kv_heads);
         const int s0 = (is_q || is_k) ? c0 : item * 16, s1 = (is_q || is_k) ? c1 : item * 16 + 8;
@@ -197,7 +207,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, !kDense ? 1 : kFp8 ? kDenseBl
             x1 = narrow<kBf16>(f + 8);
         }
         if (is_q && work) {
-            uint16_t* dst = p.q_out + token * p.q_out_stride + static_cast<int64_t>(h) * p.head_dim;
+            uint16_t* dst = q_out_row + static_cast<int64_t>(h) * p.head_dim;
             *reinterpret_cast<uint4*>(dst + s0) = x0;
             *reinterpret_cast<uint4*>(dst + s1) = x1;
         }
@@ -223,7 +233,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, !kDense ? 1 : kFp8 ? kDenseBl
                 *reinterpret_cast<uint2*>(dst + s1) = make_uint2(c[2], c[3]);
                 if (item == 0) (is_k ? p.ks : p.vs)[(page * p.kv_heads + kvh) * p.page_size + off] = s;
             }
-        } else if (!is_q && work) {
+        } else if (kAppend && !is_q && work) {
             uint16_t* dst = reinterpret_cast<uint16_t*>(is_k ? p.kc : p.vc) + page * p.page_stride +
                             kvh * p.head_stride + off * p.token_stride;
             *reinterpret_cast<uint4*>(dst + s0) = x0;
@@ -244,10 +254,13 @@ __global__ void __launch_bounds__(kRopeWarps * 32, !kDense ? 1 : kFp8 ? kDenseBl
 template <int P, bool kDense>
 cudaError_t launch_form(const cudaLaunchConfig_t& cfg, const RopeParams& p, bool bf16, bool fp8) {
     if (fp8)
-        return bf16 ? cudaLaunchKernelEx(&cfg, rope_kernel<P, true, true, kDense>, p)
-                    : cudaLaunchKernelEx(&cfg, rope_kernel<P, false, true, kDense>, p);
-    return bf16 ? cudaLaunchKernelEx(&cfg, rope_kernel<P, true, false, kDense>, p)
-                : cudaLaunchKernelEx(&cfg, rope_kernel<P, false, false, kDense>, p);
+        return bf16 ? cudaLaunchKernelEx(&cfg, rope_kernel<P, true, kAppendCodes, kDense>, p)
+                    : cudaLaunchKernelEx(&cfg, rope_kernel<P, false, kAppendCodes, kDense>, p);
+    if (p.kv_heads)
+        return bf16 ? cudaLaunchKernelEx(&cfg, rope_kernel<P, true, kAppend16, kDense>, p)
+                    : cudaLaunchKernelEx(&cfg, rope_kernel<P, false, kAppend16, kDense>, p);
+    return bf16 ? cudaLaunchKernelEx(&cfg, rope_kernel<P, true, kRotate, kDense>, p)
+                : cudaLaunchKernelEx(&cfg, rope_kernel<P, false, kRotate, kDense>, p);
 }
 
 template <int P>
@@ -315,6 +328,7 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
         p.head_stride = c.head_stride;
         p.token_stride = c.token_stride;
         p.page_size = c.page_size;
+        while ((1 << p.log_page) < c.page_size) ++p.log_page;
         fp8 = c.dtype == FP8W_E4M3;
     }
     const bool bf16 = a.act == FP8W_BF16;
