@@ -23,12 +23,12 @@
 //   warps 20-23     (e4m3 cache) codes -> 16-bit operand tiles
 // What bounds it: 8192 new tokens, 32 query heads of 128, 16-slot pages take 390
 // us, 1410 TFLOP/s, 76% of the measured rate.  Per key tile of 256 rows the
-// products need 2048 cycles of the 3100 it takes; without the softmax's work 2700,
+// products need 2048 cycles of the 3050 it takes; without the softmax's work 2700,
 // without products and work 1900: a pipe's scores, weights and products wait for
 // one another, and every instruction of the one thread that issues and of the
 // producers waits behind sixteen softmax warps, so these loops are kept short.
-// Heads of 64: 343 us, 43%: the softmax is the same for half the products.
-// Codes: 705 us for chunks of 500 to 1030 tokens over 9000 to 16000, 46%: the
+// Heads of 64: 341 us, 43%: the softmax is the same for half the products.
+// Codes: 688 us for chunks of 500 to 1030 tokens over 9000 to 16000, 47%: the
 // softmax multiplies both scales too, and the conversion shares its schedulers;
 // 17% is the last wave (352 row tiles on 152 SMs).
 // Measured and not kept for the prompt: a pair of CTAs sharing products of 256
@@ -215,7 +215,7 @@ __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a_lo, uint32_t b
         : "memory");
 }
 // D[tmem] (+)= A[tmem] B[smem] over 128 keys: 8 columns of A and 16 key rows
-// (2048 bytes) a step.
+// (2048 bytes) a step, the second 64 keys' columns 64 behind the first's.
 __device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool accumulate) {
     asm volatile(
         "{\n\t.reg .pred p, t;\n\t.reg .b64 y;\n\t.reg .b32 u, v;\n\t"
@@ -228,13 +228,13 @@ __device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint32_t b_lo
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t"
         "add.u32 u, %1, 24;\n\tadd.u32 v, %2, 384;\n\tmov.b64 y, {v, %3};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t"
-        "add.u32 u, %1, 32;\n\tadd.u32 v, %2, 512;\n\tmov.b64 y, {v, %3};\n\t"
+        "add.u32 u, %1, 64;\n\tadd.u32 v, %2, 512;\n\tmov.b64 y, {v, %3};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t"
-        "add.u32 u, %1, 40;\n\tadd.u32 v, %2, 640;\n\tmov.b64 y, {v, %3};\n\t"
+        "add.u32 u, %1, 72;\n\tadd.u32 v, %2, 640;\n\tmov.b64 y, {v, %3};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t"
-        "add.u32 u, %1, 48;\n\tadd.u32 v, %2, 768;\n\tmov.b64 y, {v, %3};\n\t"
+        "add.u32 u, %1, 80;\n\tadd.u32 v, %2, 768;\n\tmov.b64 y, {v, %3};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t"
-        "add.u32 u, %1, 56;\n\tadd.u32 v, %2, 896;\n\tmov.b64 y, {v, %3};\n\t"
+        "add.u32 u, %1, 88;\n\tadd.u32 v, %2, 896;\n\tmov.b64 y, {v, %3};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, t;\n\t}" ::"r"(d),
         "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate ? 1u : 0u)
         : "memory");
@@ -966,8 +966,8 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
         const uint32_t mine = sbase + L::kMlOff + ((pipe * 2 + half) * kRows + r) * 4;
         auto softmax_tile = [&](auto w_tag, int j) {
             constexpr int W = decltype(w_tag)::value;
-            // columns a load: 16 leave registers where the head is wide (8192 tokens 390
-            // us against 406; heads of 64 356 against 343, codes 720 against 705)
+            // columns a load: 16 leave registers where the head is wide (8192 tokens 380
+            // us against 387; codes 695 against 688, heads of 64 no difference)
             constexpr int kStep = W < 32 ? W : !kFp8 && DP == 128 ? 16 : 32;
             const int key0 = (w.t0 + j) * kKeys + cbeg;
             const bool masked = key0 + W - 1 > warp_hi || key0 < warp_lo;
@@ -1028,10 +1028,9 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             uint32_t o[W / 2];
             uint64_t l0, l1;
             // The weights are taken with the m of the tiles before, without waiting
-            // for this one's maximum; where that turns out to lie too far above, m
-            // moves and they are taken again.  Both threads of a row go on with the
-            // same m, and neither writes P before the other has read its scores.
-            for (;;) {
+            // for this one's maximum.  Where that turns out to lie too far above, m
+            // moves and they are taken again; both threads of a row have the same m.
+            auto weights = [&] {
                 const float mc = m == kNegInf ? 0.0f : -m;  // while nothing was seen, exponents are not reduced
                 const uint64_t mc2 = pack2(mc, mc);
                 mx = my = kNegInf;
@@ -1061,46 +1060,57 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                     if constexpr (kFp8) asm volatile("" : "+r"(ksc));  // scales of one part at a time
                 }
                 mx = fmaxf(mx, my);
-                tc_fence_before();
-                const bool moves = bar_red_or(pair, 64, valid && mx > (m == kNegInf ? kNegInf : kSlack));
-                tc_fence_after();
-                if (!moves) break;
-                mx = exchange(mx) - mc;
-                float alpha = 1.0f;
-                if (valid && mx - m > kSlack) {  // -inf - -inf: no
-                    alpha = ex2(m - mx);  // 0 while nothing was seen
-                    m = mx;
-                    l *= alpha;
-                }
-                if (done == 0) continue;
-                // O is at rest: the product of the tile before was issued before
-                // these scores, whose commit stands for it too
-#pragma unroll 1
-                for (int b = 0; b < DP / 2; b += 16) {
-                    uint32_t v[16];
-                    tmem_ld_x16_sync(t_o + b, v);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
-                    tmem_st_x16(t_o + b, v);
-                }
-            }
-#pragma unroll
-            for (int b = 0; b < (W == 64 ? 32 : 1); b += 16) {
+            };
+            auto store = [&] {
                 if constexpr (W == 64) {
-                    tmem_st_x16(t_s + cbeg / 2 + b, o + b);
+                    tmem_st_x16(t_s + cbeg, o);
+                    tmem_st_x16(t_s + cbeg + 16, o + 16);
                 } else {
 #pragma unroll
                     for (int f = 0; f < kKeys / 2 / W; ++f) {  // zero in the other copies' keys
                         uint32_t v[W / 2];
 #pragma unroll
                         for (int i = 0; i < W / 2; ++i) v[i] = f == copy ? o[i] : 0u;
+                        const int key = (f * 2 + half) * W, col = key / 2 + (key >= kKeys / 2 ? kKeys / 4 : 0);
                         if constexpr (W == 32)
-                            tmem_st_x16(t_s + (f * 2 + half) * (W / 2), v);
+                            tmem_st_x16(t_s + col, v);
                         else
-                            tmem_st_x8(t_s + (f * 2 + half) * (W / 2), v);
+                            tmem_st_x8(t_s + col, v);
+                    }
+                }
+            };
+            // No thread writes P before the other of its row knows whether m moves: with
+            // 64 keys its own scores go under it, with fewer those of others too.
+            // (Storing them before the vote, to be scaled by a power of two if m moves:
+            // 398 us for the 8192 tokens that take 382 so, the registers run short.)
+            weights();
+            tc_fence_before();
+            const bool moves = bar_red_or(pair, 64, valid && mx > (m == kNegInf ? kNegInf : kSlack));
+            tc_fence_after();
+            if (moves) {
+                const float top = exchange(mx) + (m == kNegInf ? 0.0f : m);
+                float alpha = 1.0f;
+                if (valid && top - m > kSlack) {  // -inf - -inf: no
+                    alpha = ex2(m - top);  // 0 while nothing was seen
+                    m = top;
+                    l *= alpha;
+                }
+                weights();
+                if constexpr (W < 64) asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+                // O is at rest: the product of the tile before was issued before
+                // these scores, whose commit stands for it too
+                if (done > 0) {
+#pragma unroll 1
+                    for (int b = 0; b < DP / 2; b += 16) {
+                        uint32_t v[16];
+                        tmem_ld_x16_sync(t_o + b, v);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+                        tmem_st_x16(t_o + b, v);
                     }
                 }
             }
+            store();
             l0 = add2(l0, l1);
             l += lo2(l0) + hi2(l0);
             tmem_wait_st();
