@@ -140,13 +140,12 @@ def test_many_short_sequences():
     run(new, [n + (i * 13) % 90 for i, n in enumerate(new)], 1, 2, 64, 16)
 
 
-# Long prompts of many heads: a sequence's rows, 512 at a time, to a pair of
-# CTAs that share every key tile.
+# Long prompts of many heads: several row tiles a sequence, several waves of them.
 
 @pytest.mark.parametrize("dtype,codes", [("bf16", False), ("f16", False), ("bf16", True), ("f16", True)])
 @pytest.mark.parametrize("page", [16, 64, 256])
 def test_long_prompts(page, dtype, codes):
-    # tiles of 512 rows full, by one row more, of a pipe's rows alone, of few
+    # row tiles full, by one row more, of a pipe's rows alone, of few
     run([1100, 512, 513, 1700, 3, 0, 256], [1100, 2000, 513, 1701, 5, 40, 300], 26, 1, 128, page, dtype, codes)
 
 
@@ -246,6 +245,22 @@ def test_pages_beyond_4_gib():
     out = fw.paged_attention(q, fw.KVCache(k, v), table, lens)
     rows = [t.flip(0)[:, 0].reshape(-1, 1, dim)[:40 * page - 3].double() for t in (k, v)]
     want, tol = attend(torch, q.double(), rows[0], rows[1], 1, 40 * page - 3, dim ** -0.5, 0, "bf16")
+    check(torch, out, want, tol)
+
+
+def test_pages_beyond_4_gib_many_rows():
+    page, dim, stride, n = 16, 128, 1 << 26, 30
+    big = torch.empty(40 * stride, dtype=torch.bfloat16, device=DEV)
+    k, v = (torch.as_strided(big, (40, 1, page, dim), (stride, page * dim, dim, 1), off) for off in (0, 1 << 20))
+    for t in (k, v):
+        t.copy_(torch.randn(t.shape, device=DEV))
+    table = torch.arange(39, -1, -1, dtype=torch.int32, device=DEV)[None]
+    length = 40 * page - 3
+    lens, starts = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([length], [0, n]))
+    q = torch.randn((n, 4, dim), device=DEV).bfloat16()
+    out = fw.paged_attention(q, fw.KVCache(k, v), table, lens, starts=starts)
+    rows = [t.flip(0)[:, 0].reshape(-1, 1, dim)[:length].double() for t in (k, v)]
+    want, tol = attend(torch, q.double(), rows[0], rows[1], n, length, dim ** -0.5, 0, "bf16")
     check(torch, out, want, tol)
 
 
