@@ -21,8 +21,8 @@
 //   warps 16, 18, 19 (with codes 16, 18) TMA producers of key and value tiles
 //   warp 17         MMA issue, one thread; owns TMEM
 //   warps 20-23     (e4m3 cache) codes -> 16-bit operand tiles
-// What bounds it: 8192 new tokens, 32 query heads of 128, 16-slot pages take 390
-// us, 1410 TFLOP/s, 76% of the measured rate.  Per key tile of 256 rows the
+// What bounds it: 8192 new tokens, 32 query heads of 128, 16-slot pages take 380
+// us, 1446 TFLOP/s, 78% of the measured rate.  Per key tile of 256 rows the
 // products need 2048 cycles of the 3050 it takes; without the softmax's work 2700,
 // without products and work 1900: a pipe's scores, weights and products wait for
 // one another, and every instruction of the one thread that issues and of the
