@@ -81,6 +81,10 @@ struct FewShape {
     static constexpr uint32_t kStageOff = 0;                           // fp32 [warps][rows][DP]
     static constexpr uint32_t kMlOff = kFewWarps * kTile * DP * 4;
     static constexpr uint32_t kJoinedOff = kMlOff + kFewWarps * kTile * 8;
+    // Registers that a load leaves out keep their values: fewer instructions, but
+    // they stay occupied, and the wide forms have none to spare (a decode batch of
+    // heads of 64: 122 us against 143; of 128 no difference, its codes 191 against 142).
+    static constexpr bool kKeeps = DP == 64 && !kFp8;
     // the queries' operands: registers, or shared memory where those are short
     static constexpr bool kQShared = NT == 2 && DP == 128 && !kFp8;
     static constexpr uint32_t kQOff = kJoinedOff + kTile * 8;
@@ -230,7 +234,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
         }
     };
     auto load = [&](int st, const int (&e)[kSubs], H& x) {
-        // slots at or past `end` may hold anything: zeros instead
+        // Slots at or past `end` may hold anything and are not read: zeros instead, or
+        // (kKeeps) what an earlier step left in the registers, finite values whose
+        // weights are 0.
 #pragma unroll
         for (int i = 0; i < kSubs; ++i) {
             const int key16 = st * kStepKeys + 16 * i, slot = key16 & (p.page_size - 1);
@@ -244,7 +250,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
                 const bool in = page && key < end && key >= first;
 #pragma unroll
                 for (int j = 0; j < S::kKeyPieces; ++j) {
-                    x.k[i][r][j] = make_uint4(0u, 0u, 0u, 0u);
+                    if constexpr (!S::kKeeps) x.k[i][r][j] = make_uint4(0u, 0u, 0u, 0u);
                     if (in && j * 64 + t * 16 < p.head_dim * kEl) x.k[i][r][j] = ldg_stream_v4(kthread + at + 8 * r * token_bytes + j * 64);
                 }
                 if constexpr (kFp8) {
@@ -260,7 +266,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
                 const uint8_t* row = vthread + at + r * token_bytes;
 #pragma unroll
                 for (int h = 0; h < S::kValuePieces; ++h) {
-                    x.v[i][j][h] = make_uint4(0u, 0u, 0u, 0u);
+                    if constexpr (!S::kKeeps) x.v[i][j][h] = make_uint4(0u, 0u, 0u, 0u);
                     if constexpr (kFp8) {
                         if (in && g * (DP / 8) < p.head_dim) x.v[i][j][h] = load_codes(row);
                     } else {
@@ -431,7 +437,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
         // around the loads of whole steps the same loop took a tenth longer.
         int st = step0 + rank * kFewWarps + warp;
         int e[kSubs];
-        H x0, x1;
+        H x0 = {}, x1 = {};
         entries(st, e);
         load(st, e, x0);
         entries(st + workers, e);
