@@ -46,8 +46,11 @@
 // Long caches and few rows: the CTAs of a cluster take equal runs of key tiles
 // and join their (m, sum, O) in distributed shared memory, in rank order.
 //
-// Every wait is bounded; a CTA that gives up records a code, raises its abort
-// flag, lets its copies and MMAs land and frees TMEM.
+// Every wait on an mbarrier is bounded; a CTA that gives up records a code, raises
+// its abort flag, lets its copies and MMAs land and frees TMEM.  The named barriers
+// of the softmax warps have no bound, so no warp passes one by: what a wait came to
+// decides what is waited for and written next, never who takes part in a barrier
+// (a warp that gave up works on whatever its tiles' tensor memory holds).
 #include <mutex>
 #include <type_traits>
 
@@ -387,7 +390,7 @@ __device__ __noinline__ void join_results(const AttnParams& p, const Work& w, co
         softmax_bar();
         if (!w.two) {
             const bool direct = split == 1 && p.cl == 1;
-            if (pipe == 0 && ok && busy) {
+            if (pipe == 0 && busy) {
                 // add pipe 1's partial to this one's
                 const float2 other = valid ? lds_f2(ml + r * 8) : make_float2(0.0f, 0.0f);
                 const float mine_l = done > 0 ? l : 0.0f;
@@ -414,20 +417,18 @@ __device__ __noinline__ void join_results(const AttnParams& p, const Work& w, co
                         for (int e = 0; e < 4; ++e)
                             o[i + e] = __float_as_uint(a0 > 0.0f ? fmaf(__uint_as_float(o[i + e]), a0, x[e]) : x[e]);
                     }
-                    if (valid && direct) {
-                        {
-                    uint16_t* dst = out_at(w.row0 + r);
+                    if (valid && direct && ok) {
+                        uint16_t* dst = out_at(w.row0 + r);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        if (cout + b + i >= p.head_dim) break;
-                        uint32_t v[4];
+                        for (int i = 0; i < 32; i += 8) {
+                            if (cout + b + i >= p.head_dim) break;
+                            uint32_t v[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            v[e] = pack16<kBf16>(__uint_as_float(o[i + 2 * e]) * inv, __uint_as_float(o[i + 2 * e + 1]) * inv);
-                        *reinterpret_cast<uint4*>(dst + cout + b + i) = make_uint4(v[0], v[1], v[2], v[3]);
-                    }
-                }
-                    } else if (valid) {
+                            for (int e = 0; e < 4; ++e)
+                                v[e] = pack16<kBf16>(__uint_as_float(o[i + 2 * e]) * inv, __uint_as_float(o[i + 2 * e + 1]) * inv);
+                            *reinterpret_cast<uint4*>(dst + cout + b + i) = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
+                    } else if (valid && !direct) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) sts128(stage_at(r, (cout + b + i) / 4), o[i], o[i + 1], o[i + 2], o[i + 3]);
                     }
@@ -611,8 +612,8 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
     const int item = static_cast<int>(blockIdx.x) / p.cl;
     const int tile = item / p.kv_heads, head = item - tile * p.kv_heads;
     Work w = {};
-    const bool have = !*abort_flag && find_work(p, tile, head, rank, w,
-                                                blockIdx.x == 0 && warp == 0);
+    // the same for all threads (not by the abort flag, which a warp may raise meanwhile)
+    const bool have = !(sbase & 1023u) && find_work(p, tile, head, rank, w, blockIdx.x == 0 && warp == 0);
     if (!have) w = Work{};
     const int n = w.cnt;
     // Ring positions: K0 K1 V0 K2 V1 .. K(n-1) V(n-2) V(n-1).
@@ -1119,10 +1120,9 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
 
         const int step = w.two ? 1 : 2, jn = w.two && pipe == 0 ? w.cnt0 : n;
         for (int j = w.two ? 0 : pipe; j < jn; j += step, ++done) {
-            if (!mbar_wait_warp(sfull(pipe), static_cast<uint32_t>(done & 1), abort_flag)) {
-                if (lane == 0) attn_error(kErrWaitMma, abort_flag);
-                ok = false;
-                break;
+            if (ok) {
+                ok = mbar_wait_warp(sfull(pipe), static_cast<uint32_t>(done & 1), abort_flag);
+                if (!ok && lane == 0) attn_error(kErrWaitMma, abort_flag);
             }
             tc_fence_after();
             if (busy) {
@@ -1132,7 +1132,6 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                     softmax_tile(std::integral_constant<int, 32>{}, j);
                 else
                     softmax_tile(std::integral_constant<int, 64>{}, j);
-                if (!ok) break;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(pfull(pipe));
