@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                 const int key = key0 + j * kKeys;
                 return j < n && lives && key < w.end && key + box > w.first_key;
             };
-            auto entry_of = [&](int j) { return wanted(j) ? __ldg(row + ((key0 + j * kKeys) >> p.log_page)) : none; };
+            auto entry_of = [&](int j) { return wanted(j) ? row[(key0 + j * kKeys) >> p.log_page] : none; };
             auto page_of = [&](int j, int entry) {
                 if (static_cast<uint32_t>(entry) < static_cast<uint32_t>(none)) return entry;
                 if (wanted(j)) atomicCAS(&g_attention_error, 0, 7000 + kErrIndex);
@@ -827,11 +827,11 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             // neither is waited for.
             const int64_t head_scales = static_cast<int64_t>(w.head) * p.page_size;
             const int64_t page_scales = static_cast<int64_t>(p.kv_heads) * p.page_size;
-            auto page_at = [&](int j) { return live_at(j) ? __ldg(row + (((w.t0 + j) * kKeys + r) >> p.log_page)) : -1; };
+            auto page_at = [&](int j) { return live_at(j) ? row[((w.t0 + j) * kKeys + r) >> p.log_page] : -1; };
             auto scales_at = [&](int j, int pg) {
                 if (pg < 0 || pg >= p.num_pages) return make_float2(0.0f, 0.0f);
                 const int64_t at = head_scales + pg * page_scales + (((w.t0 + j) * kKeys + r) & (p.page_size - 1));
-                return make_float2(__ldg(p.k_scales + at), __ldg(p.v_scales + at));
+                return make_float2(p.k_scales[at], p.v_scales[at]);
             };
             float2 next = scales_at(0, page_at(0));
             int page = page_at(1);

@@ -33,6 +33,16 @@ struct AttnParams {
     int cl;          // CTAs a cluster
 };
 
+// 16 bytes that are read once, not kept in L1.  An ordinary load, as all loads of
+// operands here are: these kernels start while those ahead of them in the stream
+// still write pages, scales and indices, and the wait for them orders ordinary
+// loads only, not those of the read-only path.
+__device__ __forceinline__ uint4 ld_stream_v4(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
 // A tile of `tile_rows` rows (counted token * group + head) of one sequence.
 struct SeqTile {
     int seq, inner;        // the sequence, the tile's number in it
@@ -54,7 +64,7 @@ __device__ __forceinline__ bool find_tile(const AttnParams& p, int tile_rows, in
         if (f.seq >= p.seqs) return false;
         f.begin = f.seq;
         f.count = 1;
-        f.len = __ldg(p.lens + f.seq);
+        f.len = p.lens[f.seq];
     } else {
         int64_t before = 0;
         for (int b0 = 0; b0 < p.seqs; b0 += 32) {
@@ -62,9 +72,9 @@ __device__ __forceinline__ bool find_tile(const AttnParams& p, int tile_rows, in
             int64_t s = 0, n = 0;
             int size = 0;
             if (b < p.seqs) {
-                size = __ldg(p.lens + b);
-                s = __ldg(p.starts + b);
-                n = __ldg(p.starts + b + 1) - s;
+                size = p.lens[b];
+                s = p.starts[b];
+                n = p.starts[b + 1] - s;
                 if (s < 0 || n < 0 || s + n > p.tokens) {
                     if (report) atomicCAS(error, 0, 7000 + kErrIndex);
                     n = 0;

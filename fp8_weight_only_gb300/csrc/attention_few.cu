@@ -217,9 +217,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
     auto load_codes = [&](const uint8_t* at) {  // a value row's codes of this thread
         uint4 y = make_uint4(0u, 0u, 0u, 0u);
         if constexpr (DP == 128) {
-            y = ldg_stream_v4(at);
+            y = ld_stream_v4(at);
         } else {
-            const uint2 z = __ldg(reinterpret_cast<const uint2*>(at));
+            const uint2 z = *reinterpret_cast<const uint2*>(at);
             y.x = z.x, y.y = z.y;
         }
         return y;
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
 #pragma unroll
         for (int i = 0; i < kSubs; ++i) {
             const int key = st * kStepKeys + 16 * i;
-            e[i] = st < steps && key < end && key + 16 > first ? __ldg(table + (key >> p.log_page)) : -1;
+            e[i] = st < steps && key < end && key + 16 > first ? table[key >> p.log_page] : -1;
         }
     };
     auto load = [&](int st, const int (&e)[kSubs], H& x) {
@@ -251,12 +251,12 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
 #pragma unroll
                 for (int j = 0; j < S::kKeyPieces; ++j) {
                     if constexpr (!S::kKeeps) x.k[i][r][j] = make_uint4(0u, 0u, 0u, 0u);
-                    if (in && j * 64 + t * 16 < p.head_dim * kEl) x.k[i][r][j] = ldg_stream_v4(kthread + at + 8 * r * token_bytes + j * 64);
+                    if (in && j * 64 + t * 16 < p.head_dim * kEl) x.k[i][r][j] = ld_stream_v4(kthread + at + 8 * r * token_bytes + j * 64);
                 }
                 if constexpr (kFp8) {
                     const int64_t sc = (static_cast<int64_t>(e[i]) * p.kv_heads + head) * p.page_size + slot + g + 8 * r;
-                    x.ks[i][r] = in ? __ldg(p.k_scales + sc) : 0.0f;
-                    x.vs[i][r] = in ? __ldg(p.v_scales + sc) : 0.0f;
+                    x.ks[i][r] = in ? p.k_scales[sc] : 0.0f;
+                    x.vs[i][r] = in ? p.v_scales[sc] : 0.0f;
                 }
             }
 #pragma unroll
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
                     if constexpr (kFp8) {
                         if (in && g * (DP / 8) < p.head_dim) x.v[i][j][h] = load_codes(row);
                     } else {
-                        if (in && h * 64 + g * 8 < p.head_dim) x.v[i][j][h] = ldg_stream_v4(row + h * 128);
+                        if (in && h * 64 + g * 8 < p.head_dim) x.v[i][j][h] = ld_stream_v4(row + h * 128);
                     }
                 }
             }

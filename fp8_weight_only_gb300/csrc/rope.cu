@@ -16,7 +16,9 @@
 // (in-place calls need no further order).  A warp takes a token, or with few
 // tokens a part of its heads: 32 / P heads a step (P lanes a head), kAhead
 // steps' loads in flight, the first before the position and the table row are
-// asked for, and its cosines and sines stay in registers over the heads.
+// asked for, and its cosines and sines stay in registers over the heads.  All
+// loads are ordinary ones, none of the read-only path: the kernel starts while
+// those ahead of it in the stream still write, and its wait orders ordinary loads.
 // 16384 tokens of 40 heads of 128, three axes: 58.5 us, 5.9 TB/s (87% of the
 // measured copy rate), one axis 53.6 us; 8192 tokens appended 33.9 us (88%), as
 // codes 41.6 us (66%: sixteen IEEE divisions a lane); one token 1.8 us.
@@ -110,7 +112,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, !kDense ? 1 : kKind == kAppen
     pdl_wait();
 
     int64_t slot = 0;
-    if constexpr (kAppend) slot = __ldg(p.slots + token);
+    if constexpr (kAppend) slot = p.slots[token];
     uint4 x[kAhead][2];
     auto head_of = [&](int step) { return step * kHeads + lane / P; };
     const uint16_t* const q_row = p.q + token * p.q_stride;
@@ -137,7 +139,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, !kDense ? 1 : kKind == kAppen
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
             if (a >= p.axes) break;
-            int64_t at = __ldg(p.positions + a * p.tokens + token);
+            int64_t at = p.positions[a * p.tokens + token];
             if (at < 0 || at >= p.max_pos) {
                 atomicCAS(&g_rope_error, 0, 6000 + kErrIndex);
                 at = at < 0 ? 0 : p.max_pos - 1;
@@ -156,8 +158,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, !kDense ? 1 : kKind == kAppen
             const float* row = row_of(axis_of(i0)) + i0;
 #pragma unroll
             for (int e = 0; e < 8; e += 4) {
-                const float4 c = __ldg(reinterpret_cast<const float4*>(row + e));
-                const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + e));
+                const float4 c = *reinterpret_cast<const float4*>(row + e);
+                const float4 s = *reinterpret_cast<const float4*>(row + half + e);
                 cs[e] = c.x, cs[e + 1] = c.y, cs[e + 2] = c.z, cs[e + 3] = c.w;
                 sn[e] = s.x, sn[e + 1] = s.y, sn[e + 2] = s.z, sn[e + 3] = s.w;
             }
@@ -165,8 +167,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, !kDense ? 1 : kKind == kAppen
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float* row = row_of(axis_of(i0 + e)) + i0 + e;
-                cs[e] = __ldg(row);
-                sn[e] = __ldg(row + half);
+                cs[e] = *row;
+                sn[e] = row[half];
             }
         }
     }
