@@ -366,6 +366,8 @@ __device__ __noinline__ void join_results(const AttnParams& p, const Work& w, co
         const int t = row / p.group, g = row - t * p.group;
         return out + t * p.out_stride + g * p.head_dim;
     };
+    const int64_t sees_from = -static_cast<int64_t>(w.pos0) * p.group - w.row0;  // the CTA's first row at position 0 or above
+    auto sees = [&](int row) { return row >= sees_from; };
     const int rounds = w.two ? 2 : 1;
     softmax_bar();  // both pipes' products are complete: Q's place is free
     for (int round = 0; round < rounds; ++round) {
@@ -394,11 +396,11 @@ __device__ __noinline__ void join_results(const AttnParams& p, const Work& w, co
                 // add pipe 1's partial to this one's
                 const float2 other = valid ? lds_f2(ml + r * 8) : make_float2(0.0f, 0.0f);
                 const float mine_l = done > 0 ? l : 0.0f;
-                const float top = fmaxf(mine_l > 0.0f ? m : other.x, other.y > 0.0f ? other.x : m);
-                const float a0 = mine_l > 0.0f ? ex2(m - top) : 0.0f;
-                const float a1 = other.y > 0.0f ? ex2(other.x - top) : 0.0f;
+                const float top = fmaxf(mine_l != 0.0f ? m : other.x, other.y != 0.0f ? other.x : m);
+                const float a0 = mine_l != 0.0f ? ex2(m - top) : 0.0f;
+                const float a1 = other.y != 0.0f ? ex2(other.x - top) : 0.0f;
                 const float sum = a0 * mine_l + a1 * other.y;
-                const float inv = sum > 0.0f ? kUnscale / sum : 0.0f;
+                const float inv = kUnscale * weight_inverse(sum, sees(r));
                 // both threads of the row have read its (m, l)
                 asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
 #pragma unroll
@@ -448,12 +450,12 @@ __device__ __noinline__ void join_results(const AttnParams& p, const Work& w, co
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
                 q[f] = f < split ? lds_f2(ml + (f * per_copy + row) * 8) : make_float2(kNegInf, 0.0f);
-                if (q[f].y > 0.0f) top = fmaxf(top, q[f].x);
+                if (q[f].y != 0.0f) top = fmaxf(top, q[f].x);
             }
             float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
-                if (!(q[f].y > 0.0f)) continue;
+                if (q[f].y == 0.0f) continue;
                 const uint4 v = lds128(stage_at(f * per_copy + row, ch));
                 const float a = ex2(q[f].x - top);
                 sum = fmaf(q[f].y, a, sum);
@@ -463,7 +465,7 @@ __device__ __noinline__ void join_results(const AttnParams& p, const Work& w, co
                 acc[3] = fmaf(__uint_as_float(v.w), a, acc[3]);
             }
             if (p.cl == 1) {
-                const float inv = sum > 0.0f ? kUnscale / sum : 0.0f;
+                const float inv = kUnscale * weight_inverse(sum, sees(round * kRows + row));
                 if (ch * 4 < p.head_dim)
                     *reinterpret_cast<uint2*>(out_at(w.row0 + row) + ch * 4) =
                         make_uint2(pack16<kBf16>(acc[0] * inv, acc[1] * inv), pack16<kBf16>(acc[2] * inv, acc[3] * inv));
@@ -507,7 +509,7 @@ __device__ __noinline__ void join_results(const AttnParams& p, const Work& w, co
                     }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        if (!(q[e].y > 0.0f)) continue;
+                        if (q[e].y == 0.0f) continue;
                         const float to = fmaxf(top, q[e].x);
                         const float x = ex2(top - to), y = ex2(q[e].x - to);
                         top = to;
@@ -523,7 +525,7 @@ __device__ __noinline__ void join_results(const AttnParams& p, const Work& w, co
                     const float4 o = make_float4(__shfl_xor_sync(0xffffffffu, acc.x, d), __shfl_xor_sync(0xffffffffu, acc.y, d),
                                                  __shfl_xor_sync(0xffffffffu, acc.z, d), __shfl_xor_sync(0xffffffffu, acc.w, d));
                     const float to = fmaxf(top, o_top);
-                    const float x = sum > 0.0f ? ex2(top - to) : 0.0f, y = o_sum > 0.0f ? ex2(o_top - to) : 0.0f;
+                    const float x = sum != 0.0f ? ex2(top - to) : 0.0f, y = o_sum != 0.0f ? ex2(o_top - to) : 0.0f;
                     top = to;
                     sum = sum * x + o_sum * y;
                     acc.x = acc.x * x + o.x * y;
@@ -531,7 +533,7 @@ __device__ __noinline__ void join_results(const AttnParams& p, const Work& w, co
                     acc.z = acc.z * x + o.z * y;
                     acc.w = acc.w * x + o.w * y;
                 }
-                const float inv = sum > 0.0f ? kUnscale / sum : 0.0f;
+                const float inv = kUnscale * weight_inverse(sum, sees(round * kRows + row));
                 if (live && k0 == 0 && ch * 4 < p.head_dim)
                     *reinterpret_cast<uint2*>(out_at(w.row0 + round * kRows + row) + ch * 4) =
                         make_uint2(pack16<kBf16>(acc.x * inv, acc.y * inv), pack16<kBf16>(acc.z * inv, acc.w * inv));
@@ -1156,7 +1158,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                 // reads any more (half a row a warp): 16-byte chunks swizzled by the row,
                 // then 16 bytes a lane along the rows to memory.
                 constexpr int kHalf = DP / 2, kChunks = kHalf / 8, kRowsAtOnce = 32 / kChunks;
-                const float inv = l > 0.0f ? 1.0f / (kPScale * l) : 0.0f;
+                const float inv = weight_inverse(kPScale * l, hi >= 0);
                 const uint32_t mine = sbase + L::kQOff + pipe * L::kTileBytes + (half * 4 + quarter) * (32 * kHalf * 2);
 #pragma unroll
                 for (int b = 0; b < kHalf; b += 32) {

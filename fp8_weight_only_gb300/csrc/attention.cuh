@@ -109,6 +109,14 @@ __device__ __forceinline__ bool find_tile(const AttnParams& p, int tile_rows, in
     return true;
 }
 
+// What a row's sum of weighted values is multiplied by.  A sum of weights is 0 where
+// the row saw no key, and partial ones are left out of a join for that alone: one
+// that is NaN (a query or score that is not finite) has to reach the output.  A row
+// that sees keys and still has 0 has scores of -inf only, whose softmax is NaN too.
+__device__ __forceinline__ float weight_inverse(float sum, bool sees) {
+    return sum != 0.0f ? 1.0f / sum : sees ? __int_as_float(0x7fffffff) : 0.0f;
+}
+
 // Bound on the row tiles of all sequences, from what the host knows.
 inline int64_t attention_row_tiles(const AttentionArgs& a, int group, int tile_rows) {
     const int64_t most_new = a.starts ? (a.max_new > 0 ? a.max_new : a.tokens) : 1;

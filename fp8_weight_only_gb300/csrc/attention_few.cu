@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
                         for (int h = 0; h < 2; ++h) mx = fmaxf(mx, s[i][n][2 * h + r] + (kFp8 ? lv[kFp8 ? i : 0][h] : 0.0f));
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                    if (mx > m[n][r]) {
+                    if (mx - m[n][r] > kSlack) {  // by its own row alone: other rows of the tile change nothing in it
                         const float alpha = ex2(m[n][r] - mx);
                         m[n][r] = mx;
                         l[n][r] *= alpha;
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
         }
     __syncthreads();
     auto write = [&](int row, int chunk, const float* acc, float sum) {
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        const float inv = weight_inverse(sum, pos0 + (row0 + row) / p.group >= 0);
         if (chunk * 4 < p.head_dim)
             *reinterpret_cast<uint2*>(p.out + row_at(row, p.out_stride) + chunk * 4) =
                 make_uint2(pack16<kBf16>(acc[0] * inv, acc[1] * inv), pack16<kBf16>(acc[2] * inv, acc[3] * inv));
@@ -497,11 +497,11 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
 #pragma unroll
         for (int w = 0; w < kFewWarps; ++w) {
             asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(q[w].x), "=f"(q[w].y) : "r"(ml_at(w, row)) : "memory");
-            if (q[w].y > 0.0f) top = fmaxf(top, q[w].x);
+            if (q[w].y != 0.0f) top = fmaxf(top, q[w].x);
         }
 #pragma unroll
         for (int w = 0; w < kFewWarps; ++w) {
-            if (!(q[w].y > 0.0f)) continue;
+            if (q[w].y == 0.0f) continue;
             const uint4 y = lds128(stage_at(w, row, chunk));
             const float a = ex2(q[w].x - top);
             sum = fmaf(q[w].y, a, sum);
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
             const uint32_t joined = sbase + S::kJoinedOff + row * 8, part = stage_at(0, row, chunk);
             float top = kNegInf, sum = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             auto add = [&](float o_top, float o_sum, const float (&y)[4]) {
-                if (!(o_sum > 0.0f)) return;
+                if (o_sum == 0.0f) return;
                 const float to = fmaxf(top, o_top);
                 const float a = ex2(top - to), z = ex2(o_top - to);
                 top = to;

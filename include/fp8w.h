@@ -453,6 +453,8 @@ FP8W_API fp8w_status fp8w_rope_append(const void *q, const void *k, const void *
  * tokens of len in all, new token i is at position len - n + i and sees
  * positions 0 .. len - n + i, with window > 0 only the last `window` of them.
  * A token that sees none (len 0, or a position below 0) gets zeros.
+ * A query that is not finite, or a score beyond fp32, makes its row NaN, and no
+ * other row.
  *   q            [tokens, q_heads, head_dim] act_dtype, token stride q_stride;
  *                q_heads a multiple of the cache's kv_heads, at most 4096 times them.
  *   block_table  [seqs, table_width] int32, device: page of the sequence's
