@@ -49,8 +49,8 @@
 // Every wait on an mbarrier is bounded; a CTA that gives up records a code, raises
 // its abort flag, lets its copies and MMAs land and frees TMEM.  The named barriers
 // of the softmax warps have no bound, so no warp passes one by: what a wait came to
-// decides what is waited for and written next, never who takes part in a barrier
-// (a warp that gave up works on whatever its tiles' tensor memory holds).
+// decides what is worked on and written next, never who takes part in a barrier (a
+// warp that gave up takes part in those of its remaining tiles).
 #include <mutex>
 #include <type_traits>
 
@@ -1121,10 +1121,12 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
         };
 
         const int step = w.two ? 1 : 2, jn = w.two && pipe == 0 ? w.cnt0 : n;
-        for (int j = w.two ? 0 : pipe; j < jn; j += step, ++done) {
-            if (ok) {
-                ok = mbar_wait_warp(sfull(pipe), static_cast<uint32_t>(done & 1), abort_flag);
-                if (!ok && lane == 0) attn_error(kErrWaitMma, abort_flag);
+        int j = w.two ? 0 : pipe;
+        for (; j < jn; j += step, ++done) {
+            if (!mbar_wait_warp(sfull(pipe), static_cast<uint32_t>(done & 1), abort_flag)) {
+                if (lane == 0) attn_error(kErrWaitMma, abort_flag);
+                ok = false;
+                break;
             }
             tc_fence_after();
             if (busy) {
@@ -1137,6 +1139,16 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(pfull(pipe));
+        }
+        // The tiles of a warp that gave up: softmax_tile's barriers, for the row's other
+        // warp may still take them.  (Going on in the loop above without its waits: 418 us
+        // for the 8192 tokens that take 403 so.)
+        for (; j < jn && busy; j += step, ++done) {
+            if (done == 0) asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+            if (bar_red_or(pair, 64, false)) {
+                asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+                if (split > 1) asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+            }
         }
         // --------------------------------------------------- the result --
         if (ok && done > 0) {
