@@ -344,13 +344,39 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
                     if constexpr (!kFp8) grow |= y - m[n][j & 1] > kSlack;  // -inf - -inf: no
                 }
             }
-        float lv[kFp8 ? kSubs : 1][2];
+        float vs[kFp8 ? kSubs : 1][2], lv[kFp8 ? kSubs : 1][2];
         if constexpr (kFp8) {
+            // A row of zeros has the scale 1, as if its values reached 448: left so, a
+            // large score there would set the reference and the weights of small values
+            // would go below fp16.  So where a scale is 1, look at the codes: 0 for it.
+            bool one = false;
 #pragma unroll
             for (int i = 0; i < kSubs; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    lv[i][h] = fmaxf(lg2(x.vs[i][h]), -100.0f);  // weights stay finite; such values are nothing in 16 bits
+                    vs[i][h] = x.vs[i][h];
+                    one |= vs[i][h] == 1.0f;
+                }
+            if (__any_sync(0xffffffffu, one)) {
+#pragma unroll
+                for (int i = 0; i < kSubs; ++i) {
+                    unsigned any = 0;  // a bit for each of the 16 keys
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint4 y = x.v[i][j][0];
+                        if ((y.x | y.y | y.z | y.w) & 0x7F7F7F7Fu) any |= 1u << (2 * t + (j >> 1) * 8 + (j & 1));
+                    }
+                    any = __reduce_or_sync(0xffffffffu, any);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (!(any >> (g + 8 * h) & 1u)) vs[i][h] = 0.0f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kSubs; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    lv[i][h] = fmaxf(lg2(vs[i][h]), -100.0f);  // weights stay finite; such values are nothing in 16 bits
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -390,8 +416,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
                     l[n][0] += e0;
                     l[n][1] += e1;
                     if constexpr (kFp8) {
-                        e0 *= x.vs[i][h];
-                        e1 *= x.vs[i][h];
+                        e0 *= vs[i][h];
+                        e1 *= vs[i][h];
                     }
                     b[n][h] = transpose8(pack16<kMmaBf16>(e0, e1));
                 }
