@@ -1121,6 +1121,9 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
         };
 
         const int step = w.two ? 1 : 2, jn = w.two && pipe == 0 ? w.cnt0 : n;
+        // A pipe without a tile (none of its rows sees a key) waits for no product, and
+        // the results go where the other warps may still be putting queries.
+        if (jn == 0 && n > 0 && !mbar_wait_warp(qfull, 0, abort_flag) && lane == 0) attn_error(kErrWaitDequant, abort_flag);
         int j = w.two ? 0 : pipe;
         for (; j < jn; j += step, ++done) {
             if (!mbar_wait_warp(sfull(pipe), static_cast<uint32_t>(done & 1), abort_flag)) {
