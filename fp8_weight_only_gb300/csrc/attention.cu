@@ -41,7 +41,11 @@
 // adding to it.  p stays below 2^8, and the sums are fp32.
 //
 // e4m3 caches: codes convert exactly; the key scales multiply the columns of S
-// and the value scales those of P, in fp32, so no scale is ever rounded.
+// and the value scales those of P, in fp32, so what is rounded to 16 bits is a
+// weight times its value scale.  With fp16 weights that product has to stay among
+// fp16's numbers whatever the scales are, so m is then the reference of p v_scale
+// (the maximum is taken of exponents plus log2 v_scale), and the sum of the p
+// alone, which is fp32, takes what stands against it.  bf16 has the range anyway.
 //
 // Long caches and few rows: the CTAs of a cluster take equal runs of key tiles
 // and join their (m, sum, O) in distributed shared memory, in rank order.
@@ -88,11 +92,12 @@ struct AttnSmem {
     // with 6 it is key tile m - 3, multiplied after value tile m - 5 was.
     static constexpr int kLoaders = kFp8 ? 2 : 3;                // warps that load: kLoadWarp and those after kMmaWarp
     static constexpr int kScaleSlots = DP == 128 ? 4 : 8;
+    static constexpr int kScaleWords = 3 * kKeys + 64;           // of a slot (4 of the 64 are used)
     static constexpr uint32_t kQOff = 0;                         // two row tiles; later a 128 x DP fp32 partial
     static constexpr uint32_t kRingOff = 2 * kTileBytes;
     static constexpr uint32_t kRawOff = kRingOff + kStages * kTileBytes;
-    static constexpr uint32_t kScaleOff = kRawOff + kRaw * kRawBytes;  // [slot][k, v][128] fp32
-    static constexpr uint32_t kMlOff = kScaleOff + (kFp8 ? kScaleSlots * 2 * kKeys * 4 : 0);
+    static constexpr uint32_t kScaleOff = kRawOff + kRaw * kRawBytes;  // [slot][k, v, log2 v][128], each warp's largest log2 v [4], fp32
+    static constexpr uint32_t kMlOff = kScaleOff + (kFp8 ? kScaleSlots * kScaleWords * 4 : 0);
     static constexpr uint32_t kJoinedOff = kMlOff + kRows * 8;   // (m, l) of the CTA's rows, for the cluster
     static constexpr uint32_t kBarOff = kJoinedOff + kRows * 8;
     // full, empty [kStages] | rawfull, rawempty [kRaw] | sfull, pfull, ofull [2] | qfull | joinfull, joinfree | drain | tail
@@ -330,16 +335,32 @@ struct Join {
     float m, l;
 };
 
-template <int DP, bool kFp8, bool kBf16>
-struct Weights {
-    // fp16 weights with e4m3 scales: p * v_scale * 2^4 keeps the products of
-    // small scales among fp16's normal numbers, and with p below 2^4 it cannot
-    // overflow (scales reach 65504 / 448 = 146.2 for fp16 values).  No slack and
-    // 2^8 would reach smaller scales, but rescales O at most of the first tiles.
-    static constexpr bool kScaledF16 = kFp8 && !kBf16;
-    static constexpr float kSlack = kScaledF16 ? 4.0f : 8.0f;
-    static constexpr float kScale = kScaledF16 ? 16.0f : 1.0f;
-};
+// The largest of a row's exponents plus log2 of the value scales, less m, over
+// `width` columns of scores from taddr on (ksc: their first key scale); top, bot:
+// the last and first column that the row sees.  Out of line, for the loop over the
+// tiles has no registers to spare for it (773 us for the chunks of codes that take
+// 696 so).
+__device__ __noinline__ float scaled_peak(uint32_t taddr, uint32_t ksc, int width, float less_m, bool masked, int top, int bot) {
+    float mx = kNegInf, my = kNegInf;
+    const uint64_t less_m2 = pack2(less_m, less_m);
+#pragma unroll 1
+    for (int b = 0; b < width; b += 16) {
+        uint32_t v[16];
+        tmem_ld_x16_sync(taddr + b, v);
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            const float4 f = lds_f4(ksc + (b + i) * 4), g = lds_f4(ksc + (2 * kKeys + b + i) * 4);
+            uint64_t x = fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), pack2(f.x, f.y), less_m2);
+            uint64_t y = fma2(pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), pack2(f.z, f.w), less_m2);
+            x = add2(x, pack2(g.x, g.y));
+            y = add2(y, pack2(g.z, g.w));
+            auto seen = [&](int e, float z) { return masked && (b + i + e > top || b + i + e < bot) ? kNegInf : z; };
+            mx = max3(mx, seen(0, lo2(x)), seen(1, hi2(x)));
+            my = max3(my, seen(2, lo2(y)), seen(3, hi2(y)));
+        }
+    }
+    return fmaxf(mx, my);
+}
 
 // Partial results through shared memory to the output: the pipes', the copies'
 // and then the cluster's.  Rounds: one, or one for each row tile.  A function of
@@ -348,7 +369,6 @@ struct Weights {
 template <int DP, bool kBf16, bool kFp8>
 __device__ __noinline__ void join_results(const AttnParams& p, const Work& w, const Join& a, volatile int* abort_flag) {
     using L = AttnSmem<DP, kFp8>;
-    constexpr float kUnscale = 1.0f / Weights<DP, kFp8, kBf16>::kScale;
     const uint32_t sbase = a.sbase, t_o = a.t_o, joinfull = a.joinfull, joinfree = a.joinfree;
     const int rank = a.rank, tid = threadIdx.x, split = a.split, done = a.done, per_copy = kRows / split;
     constexpr int kHalf = DP / 2;          // output columns a thread
@@ -400,7 +420,7 @@ __device__ __noinline__ void join_results(const AttnParams& p, const Work& w, co
                 const float a0 = mine_l != 0.0f ? ex2(m - top) : 0.0f;
                 const float a1 = other.y != 0.0f ? ex2(other.x - top) : 0.0f;
                 const float sum = a0 * mine_l + a1 * other.y;
-                const float inv = kUnscale * weight_inverse(sum, sees(r));
+                const float inv = weight_inverse(sum, sees(r));
                 // both threads of the row have read its (m, l)
                 asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
 #pragma unroll
@@ -465,7 +485,7 @@ __device__ __noinline__ void join_results(const AttnParams& p, const Work& w, co
                 acc[3] = fmaf(__uint_as_float(v.w), a, acc[3]);
             }
             if (p.cl == 1) {
-                const float inv = kUnscale * weight_inverse(sum, sees(round * kRows + row));
+                const float inv = weight_inverse(sum, sees(round * kRows + row));
                 if (ch * 4 < p.head_dim)
                     *reinterpret_cast<uint2*>(out_at(w.row0 + row) + ch * 4) =
                         make_uint2(pack16<kBf16>(acc[0] * inv, acc[1] * inv), pack16<kBf16>(acc[2] * inv, acc[3] * inv));
@@ -533,7 +553,7 @@ __device__ __noinline__ void join_results(const AttnParams& p, const Work& w, co
                     acc.z = acc.z * x + o.z * y;
                     acc.w = acc.w * x + o.w * y;
                 }
-                const float inv = kUnscale * weight_inverse(sum, sees(round * kRows + row));
+                const float inv = weight_inverse(sum, sees(round * kRows + row));
                 if (live && k0 == 0 && ch * 4 < p.head_dim)
                     *reinterpret_cast<uint2*>(out_at(w.row0 + round * kRows + row) + ch * 4) =
                         make_uint2(pack16<kBf16>(acc.x * inv, acc.y * inv), pack16<kBf16>(acc.z * inv, acc.w * inv));
@@ -569,7 +589,8 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr float kSlack = Weights<DP, kFp8, kBf16>::kSlack, kPScale = Weights<DP, kFp8, kBf16>::kScale;
+    constexpr float kSlack = 8.0f;
+    constexpr bool kScaledF16 = kFp8 && !kBf16;  // m is the reference of weight times value scale
 
     if (warp == kMmaWarp) {
         tmem_alloc(smem_u32(tmem_slot), kAttnTmemCols);
@@ -835,6 +856,21 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                 const int64_t at = head_scales + pg * page_scales + (((w.t0 + j) * kKeys + r) & (p.page_size - 1));
                 return make_float2(p.k_scales[at], p.v_scales[at]);
             };
+            // Whether a value row is all zeros.  Its scale is 1 then, as if its values
+            // reached 448, and a large score there would set the reference of the weights
+            // of small values.  Its codes are looked at where they are, ahead of their
+            // tile: rows of other values that have this very scale mostly end with the
+            // first chunk.
+            auto zero_row = [&](int j) {
+                const int pg = page_at(j), slot = ((w.t0 + j) * kKeys + r) & (p.page_size - 1);
+                if (pg < 0 || pg >= p.num_pages) return true;
+                const uint8_t* at = static_cast<const uint8_t*>(p.v) + pg * p.page_stride + w.head * p.head_stride + slot * p.token_stride;
+                for (int u = 0; u < p.head_dim; u += 16) {
+                    const uint4 y = *reinterpret_cast<const uint4*>(at + u);
+                    if ((y.x | y.y | y.z | y.w) & 0x7F7F7F7Fu) return false;
+                }
+                return true;
+            };
             float2 next = scales_at(0, page_at(0));
             int page = page_at(1);
             uint32_t s = 0, phase = 0, d = 0;        // raw stage of the position, use of it, ring stage
@@ -888,9 +924,18 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                     sts128(sub + (((2 * u + 1) & 7) ^ swz) * 16, v[4], v[5], v[6], v[7]);
                 }
                 if (is_k) {  // the softmax needs both as soon as the tile's scores are there
-                    float* sc = reinterpret_cast<float*>(smem + L::kScaleOff) + (j % L::kScaleSlots) * 2 * kKeys + r;
+                    float* sc = reinterpret_cast<float*>(smem + L::kScaleOff) + (j % L::kScaleSlots) * L::kScaleWords + r;
                     sc[0] = scale.x * p.c;
-                    sc[kKeys] = scale.y * kPScale;
+                    if constexpr (kScaledF16) {
+                        const float vs = scale.y == 1.0f && zero_row(j) ? 0.0f : scale.y;
+                        sc[kKeys] = vs;
+                        const float log2_vs = log2_scale(vs);  // above -128: the sum's bits are in its order
+                        sc[2 * kKeys] = log2_vs;
+                        const int top = __reduce_max_sync(0xffffffffu, __float_as_int(log2_vs + 128.0f));
+                        if (lane == 0) sc[3 * kKeys - r + (warp & 3)] = __int_as_float(top) - 128.0f;
+                    } else {
+                        sc[kKeys] = scale.y;
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -975,7 +1020,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             const int key0 = (w.t0 + j) * kKeys + cbeg;
             const bool masked = key0 + W - 1 > warp_hi || key0 < warp_lo;
             // address taken after the wait, so the reads below stay behind it
-            uint32_t ksc = sbase + L::kScaleOff + (j % L::kScaleSlots) * (2 * kKeys * 4) + cbeg * 4;
+            uint32_t ksc = sbase + L::kScaleOff + (j % L::kScaleSlots) * (L::kScaleWords * 4) + cbeg * 4;
             asm volatile("" : "+r"(ksc)::"memory");
             // kStep exponents from the b-th on: scores times c (with codes, times key
             // scales that hold it) less m, masked
@@ -1015,24 +1060,32 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                 return fmaxf(x, other);
             };
             float mx = kNegInf, my = kNegInf;
-            if (done == 0) {  // the first tile's maximum is the first m
+            // The maximum of what m is the reference of, less m.
+            auto peak = [&](float less_m) {
+                if constexpr (kScaledF16) return scaled_peak(t_s + cbeg, ksc, W, less_m, masked, hi - key0, lo - key0);
+                const uint64_t less_m2 = pack2(less_m, less_m);
 #pragma unroll 1
                 for (int b = 0; b < W; b += kStep) {
                     uint32_t v[kStep];
-                    exponents(b, 0ull, v);
+                    exponents(b, less_m2, v);
 #pragma unroll
                     for (int i = 0; i < kStep; i += 4) {
                         mx = max3(mx, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
                         my = max3(my, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
                     }
                 }
-                m = exchange(fmaxf(mx, my));
-            }
+                return fmaxf(mx, my);
+            };
+            if (done == 0) m = exchange(peak(0.0f));  // the first tile's maximum is the first m
             uint32_t o[W / 2];
             uint64_t l0, l1;
             // The weights are taken with the m of the tiles before, without waiting
             // for this one's maximum.  Where that turns out to lie too far above, m
             // moves and they are taken again; both threads of a row have the same m.
+            // With kScaledF16 the largest exponent and the tile's largest scale bound what
+            // m is the reference of; its own maximum, which reads log2 of each scale, is
+            // looked for where that bound lies above only (in every tile: 766 us for the
+            // chunks of codes that take 696 so).
             auto weights = [&] {
                 const float mc = m == kNegInf ? 0.0f : -m;  // while nothing was seen, exponents are not reduced
                 const uint64_t mc2 = pack2(mc, mc);
@@ -1088,9 +1141,14 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             // 398 us for the 8192 tokens that take 382 so, the registers run short.)
             weights();
             tc_fence_before();
+            if constexpr (kScaledF16) {
+                const float4 f = lds_f4(ksc + (3 * kKeys - cbeg) * 4);
+                mx += max3(fmaxf(f.x, f.y), f.z, f.w);
+            }
             const bool moves = bar_red_or(pair, 64, valid && mx > (m == kNegInf ? kNegInf : kSlack));
             tc_fence_after();
             if (moves) {
+                if constexpr (kScaledF16) mx = peak(m == kNegInf ? 0.0f : -m);
                 const float top = exchange(mx) + (m == kNegInf ? 0.0f : m);
                 float alpha = 1.0f;
                 if (valid && top - m > kSlack) {  // -inf - -inf: no
@@ -1173,7 +1231,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                 // reads any more (half a row a warp): 16-byte chunks swizzled by the row,
                 // then 16 bytes a lane along the rows to memory.
                 constexpr int kHalf = DP / 2, kChunks = kHalf / 8, kRowsAtOnce = 32 / kChunks;
-                const float inv = weight_inverse(kPScale * l, hi >= 0);
+                const float inv = weight_inverse(l, hi >= 0);
                 const uint32_t mine = sbase + L::kQOff + pipe * L::kTileBytes + (half * 4 + quarter) * (32 * kHalf * 2);
 #pragma unroll
                 for (int b = 0; b < kHalf; b += 32) {

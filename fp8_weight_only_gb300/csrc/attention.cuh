@@ -173,6 +173,15 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// log2 of a value scale for the reference of weight times value scale, with a
+// floor (scales of 0 too): the weight alone, up to this much larger, stays finite,
+// and smaller values are nothing in 16 bits.
+__device__ __forceinline__ float log2_scale(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return fmaxf(y, -100.0f);
+}
+
 // Two fp32 -> packed 16-bit pair (first in the low half), rounded to nearest.
 template <bool kBf16>
 __device__ __forceinline__ uint32_t pack16(float first, float second) {

@@ -58,12 +58,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint4& a, uint32_t
             : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ float lg2(float x) {
-    float y;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // An 8 x 8 matrix of 16-bit values, a row to four lanes: its transpose.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
@@ -376,7 +370,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
             for (int i = 0; i < kSubs; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    lv[i][h] = fmaxf(lg2(vs[i][h]), -100.0f);  // weights stay finite; such values are nothing in 16 bits
+                    lv[i][h] = log2_scale(vs[i][h]);
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll

@@ -96,8 +96,8 @@ def tail(length, kv, dim, down, seed=2):
     return k, v
 
 
-# new tokens and query heads a key head: few rows, few rows of two tiles of 8
-ROWS = [(1, 4), (3, 5)]
+# new tokens and query heads a key head: few rows, few rows of two tiles of 8, a tile of many, a tile a pipe
+ROWS = [(1, 4), (3, 5), (60, 1), (200, 2)]
 FORMS = [("bf16", False), ("f16", False), ("bf16", True), ("f16", True)]
 
 
