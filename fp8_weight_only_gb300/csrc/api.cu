@@ -329,6 +329,9 @@ fp8w_status fp8w_paged_attention(const void* q, int act_dtype, int64_t tokens, i
     if ((st = check_rows(q, q_heads, cache->head_dim, q_stride)) != FP8W_OK) return st;
     if ((st = check_rows(out, q_heads, cache->head_dim, out_stride)) != FP8W_OK) return st;
     if (!aligned(block_table, 4) || !aligned(lens, 4) || (starts && !aligned(starts, 4))) return FP8W_ERR_ALIGN;
+    // bounds that bound nothing, so that no product or sum of them leaves its type
+    if (max_new > tokens) max_new = tokens;
+    if (window >= table_width * cache->page_size) window = 0;
     const fp8w::AttentionArgs a{q,    act_dtype, tokens, q_heads, q_stride, cache,   block_table, table_width, lens,
                                 starts, seqs,    scale,  window,  max_new,  max_len, out,         out_stride};
     return cuda_status(fp8w::launch_attention(a, static_cast<cudaStream_t>(stream)), "fp8w_paged_attention launch");

@@ -469,8 +469,9 @@ FP8W_API fp8w_status fp8w_rope_append(const void *q, const void *k, const void *
  *   scale        finite and > 0.
  *   window       0 (all positions) or the number of positions a token sees.
  *   max_new      no sequence has more new tokens than this; 0: not known.
- *                Sizes the launch; more is recorded (fp8w_device_error), and
- *                rows are then left unwritten.
+ *                Sizes the launch (a bound above `tokens` is none).  Where a
+ *                sequence has more, rows may be left unwritten; that is
+ *                recorded (fp8w_device_error).
  *   max_len      about the largest of lens; 0: table_width * page_size.  Guides
  *                how the work is split and nothing else.
  *   out          like q, with out_stride (output); it may not overlap q.

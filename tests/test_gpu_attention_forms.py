@@ -1,8 +1,10 @@
 """GPU tests of the forms of paged attention that a call with max_new reaches:
 few rows in tiles of 16, one tile and several a sequence, with 16-bit pages and
-codes, windows and splits over a cluster."""
+codes, windows and splits over a cluster; hints beyond all bounds."""
+import numpy as np
 import pytest
 
+from tests.attention_reference import Paged, bits
 from tests.test_gpu_attention import run
 
 torch = pytest.importorskip("torch")
@@ -11,6 +13,9 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():  # pragma: no cover
     pytest.skip("needs a GPU", allow_module_level=True)
 
+import fp8_weight_only_gb300 as fw  # noqa: E402
+
+DEV = torch.device("cuda:0")
 FORMS = [("bf16", False), ("f16", False), ("bf16", True), ("f16", True)]
 
 
@@ -59,3 +64,23 @@ def test_a_tile_of_rows_before_the_first_position_beside_one_that_sees_keys(dim,
         _, _, out = run(new, lens, 8, 1, dim, 16, dtype, codes, seed=seed)
         for b, t in enumerate(lens):
             assert not out[256 * b:256 * (b + 1) - t].any()
+
+
+@pytest.mark.parametrize("max_new", [2 ** 62, 2 ** 62 + 1, 2 ** 63 - 1])
+def test_a_bound_on_new_tokens_above_all_tokens_is_no_bound(max_new):
+    for new, lens in (([1, 3], [700, 90]), ([200, 7], [300, 90])):
+        _, _, want = run(new, lens, 2, 4, 64, 16)
+        _, _, got = run(new, lens, 2, 4, 64, 16, max_new=max_new)
+        assert np.array_equal(bits(got), bits(want))
+
+
+@pytest.mark.parametrize("new,lens", [([1, 1], [9000, 0]), ([3, 5], [700, 2]), ([200, 300], [9000, 20])])
+def test_a_window_above_all_positions_is_none(new, lens):
+    paged = Paged(torch, fw, 5, lens, 1, 64, 16, "bf16", False, "heads")
+    q = torch.randn((sum(new), 4, 64), device=DEV).bfloat16()
+    starts = torch.tensor([0] + new, device=DEV).cumsum(0).int()
+    want = fw.paged_attention(q, paged.cache, paged.table, paged.lens_t, starts=starts)
+    for window in (9100, 2 ** 31, 2 ** 62, 2 ** 63 - 1):
+        got = fw.paged_attention(q, paged.cache, paged.table, paged.lens_t, starts=starts, window=window)
+        assert np.array_equal(bits(got), bits(want))
+    assert fw.device_error() == 0
