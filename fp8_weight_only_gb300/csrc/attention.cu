@@ -38,7 +38,8 @@
 // 52 instead of 39 for mixed lengths; two CTAs a tile's keys, joined: 782.
 // The reference m moves only when a row's maximum has grown by more than
 // 2^8 (kSlack) over it: then the row's O is rescaled, after the MMA that is
-// adding to it.  p stays below 2^8, and the sums are fp32.
+// adding to it.  p stays below 2^8 (fp16: all of them 2^kLiftF16 times as large),
+// and the sums are fp32.
 //
 // e4m3 caches: codes convert exactly; the key scales multiply the columns of S
 // and the value scales those of P, in fp32, so what is rounded to 16 bits is a
@@ -589,7 +590,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr float kSlack = 8.0f;
+    constexpr float kSlack = 8.0f, kLift = kBf16 ? 0.0f : kLiftF16;
     constexpr bool kScaledF16 = kFp8 && !kBf16;  // m is the reference of weight times value scale
 
     if (warp == kMmaWarp) {
@@ -1004,7 +1005,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
         const uint32_t t_s = tmem + tq + pipe * kKeys, t_o = tmem + tq + 2 * kKeys + pipe * DP + half * (DP / 2);
         const float c = p.c;
         const uint64_t c2 = pack2(c, c);
-        float m = kNegInf, l = 0.0f;  // the row's reference, in exponents of two, and its sum
+        float m = kNegInf, l = 0.0f;  // the row's reference, in exponents of two and less kLift, and its sum
         int done = 0;                 // tiles of this pipe
         bool ok = true;
 
@@ -1061,13 +1062,13 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             };
             float mx = kNegInf, my = kNegInf;
             // The maximum of what m is the reference of, less m.
-            auto peak = [&](float less_m) {
-                if constexpr (kScaledF16) return scaled_peak(t_s + cbeg, ksc, W, less_m, masked, hi - key0, lo - key0);
-                const uint64_t less_m2 = pack2(less_m, less_m);
+            auto peak = [&](float less) {
+                if constexpr (kScaledF16) return scaled_peak(t_s + cbeg, ksc, W, less, masked, hi - key0, lo - key0);
+                const uint64_t less2 = pack2(less, less);
 #pragma unroll 1
                 for (int b = 0; b < W; b += kStep) {
                     uint32_t v[kStep];
-                    exponents(b, less_m2, v);
+                    exponents(b, less2, v);
 #pragma unroll
                     for (int i = 0; i < kStep; i += 4) {
                         mx = max3(mx, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
@@ -1076,7 +1077,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                 }
                 return fmaxf(mx, my);
             };
-            if (done == 0) m = exchange(peak(0.0f));  // the first tile's maximum is the first m
+            if (done == 0) m = exchange(peak(0.0f)) - kLift;  // the first tile's maximum is the first m
             uint32_t o[W / 2];
             uint64_t l0, l1;
             // The weights are taken with the m of the tiles before, without waiting
@@ -1145,11 +1146,11 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                 const float4 f = lds_f4(ksc + (3 * kKeys - cbeg) * 4);
                 mx += max3(fmaxf(f.x, f.y), f.z, f.w);
             }
-            const bool moves = bar_red_or(pair, 64, valid && mx > (m == kNegInf ? kNegInf : kSlack));
+            const bool moves = bar_red_or(pair, 64, valid && mx > (m == kNegInf ? kNegInf : kSlack + kLift));
             tc_fence_after();
             if (moves) {
                 if constexpr (kScaledF16) mx = peak(m == kNegInf ? 0.0f : -m);
-                const float top = exchange(mx) + (m == kNegInf ? 0.0f : m);
+                const float top = exchange(mx) + (m == kNegInf ? 0.0f : m) - kLift;
                 float alpha = 1.0f;
                 if (valid && top - m > kSlack) {  // -inf - -inf: no
                     alpha = ex2(m - top);  // 0 while nothing was seen

@@ -173,13 +173,20 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// fp16 weights (with codes: weights times value scales) are taken 2^kLiftF16 times
+// as large, sums of them too: with references that lag by 2^8 at most they reach
+// 2^15, and what a weight loses below fp16's normal numbers is at most 2^-32 of the
+// largest (2^-25 without; a long tail of small weights may be all there is, where
+// the largest ones' values are zero).
+constexpr float kLiftF16 = 7.0f;
+
 // log2 of a value scale for the reference of weight times value scale, with a
-// floor (scales of 0 too): the weight alone, up to this much larger, stays finite,
-// and smaller values are nothing in 16 bits.
+// floor (scales of 0 too): the sum of the weights alone, up to this much larger,
+// stays finite, and smaller values are nothing in 16 bits.
 __device__ __forceinline__ float log2_scale(float x) {
     float y;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return fmaxf(y, -100.0f);
+    return fmaxf(y, -90.0f);
 }
 
 // Two fp32 -> packed 16-bit pair (first in the low half), rounded to nearest.

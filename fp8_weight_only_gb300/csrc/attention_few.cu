@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
     // instruction makes two of them, and the weights round to 11 bits.  bf16
     // queries go over exactly but for a power of two a row (below).
     constexpr bool kMmaBf16 = kBf16 && !kFp8;
-    constexpr float kSlack = 8.0f;
+    constexpr float kSlack = 8.0f, kLift = kMmaBf16 ? 0.0f : kLiftF16;
     __shared__ __align__(16) uint8_t smem[S::kBytes];
     const uint32_t sbase = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
             uint32_t b[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const float ref0 = m[n][0] == kNegInf ? 0.0f : m[n][0], ref1 = m[n][1] == kNegInf ? 0.0f : m[n][1];
+                const float ref0 = m[n][0] == kNegInf ? 0.0f : m[n][0] - kLift, ref1 = m[n][1] == kNegInf ? 0.0f : m[n][1] - kLift;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float e0 = ex2(s[i][n][2 * h] - ref0), e1 = ex2(s[i][n][2 * h + 1] - ref1);

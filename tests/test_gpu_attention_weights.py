@@ -4,12 +4,12 @@ from token to token and head to head, keys of the largest scores whose values
 are zero.
 
 Weights that are held in fp16 are off by 2^-11 of themselves or, below its
-normal range, by 2^-25, where the largest weight (with codes: weight times value
-scale) is at least 1.  So the bound is that of attention_reference with the term
-for weights below the normal range replaced by  keys 2^-25 max_j p_j max_d |v_jd|
-(with 16-bit pages, where it is the weight alone that is held: keys 2^-25 max_j
-p_j max |v|).  The bound shrinks with the values.  fp16 outputs below its normal
-range are off by 2^-25."""
+normal range, by 2^-25 of a unit of which the largest weight (with codes:
+weight times value) has at least 2^7: by 2^-32 of that one.  So the bound is
+that of attention_reference with the term for weights below the normal range
+replaced by  keys 2^-32 max_j p_j max_d |v_jd|  (with 16-bit pages, where it is
+the weight alone that is held: keys 2^-32 max_j p_j max |v|).  The bound shrinks
+with the values.  fp16 outputs below its normal range are off by 2^-25."""
 import pytest
 
 from tests.attention_reference import ROUND, check
@@ -74,7 +74,7 @@ def compare(k, v, new, group, dtype, codes, page=32):
         e_s = (dim + 8) * 2.0 ** -23 * 4.0 * hk[:, h, 0].abs().max() + 2.0 ** -18
         t = u * (a + o.abs()) + 2 * e_s * a + length * 2.0 ** -23 * a
         if dtype == "f16" or codes:
-            t = t + length * 2.0 ** -25 * big[:, None]
+            t = t + length * 2.0 ** -32 * big[:, None]
         if dtype == "f16":
             t = t + 2.0 ** -25
         for g in range(group):
@@ -146,6 +146,15 @@ def test_value_scale_of_exactly_one(codes, new, group):
     v = torch.where(v == 1.0, 448.0, v)
     v[::3] *= 1e-3
     compare(k, v, new, group, "f16", codes)
+
+
+@pytest.mark.parametrize("new,group", ROWS)
+@pytest.mark.parametrize("codes", [False, True])
+def test_weights_below_2_to_the_minus_25(codes, new, group):
+    # the dominant keys, one in 16, have zero values: what the output has comes from the others
+    k, v = tail(512, 2, 64, 17.6)
+    k[7::16, :, 0], v[7::16], v[256], v[170] = 0.0, 0.0, 0.0, 0.0
+    compare(k, v * 2.0 ** 15, new, group, "f16", codes)
 
 
 def test_bf16_values_of_extreme_size():
