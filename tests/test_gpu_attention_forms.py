@@ -84,3 +84,10 @@ def test_a_window_above_all_positions_is_none(new, lens):
         got = fw.paged_attention(q, paged.cache, paged.table, paged.lens_t, starts=starts, window=window)
         assert np.array_equal(bits(got), bits(want))
     assert fw.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype,codes", FORMS)
+@pytest.mark.parametrize("dim", [16, 32, 48])
+def test_many_rows_of_small_heads(dim, dtype, codes):
+    run([300, 20], [300, 700], 2, 3, dim, 16, dtype, codes)
+    run([64], [5000], 1, 1, dim, 128, dtype, codes, layout="tokens")
