@@ -337,6 +337,7 @@ class Rope:
         if not 1 <= len(sections) <= 4:
             raise ValueError("1 to 4 sections, got %d" % len(sections))
         self.table = table
+        self.index = table.get_device()
         self.axes = len(sections)
         self.spec = RopeSpec(table.data_ptr(), table.shape[0], table.shape[1], 1 if interleaved else 0, self.axes,
                              (ctypes.c_int * 4)(*sections))
@@ -446,6 +447,8 @@ def rope(x, positions, rope, out=None):
         out, os_ = _empty_like(x, memory_format=_dense), heads * dim
     else:
         os_ = _rows("out", out, dev, dtype, shape)
+    if rope.index != dev:
+        raise TypeError("the rope's table must be on the operands' device")
     axes = rope.axes
     pos = _index("positions", positions, _int32, (tokens,) if axes == 1 and positions.dim() == 1 else (axes, tokens), dev)
     st = _lib.fp8w_rope(x.data_ptr(), act, tokens, heads, dim, xs, pos, rope._ref, out.data_ptr(), os_, _stream_of(dev))
@@ -474,6 +477,8 @@ def rope_append(q, k, v, slots, cache, positions=None, rope=None, out=None):
     if (rope is None) != (positions is None):
         raise ValueError("positions and rope come together")
     if rope is not None:
+        if rope.index != dev:
+            raise TypeError("the rope's table must be on the operands' device")
         axes, spec = rope.axes, rope._ref
         pos = _index("positions", positions, _int32, (tokens,) if axes == 1 and positions.dim() == 1 else (axes, tokens), dev)
     if q is not None:
