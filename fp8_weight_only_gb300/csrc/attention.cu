@@ -21,16 +21,19 @@
 //   warps 16, 18, 19 (with codes 16, 18) TMA producers of key and value tiles
 //   warp 17         MMA issue, one thread; owns TMEM
 //   warps 20-23     (e4m3 cache) codes -> 16-bit operand tiles
-// What bounds it: 8192 new tokens, 32 query heads of 128, 16-slot pages take 380
-// us, 1446 TFLOP/s, 78% of the measured rate.  Per key tile of 256 rows the
-// products need 2048 cycles of the 3050 it takes; without the softmax's work 2700,
-// without products and work 1900: a pipe's scores, weights and products wait for
-// one another, and every instruction of the one thread that issues and of the
-// producers waits behind sixteen softmax warps, so these loops are kept short.
-// Heads of 64: 341 us, 43%: the softmax is the same for half the products.
-// Codes: 688 us for chunks of 500 to 1030 tokens over 9000 to 16000, 47%: the
-// softmax multiplies both scales too, and the conversion shares its schedulers;
-// 17% is the last wave (352 row tiles on 152 SMs).
+// What bounds it: 8192 new tokens, 32 query heads of 128, 16-slot pages take 387
+// us, 1421 TFLOP/s, 74% of the measured rate (calls back to back for longer: 407
+// us).  Per key tile of 256 rows the products need 2048 cycles of the 3100 it
+// takes; without the softmax's work 2700, without products and work 1900: a pipe's
+// scores, weights and products wait for one another, and every instruction of the
+// one thread that issues and of the producers waits behind sixteen softmax warps,
+// so these loops are kept short.  Heads of 64: 351 us, 41%: the softmax is the same
+// for half the products.  Heads of 80 and 96 are computed as heads of 128: 382 and
+// 384 us, 47% and 56%.
+// Codes: 697 us for chunks of 500 to 1030 tokens over 9000 to 16000, 45%: the
+// softmax multiplies both scales too, and the conversion shares its schedulers
+// (bf16, whose conversion takes more instructions: 734); 17% is the last wave (352
+// row tiles on 152 SMs).
 // Measured and not kept for the prompt: a pair of CTAs sharing products of 256
 // rows (cta_group::2, half of each key and value tile a CTA): 537 us when one CTA
 // took 455, each product waiting for both CTAs' softmax; scores of 64 keys at a
@@ -72,9 +75,9 @@ constexpr int kRows = 128;            // rows a tile (TMEM lanes)
 constexpr int kMaxAttnCluster = 16;
 // Up to this many rows a key head (new tokens x its query heads) the kernel for
 // few rows reads the cache faster.  It takes 16 rows at a time: with more a 16-bit
-// cache is read twice (a decode batch of 1.2 GB, 16 rows: 244 us against 251 here,
-// 24: 373 against 254), a cache of codes twice or thrice is still less than here
-// (24: 275 against 395; 48: 378 against 410; 64: 478 against 414).
+// cache is read twice (a decode batch of 1.2 GB, 16 rows: 248 us against 254 here,
+// 24: 380 against 255), a cache of codes twice or thrice is still less than here
+// (24: 287 against 395; 48: 388 against 408; 64: 491 against 411).
 constexpr int kFewRows = 16, kFewRowsCodes = 48;
 constexpr uint32_t kAttnTmemCols = 512;
 constexpr int kSoftmaxThreads = 512;   // sixteen warps
@@ -861,7 +864,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             // reached 448, and a large score there would set the reference of the weights
             // of small values.  Its codes are looked at where they are, ahead of their
             // tile: rows of other values that have this very scale mostly end with the
-            // first chunk.
+            // first chunk (the chunks of codes with this scale in all slots: 812 us, else 697).
             auto zero_row = [&](int j) {
                 const int pg = page_at(j), slot = ((w.t0 + j) * kKeys + r) & (p.page_size - 1);
                 if (pg < 0 || pg >= p.num_pages) return true;
@@ -1204,7 +1207,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
         }
         // The tiles of a warp that gave up: softmax_tile's barriers, for the row's other
         // warp may still take them.  (Going on in the loop above without its waits: 418 us
-        // for the 8192 tokens that take 403 so.)
+        // for the 8192 tokens that take 406 so.)
         for (; j < jn && busy; j += step, ++done) {
             if (done == 0) asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
             if (bar_red_or(pair, 64, false)) {

@@ -25,12 +25,13 @@
 // Each warp has its own (m, l, O); a CTA's warps join theirs in shared memory
 // and a cluster's CTAs theirs in distributed shared memory, in rank order.
 //
-// Measured: a decode batch of 96 sequences (1.2 GB of a 16-bit cache) 220 us, 5.5
+// Measured: a decode batch of 96 sequences (1.2 GB of a 16-bit cache) 224 us, 5.4
 // TB/s, 81% of the measured copy rate: the last CTAs of uneven sequences and each
-// one's start, not the loop.  The same of codes: 142 us, 65%: conversions, 45% of
-// the ALU pipe.  Two sequences of 90 and 131 thousand tokens of codes: 139 us, 53%:
-// besides, 16 (sequence, head) pairs of at most 16 CTAs are 1.7 CTAs an SM.
-// One short sequence: 7 us, four dependent reads of memory and a launch.
+// one's start, not the loop.  The same of codes: 146 us, 64%: conversions, 45% of
+// the ALU pipe.  Heads of 64: 123 us, 73%, and of codes 113, 43%.  Two sequences of
+// 90 and 131 thousand tokens of codes: 144 us, 52%: besides, 16 (sequence, head)
+// pairs of at most 16 CTAs are 1.7 CTAs an SM.
+// One short sequence: 8 us, four dependent reads of memory and a launch.
 #include <mutex>
 
 #include "attention.cuh"

@@ -19,9 +19,9 @@
 // asked for, and its cosines and sines stay in registers over the heads.  All
 // loads are ordinary ones, none of the read-only path: the kernel starts while
 // those ahead of it in the stream still write, and its wait orders ordinary loads.
-// 16384 tokens of 40 heads of 128, three axes: 58.5 us, 5.9 TB/s (87% of the
-// measured copy rate), one axis 53.6 us; 8192 tokens appended 33.9 us (88%), as
-// codes 41.6 us (66%: sixteen IEEE divisions a lane); one token 1.8 us.
+// 16384 tokens of 40 heads of 128, three axes: 59.3 us, 5.8 TB/s (87% of the
+// measured copy rate), one axis 54.8 us; 8192 tokens appended 34.6 us (88%), as
+// codes 42.4 us (66%: sixteen IEEE divisions a lane); one token 1.7 us.
 #include "fp8w_device.cuh"
 #include "fp8w_internal.h"
 

@@ -477,7 +477,10 @@ FP8W_API fp8w_status fp8w_rope_append(const void *q, const void *k, const void *
  *   out          like q, with out_stride (output); it may not overlap q.
  * Scores, softmax and sums are fp32; the softmax weights are rounded to 16 bits
  * for the second product: to act_dtype, or with codes and few rows to fp16.
- * e4m3 scales multiply scores and weights in fp32.  One rounding at the end.
+ * e4m3 scales multiply scores and weights in fp32, the weights before they are
+ * rounded.  Below its normal numbers fp16 takes at most 2^-32 of the largest
+ * from a weight (with codes: of the largest weight times value scale, rows of
+ * zeros left out).  One rounding at the end.
  * Cached values of positions below len are finite, in act_dtype's range (a
  * value that is not may reach other tokens of its sequence, none of another);
  * slots past them may hold anything.  A table entry outside the cache, a len beyond the table or
