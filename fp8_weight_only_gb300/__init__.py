@@ -11,7 +11,9 @@ raised.
     y = linear(x, codes, e8, bias)              # bf16 x for M > 1
     qx, sx = quantize_act(x)                    # W8A8: per-token e4m3 activations
     y = linear_w8a8(qx, sx, codes, scales, bias, out_dtype=torch.bfloat16)
-    cache = KVCache(k_pages, v_pages)           # paged keys and values: bf16/fp16, or e4m3 codes with scales
+    codes, blocks, scales = quantize_fp4(w)     # 4.5 bits a weight: e2m1 codes, an e4m3 scale per 16, one fp32 a row
+    y = linear_fp4(x, codes, blocks, scales, bias)
+    cache = KVCache(k_pages, v_pages)           # paged keys and values: bf16/fp16, e4m3 codes with scales, or 4 bits
     q = rope_append(q, k, v, slots, cache, positions, Rope(table))
     o = paged_attention(q, cache, block_table, lens)
 """
@@ -27,6 +29,7 @@ FP8W_BF16 = 1
 FP8W_F16 = 2
 FP8W_F32 = 3
 FP8W_E4M3 = 4
+FP8W_E2M1 = 5
 KERNEL_AUTO, KERNEL_GEMV, KERNEL_SKINNY, KERNEL_PREFILL = 0, 1, 2, 3
 
 SYMBOLS = ("fp8w_quantize", "fp8w_linear", "fp8w_linear_ex",
@@ -34,8 +37,8 @@ SYMBOLS = ("fp8w_quantize", "fp8w_linear", "fp8w_linear_ex",
            "fp8w_linear_noalloc", "fp8w_dequantize", "fp8w_quantize_grouped", "fp8w_linear_grouped",
            "fp8w_quantize_mx", "fp8w_linear_mx", "fp8w_quantize_ex", "fp8w_dequantize_grouped",
            "fp8w_dequantize_mx", "fp8w_quantize_act", "fp8w_linear_w8a8", "fp8w_rope", "fp8w_rope_append",
-           "fp8w_paged_attention")
-ABI_VERSION = 13
+           "fp8w_paged_attention", "fp8w_quantize_fp4", "fp8w_dequantize_fp4", "fp8w_linear_fp4")
+ABI_VERSION = 14
 FLAG_WEIGHTS_READY = 1
 
 
@@ -59,7 +62,8 @@ class KVCacheSpec(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
                 ("v_scales", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("dtype", ctypes.c_int),
-                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("page_size", ctypes.c_int)]
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("k_blocks", ctypes.c_void_p), ("v_blocks", ctypes.c_void_p)]
 
 
 _lib = None
@@ -112,6 +116,12 @@ def lib():
         L.fp8w_paged_attention.restype = c.c_int
         L.fp8w_paged_attention.argtypes = [P, c.c_int, c.c_int64, c.c_int, c.c_int64, KC, P, c.c_int64, P, P,
                                            c.c_int64, c.c_float, c.c_int64, c.c_int64, c.c_int64, P, c.c_int64, P]
+        L.fp8w_quantize_fp4.restype = c.c_int
+        L.fp8w_quantize_fp4.argtypes = [P, c.c_int, c.c_int64, c.c_int64, P, P, P, P]
+        L.fp8w_dequantize_fp4.restype = c.c_int
+        L.fp8w_dequantize_fp4.argtypes = [P, P, P, c.c_int64, c.c_int64, c.c_int, P, P]
+        L.fp8w_linear_fp4.restype = c.c_int
+        L.fp8w_linear_fp4.argtypes = [P, c.c_int, c.c_int64, c.c_int64, P, P, P, P, c.c_int64, P, c.c_int, P]
         L.fp8w_status_string.restype = c.c_char_p
         L.fp8w_status_string.argtypes = [c.c_int]
         L.fp8w_last_cuda_error.restype = c.c_char_p
@@ -322,6 +332,53 @@ def linear_w8a8(x_codes, x_scales, codes, scales, bias=None, out=None, out_dtype
     return out
 
 
+def quantize_fp4(w, codes=None, blocks=None, scales=None):
+    """W[N, K] (CUDA, contiguous; float32, bfloat16 or float16; K % 32 == 0) -> the
+    4-bit form (codes uint8 [N, K / 2], blocks uint8 [N, K / 16], scales fp32 [N]):
+    two e2m1 codes a byte (the first in the low half), an e4m3 scale per 16 of a
+    row and one fp32 a row."""
+    import torch
+    kind = {torch.float32: FP8W_F32, torch.bfloat16: FP8W_BF16, torch.float16: FP8W_F16}.get(w.dtype)
+    if kind is None or not w.is_cuda or w.dim() != 2 or not w.is_contiguous():
+        raise TypeError("w must be a contiguous 2-D float32, bfloat16 or float16 CUDA tensor")
+    n, k = w.shape
+    got = []
+    for name, t, dt, shape in (("codes", codes, torch.uint8, (n, k // 2)), ("blocks", blocks, torch.uint8, (n, k // 16)),
+                               ("scales", scales, torch.float32, (n,))):
+        if t is None:
+            t = torch.empty(shape, dtype=dt, device=w.device)
+        elif t.dtype != dt or t.device != w.device or not t.is_contiguous() or t.shape != shape:
+            raise TypeError("%s must be a contiguous %s %s tensor on w's device" % (name, dt, list(shape)))
+        got.append(t)
+    _check(lib().fp8w_quantize_fp4(_ptr(w), kind, n, k, _ptr(got[0]), _ptr(got[1]), _ptr(got[2]), _stream(w)))
+    return tuple(got)
+
+
+def dequantize_fp4(codes, blocks, scales, dtype=None, out=None):
+    """The values of the 4-bit form, each product rounded once to `dtype`
+    (torch.float32, bfloat16 or float16; default bfloat16): codes uint8 [.., K / 2],
+    blocks uint8 [.., K / 16], scales fp32 [..] -> [.., K].  The rows may be a
+    weight's, or a cache's slots ([pages, kv_heads, page_size], contiguous)."""
+    import torch
+    if dtype is None:
+        dtype = out.dtype if out is not None else torch.bfloat16
+    kind = {torch.float32: FP8W_F32, torch.bfloat16: FP8W_BF16, torch.float16: FP8W_F16}.get(dtype)
+    if kind is None:
+        raise TypeError("dequantize_fp4: dtype must be float32, bfloat16 or float16, got %s" % dtype)
+    for name, t, dt in (("codes", codes, torch.uint8), ("blocks", blocks, torch.uint8), ("scales", scales, torch.float32)):
+        if t.dtype != dt or not t.is_cuda or t.device != codes.device or not t.is_contiguous():
+            raise TypeError("%s must be a contiguous %s CUDA tensor on the operands' device" % (name, dt))
+    rows, k = tuple(codes.shape[:-1]), 2 * codes.shape[-1] if codes.dim() else 0
+    if scales.shape != rows or blocks.shape != rows + (k // 16,):
+        raise ValueError("shape mismatch: codes %s, blocks %s, scales %s" % (tuple(codes.shape), tuple(blocks.shape), tuple(scales.shape)))
+    if out is None:
+        out = torch.empty(rows + (k,), dtype=dtype, device=codes.device)
+    elif out.shape != rows + (k,) or out.dtype != dtype or out.device != codes.device or not out.is_contiguous():
+        raise ValueError("out must be a contiguous [.., K] tensor of the requested dtype")
+    _check(lib().fp8w_dequantize_fp4(_ptr(codes), _ptr(blocks), _ptr(scales), scales.numel(), k, kind, _ptr(out), _stream(codes)))
+    return out
+
+
 class Rope:
     """Rotary positions for rope and rope_append: table fp32 [max_pos, rot_dim]
     (CUDA, contiguous), each row the cosines of rot_dim / 2 angles and then
@@ -350,9 +407,11 @@ class KVCache:
     contiguous (a [num_pages, page_size, kv_heads, head_dim] tensor's
     transpose(1, 2), say; both the same strides): bfloat16 or float16, or
     uint8 e4m3 codes with k_scales, v_scales fp32 [num_pages, kv_heads,
-    page_size].  It keeps references to the tensors and nothing else."""
+    page_size].  With k_blocks, v_blocks uint8 [num_pages, kv_heads, page_size,
+    head_dim / 16] too, the 4-bit form: k and v are then [.., head_dim / 2]
+    bytes of two codes.  It keeps references to the tensors and nothing else."""
 
-    def __init__(self, k, v, k_scales=None, v_scales=None):
+    def __init__(self, k, v, k_scales=None, v_scales=None, k_blocks=None, v_blocks=None):
         import torch
         dtype = {torch.bfloat16: FP8W_BF16, torch.float16: FP8W_F16, torch.uint8: FP8W_E4M3}.get(k.dtype)
         if dtype is None or v.dtype != k.dtype or not k.is_cuda or v.device != k.device or k.dim() != 4:
@@ -360,18 +419,28 @@ class KVCache:
         if v.shape != k.shape or v.stride() != k.stride() or k.stride(3) != 1:
             raise ValueError("k and v must have the same shape and strides, head_dim contiguous")
         pages, heads, page, dim = k.shape
+        if k_blocks is not None or v_blocks is not None:
+            if dtype != FP8W_E4M3:
+                raise TypeError("k and v must be uint8 (two codes a byte) with k_blocks and v_blocks")
+            dtype, dim = FP8W_E2M1, 2 * dim
         for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-            if (t is None) != (dtype != FP8W_E4M3):
-                raise ValueError("%s comes with e4m3 codes, and only with them" % name)
+            if (t is None) != (dtype not in (FP8W_E4M3, FP8W_E2M1)):
+                raise ValueError("%s comes with codes, and only with them" % name)
             if t is not None and (t.dtype != torch.float32 or t.device != k.device or not t.is_contiguous() or
                                   t.shape != (pages, heads, page)):
                 raise TypeError("%s must be a contiguous float32 [num_pages, kv_heads, page_size] CUDA tensor" % name)
+        for name, t in (("k_blocks", k_blocks), ("v_blocks", v_blocks)):
+            if dtype == FP8W_E2M1 and (t is None or t.dtype != torch.uint8 or t.device != k.device or not t.is_contiguous() or
+                                       t.shape != (pages, heads, page, dim // 16)):
+                raise TypeError("%s must be a contiguous uint8 [num_pages, kv_heads, page_size, head_dim / 16] CUDA tensor" % name)
+        self.k_blocks, self.v_blocks = k_blocks, v_blocks
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
         self.device, self.dtype, self.kv_heads, self.page_size, self.head_dim = k.device, k.dtype, heads, page, dim
         self.index = k.get_device()
         self.spec = KVCacheSpec(k.data_ptr(), v.data_ptr(), None if k_scales is None else k_scales.data_ptr(),
                                 None if v_scales is None else v_scales.data_ptr(), pages, k.stride(0), k.stride(1),
-                                k.stride(2), dtype, heads, dim, page)
+                                k.stride(2), dtype, heads, dim, page, None if k_blocks is None else k_blocks.data_ptr(),
+                                None if v_blocks is None else v_blocks.data_ptr())
         self._ref = ctypes.byref(self.spec)
 
 
@@ -379,18 +448,19 @@ class KVCache:
 # host count: they read each attribute once and compare in place; _refuse finds
 # out what was wrong.
 
-_torch = _stream_of = _empty_like = _dense = _int32 = _int64 = None
+_torch = _stream_of = _empty_like = _dense = _int32 = _int64 = _empty = _uint8 = _float32 = None
 _ACT = {}
 
 
 def _load_torch():
-    global _torch, _stream_of, _empty_like, _dense, _int32, _int64
+    global _torch, _stream_of, _empty_like, _dense, _int32, _int64, _empty, _uint8, _float32
     import torch
     _ACT.update({torch.bfloat16: FP8W_BF16, torch.float16: FP8W_F16})
     # the stream's handle without a Stream object around it, where torch has it
     _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda index: torch.cuda.current_stream(index).cuda_stream)
     _empty_like, _dense, _int32, _int64 = torch.empty_like, torch.contiguous_format, torch.int32, torch.int64
+    _empty, _uint8, _float32 = torch.empty, torch.uint8, torch.float32
     lib()
     _torch = torch
 
@@ -429,6 +499,32 @@ def _index(name, t, dtype, shape, index):
     if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
         _refuse(name, t, index, dtype, shape, True)
     return t.data_ptr()
+
+
+def linear_fp4(x, codes, blocks, scales, bias=None, out=None, weights_ready=False):
+    """y[M, N] = round(scales[n] * sum_k x[m, k] * e4m3(blocks[n, k / 16]) * e2m1(codes[n, k]) + bias[n]):
+    x [M, K] bf16/fp16 on weights in the 4-bit form (quantize_fp4).  weights_ready as in linear."""
+    if _torch is None:
+        _load_torch()
+    dev, dtype, shape = x.get_device(), x.dtype, x.shape
+    act = _ACT.get(dtype)
+    if act is None or dev < 0 or len(shape) != 2 or not x.is_contiguous():
+        raise TypeError("x must be a contiguous 2-D bfloat16 or float16 CUDA tensor")
+    m, k = shape
+    n = codes.shape[0]
+    cp = _index("codes", codes, _uint8, (n, k >> 1), dev)
+    bp = _index("blocks", blocks, _uint8, (n, k >> 4), dev)
+    sp = _index("scales", scales, _float32, (n,), dev)
+    ap = None if bias is None else _index("bias", bias, _float32, (n,), dev)
+    if out is None:
+        out = _empty((m, n), dtype=dtype, device=x.device)
+    elif out.shape != (m, n) or out.dtype is not dtype or out.get_device() != dev or not out.is_contiguous():
+        raise ValueError("out must be a contiguous [M, N] tensor of x's dtype")
+    st = _lib.fp8w_linear_fp4(x.data_ptr(), act, m, k, cp, bp, sp, ap, n, out.data_ptr(), FLAG_WEIGHTS_READY if weights_ready else 0,
+                              _stream_of(dev))
+    if st:
+        _check(st)
+    return out
 
 
 def rope(x, positions, rope, out=None):

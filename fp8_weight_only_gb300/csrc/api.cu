@@ -54,20 +54,21 @@ fp8w_status check_rope_spec(const fp8w_rope_spec* s, const int32_t* positions, i
 }
 
 fp8w_status check_cache(const fp8w_kv_cache* c, int act) {
-    const bool codes = c->dtype == FP8W_E4M3;
-    if (!c->k || !c->v || (codes && (!c->k_scales || !c->v_scales))) return FP8W_ERR_NULL;
+    const bool fp4 = c->dtype == FP8W_E2M1, codes = c->dtype == FP8W_E4M3 || fp4;
+    if (!c->k || !c->v || (codes && (!c->k_scales || !c->v_scales)) || (fp4 && (!c->k_blocks || !c->v_blocks))) return FP8W_ERR_NULL;
     if (!codes && c->dtype != act) return FP8W_ERR_DTYPE;
     if (c->num_pages < 1 || c->num_pages > FP8W_MAX_DIM - 1 || c->kv_heads < 1 || c->kv_heads > 65536 ||
-        c->head_dim < 16 || c->head_dim > 128 || c->head_dim % 16 != 0)
+        c->head_dim < 16 || c->head_dim > 128 || c->head_dim % (fp4 ? 32 : 16) != 0)
         return FP8W_ERR_SHAPE;
     if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)) != 0) return FP8W_ERR_SHAPE;
-    const int64_t bytes = codes ? 1 : 2, most = (1ll << 40) / bytes;
-    if (c->token_stride < c->head_dim || c->head_stride < c->head_dim || c->page_stride < c->head_dim ||
+    const int64_t bytes = codes ? 1 : 2, most = (1ll << 40) / bytes, row = fp4 ? c->head_dim / 2 : c->head_dim;
+    if (c->token_stride < row || c->head_stride < row || c->page_stride < row ||
         c->token_stride >= most || c->head_stride >= most || c->page_stride >= most)
         return FP8W_ERR_VALUE;
-    if (!codes && (c->k_scales || c->v_scales)) return FP8W_ERR_VALUE;
+    if ((!codes && (c->k_scales || c->v_scales)) || (!fp4 && (c->k_blocks || c->v_blocks))) return FP8W_ERR_VALUE;
     if (!stride16(c->token_stride, bytes) || !stride16(c->head_stride, bytes) || !stride16(c->page_stride, bytes) ||
-        !aligned(c->k, 16) || !aligned(c->v, 16) || (codes && (!aligned(c->k_scales, 4) || !aligned(c->v_scales, 4))))
+        !aligned(c->k, 16) || !aligned(c->v, 16) || (codes && (!aligned(c->k_scales, 4) || !aligned(c->v_scales, 4))) ||
+        (fp4 && (!aligned(c->k_blocks, 16) || !aligned(c->v_blocks, 16))))
         return FP8W_ERR_ALIGN;
     return FP8W_OK;
 }
@@ -259,6 +260,46 @@ fp8w_status fp8w_linear_w8a8(const uint8_t* x_codes, const float* x_scales, int6
     fp8w::W8A8Args a{x_codes, x_scales, m, k, n, w_codes, w_scales, bias, y, out_dtype,
                      (flags & FP8W_FLAG_WEIGHTS_READY) != 0};
     return cuda_status(fp8w::launch_w8a8(a, static_cast<cudaStream_t>(stream)), "fp8w_linear_w8a8 launch");
+}
+
+// k of the 4-bit form: whole words of codes and pairs of blocks a row.
+static bool valid_k_fp4(int64_t k) { return k >= 32 && k <= FP8W_MAX_K && (k % 32) == 0; }
+
+fp8w_status fp8w_quantize_fp4(const void* w, int w_dtype, int64_t n, int64_t k, uint8_t* codes, uint8_t* blocks, float* scales,
+                              void* stream) {
+    if (!w || !codes || !blocks || !scales) return FP8W_ERR_NULL;
+    if (w_dtype != FP8W_F32 && w_dtype != FP8W_BF16 && w_dtype != FP8W_F16) return FP8W_ERR_DTYPE;
+    if (n < 1 || n > FP8W_MAX_DIM || !valid_k_fp4(k)) return FP8W_ERR_SHAPE;
+    if (!aligned(w, 16) || !aligned(codes, 16) || !aligned(blocks, 16) || !aligned(scales, 4)) return FP8W_ERR_ALIGN;
+    return cuda_status(fp8w::launch_quantize_fp4(w, w_dtype, n, k, codes, blocks, scales, static_cast<cudaStream_t>(stream)),
+                       "fp8w_quantize_fp4 launch");
+}
+
+fp8w_status fp8w_dequantize_fp4(const uint8_t* codes, const uint8_t* blocks, const float* scales, int64_t n, int64_t k,
+                                int out_dtype, void* w, void* stream) {
+    if (!codes || !blocks || !scales || !w) return FP8W_ERR_NULL;
+    if (n < 1 || n > FP8W_MAX_DIM || !valid_k_fp4(k)) return FP8W_ERR_SHAPE;
+    if (out_dtype != FP8W_F32 && out_dtype != FP8W_BF16 && out_dtype != FP8W_F16) return FP8W_ERR_DTYPE;
+    if (!aligned(codes, 16) || !aligned(blocks, 16) || !aligned(scales, 4) || !aligned(w, 16)) return FP8W_ERR_ALIGN;
+    const int kind = out_dtype == FP8W_BF16 ? 1 : out_dtype == FP8W_F16 ? 2 : 0;
+    return cuda_status(fp8w::launch_dequantize_fp4(codes, blocks, scales, n, k, kind, w, static_cast<cudaStream_t>(stream)),
+                       "fp8w_dequantize_fp4 launch");
+}
+
+fp8w_status fp8w_linear_fp4(const void* x, int act_dtype, int64_t m, int64_t k, const uint8_t* codes, const uint8_t* blocks,
+                            const float* scales, const float* bias, int64_t n, void* y, int flags, void* stream) {
+    fp8w_status st = check_linear(x, act_dtype, m, k, codes, scales, bias, n, y);
+    if (st != FP8W_OK) return st;
+    if (!blocks) return FP8W_ERR_NULL;
+    if (!valid_k_fp4(k)) return FP8W_ERR_SHAPE;
+    if (!aligned(blocks, 16)) return FP8W_ERR_ALIGN;
+    if (flags & ~FP8W_FLAG_WEIGHTS_READY) return FP8W_ERR_CONFIG;
+    fp8w::LinearArgs a{x, act_dtype, m, k, n, codes, scales, bias, y};
+    a.blocks = blocks;
+    a.early = (flags & FP8W_FLAG_WEIGHTS_READY) != 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (use_prefill(m)) return cuda_status(fp8w::launch_prefill(a, s), "fp8w_linear_fp4 prefill launch");
+    return cuda_status(fp8w::launch_fp4_few(a, s), "fp8w_linear_fp4 launch");
 }
 
 fp8w_status fp8w_rope(const void* x, int act_dtype, int64_t tokens, int heads, int head_dim, int64_t x_stride,

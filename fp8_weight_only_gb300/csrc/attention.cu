@@ -63,6 +63,7 @@
 #include <type_traits>
 
 #include "attention.cuh"
+#include "fp4.cuh"
 
 namespace fp8w {
 
@@ -84,11 +85,13 @@ constexpr int kSoftmaxThreads = 512;   // sixteen warps
 constexpr int kLoadWarp = 16, kMmaWarp = 17, kConvWarp = 20;
 constexpr int kBarSoftmax = 1;        // named barrier of the softmax warps; 2..9: of the pairs that share rows
 
-template <int DP, bool kFp8>
+template <int DP, int kForm>
 struct AttnSmem {
+    static constexpr bool kFp8 = kForm != kForm16;               // codes
+    static constexpr uint32_t kRawRow = kForm == kFormFp4 ? DP / 2 : DP;  // bytes of a key's or value's codes
     static constexpr uint32_t kSubs = DP / 64;                   // 64-value sub-tiles of a row (128 bytes)
     static constexpr uint32_t kTileBytes = kKeys * DP * 2;       // a 16-bit operand tile
-    static constexpr uint32_t kRawBytes = kKeys * DP;            // a tile of codes
+    static constexpr uint32_t kRawBytes = kKeys * kRawRow;       // a tile of codes
     static constexpr int kStages = kFp8 ? (DP == 128 ? 3 : 6) : (DP == 128 ? 5 : 10);
     static constexpr int kRaw = kFp8 ? (DP == 128 ? 3 : 6) : 0;
     // Key tile m is converted once ring position 2 m - 1 - kStages is free.  With
@@ -370,9 +373,9 @@ __device__ __noinline__ float scaled_peak(uint32_t taddr, uint32_t ksc, int widt
 // and then the cluster's.  Rounds: one, or one for each row tile.  A function of
 // its own: inlined, it took registers from the loop before it.  All softmax
 // threads call it.
-template <int DP, bool kBf16, bool kFp8>
+template <int DP, bool kBf16, int kForm>
 __device__ __noinline__ void join_results(const AttnParams& p, const Work& w, const Join& a, volatile int* abort_flag) {
-    using L = AttnSmem<DP, kFp8>;
+    using L = AttnSmem<DP, kForm>;
     const uint32_t sbase = a.sbase, t_o = a.t_o, joinfull = a.joinfull, joinfree = a.joinfree;
     const int rank = a.rank, tid = threadIdx.x, split = a.split, done = a.done, per_copy = kRows / split;
     constexpr int kHalf = DP / 2;          // output columns a thread
@@ -571,11 +574,12 @@ __device__ __noinline__ void join_results(const AttnParams& p, const Work& w, co
 
 }  // namespace
 
-template <int DP, bool kBf16, bool kFp8>
-__global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
+template <int DP, bool kBf16, int kForm>
+__global__ void __launch_bounds__(AttnSmem<DP, kForm>::kThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                      const __grid_constant__ AttnParams p) {
-    using L = AttnSmem<DP, kFp8>;
+    using L = AttnSmem<DP, kForm>;
+    constexpr bool kFp8 = L::kFp8, kFp4 = kForm == kFormFp4;  // codes; of 4 bits
     constexpr int kStages = L::kStages, kRaw = L::kRaw;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
@@ -664,8 +668,8 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             const int box = p.page_size < kKeys ? p.page_size : kKeys;
             const int mine = lane * L::kLoaders + loader, sub = mine % kCopies, at = mine / kCopies * box;
             const bool lives = at < kKeys;
-            const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, lives)) * box) * (kFp8 ? DP : 128);
-            const uint32_t dst0 = sbase + (kFp8 ? L::kRawOff + at * DP : L::kRingOff + sub * (kKeys * 128) + at * 128);
+            const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, lives)) * box) * (kFp8 ? L::kRawRow : 128);
+            const uint32_t dst0 = sbase + (kFp8 ? L::kRawOff + at * L::kRawRow : L::kRingOff + sub * (kKeys * 128) + at * 128);
             const int32_t* row = p.table + static_cast<int64_t>(w.seq) * p.table_width;
             // A lane's table entry is read two key tiles before its use and checked
             // there, so the table is not waited for.  One past the cache (which reads as
@@ -841,7 +845,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             reg_down<L::kRegsConv>();
             // One key a thread.  (Two warpgroups, half a key a thread each: 769 us for the
             // chunks that take 720 so; the schedulers have no room for more.)
-            constexpr int kChunks = DP / 16;  // 16-code chunks
+            constexpr int kChunks = L::kRawRow / 16;  // 16-byte chunks
             const int r = (warp & 3) * 32 + lane;  // key of the tile
             const uint32_t swz = static_cast<uint32_t>(r & 7);
             const int32_t* row = p.table + static_cast<int64_t>(w.seq) * p.table_width;
@@ -869,14 +873,36 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                 const int pg = page_at(j), slot = ((w.t0 + j) * kKeys + r) & (p.page_size - 1);
                 if (pg < 0 || pg >= p.num_pages) return true;
                 const uint8_t* at = static_cast<const uint8_t*>(p.v) + pg * p.page_stride + w.head * p.head_stride + slot * p.token_stride;
-                for (int u = 0; u < p.head_dim; u += 16) {
+                for (int u = 0; u < (kFp4 ? p.head_dim >> 1 : p.head_dim); u += 16) {
                     const uint4 y = *reinterpret_cast<const uint4*>(at + u);
-                    if ((y.x | y.y | y.z | y.w) & 0x7F7F7F7Fu) return false;
+                    if ((y.x | y.y | y.z | y.w) & (kFp4 ? 0x77777777u : 0x7F7F7F7Fu)) return false;
                 }
                 return true;
             };
-            float2 next = scales_at(0, page_at(0));
+            // 4 bits: the scales of a key's or value's blocks, two blocks a load, read
+            // one ring position ahead.
+            constexpr int kPairs = DP / 32;
+            struct Blocks {
+                uint32_t two[kFp4 ? kPairs : 1];
+            };
+            auto blocks_at = [&](bool of_k, int j, int pg) {
+                Blocks b = {};
+                if constexpr (kFp4) {
+                    if (live_at(j) && pg >= 0 && pg < p.num_pages) {
+                        const int64_t at = head_scales + pg * page_scales + (((w.t0 + j) * kKeys + r) & (p.page_size - 1));
+                        const uint8_t* from = (of_k ? p.k_blocks : p.v_blocks) + at * (p.head_dim >> 4);
+#pragma unroll
+                        for (int u = 0; u < kPairs; ++u)
+                            if (u * 32 < p.head_dim) b.two[u] = *reinterpret_cast<const uint16_t*>(from + 2 * u);
+                    }
+                }
+                return b;
+            };
+            const int page0 = page_at(0);
+            float2 next = scales_at(0, page0);
             int page = page_at(1);
+            int next_page = -1, k_page = page0, v_page = -1;  // of the tile behind the newest key tile, of that, and of the one before
+            Blocks ahead = blocks_at(true, 0, page0);
             uint32_t s = 0, phase = 0, d = 0;        // raw stage of the position, use of it, ring stage
             uint32_t freed = 0, fs = 0, fphase = 0;  // releases waited for; the next one's barrier and phase
             // One body for key and value tiles: two copies of it took 753 us where this takes 720.
@@ -887,18 +913,35 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
                 const bool live = live_at(j);
                 const float2 scale = next;
                 if (is_k) {
+                    if constexpr (kFp4) {
+                        if (j > 0) v_page = k_page, k_page = next_page;
+                        next_page = page;
+                    }
                     next = scales_at(j + 1, page);
                     page = page_at(j + 2);
+                }
+                Blocks blocks = {};
+                if constexpr (kFp4) {
+                    // positions go K0 K1 V0 K2 V1 .. V(n-1): after a key tile (but the first)
+                    // comes the value tile before it, after a value tile the next key tile
+                    blocks = ahead;
+                    if (i == 0 ? n > 1 : !is_k && j + 2 < n)
+                        ahead = blocks_at(true, i == 0 ? 1 : j + 2, next_page);
+                    else if (is_k && j > 0)
+                        ahead = blocks_at(false, j - 1, v_page);
+                    else if (i + 1 < 2 * n)
+                        ahead = blocks_at(false, n - 1, k_page);
                 }
                 if (!mbar_wait_warp(rawfull(s), phase, abort_flag)) {
                     if (lane == 0) attn_error(kErrWaitTma, abort_flag);
                     break;
                 }
                 uint4 c[kChunks];
-                const uint32_t src = sbase + L::kRawOff + s * L::kRawBytes + static_cast<uint32_t>(r) * DP;
+                const uint32_t src = sbase + L::kRawOff + s * L::kRawBytes + static_cast<uint32_t>(r) * L::kRawRow;
 #pragma unroll
                 for (uint32_t u = 0; u < kChunks; ++u) {
-                    c[u] = lds128(src + ((DP == 128 ? u ^ swz : u ^ (swz >> 1)) << 4));  // 128- or 64-byte swizzle
+                    // 128-, 64- or 32-byte swizzle
+                    c[u] = lds128(src + ((L::kRawRow == 128 ? u ^ swz : L::kRawRow == 64 ? u ^ (swz >> 1) : u ^ (swz >> 2)) << 4));
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(rawempty(s));
@@ -914,6 +957,23 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
 #pragma unroll
                 for (uint32_t u = 0; u < kChunks; ++u) {
                     const uint32_t w4[4] = {live ? c[u].x : 0u, live ? c[u].y : 0u, live ? c[u].z : 0u, live ? c[u].w : 0u};
+                    if constexpr (kFp4) {  // 32 values: 16-byte chunks 4 u .. 4 u + 3 of the row
+                        uint32_t f[2];
+                        if constexpr (kBf16) {
+                            uint32_t f23;
+                            block_quad_bf16(blocks.two[u], f[0], f23);
+                        } else {
+                            f[0] = block_pair_f16(blocks.two[u]);
+                        }
+                        const uint32_t sub = dst + (u >> 1) * (kKeys * 128);
+#pragma unroll
+                        for (uint32_t e = 0; e < 4; ++e) {
+                            uint32_t v[4];
+                            fp4_operands<kBf16>(w4[e], e < 2 ? both_lo(f[0]) : both_hi(f[0]), v);
+                            sts128(sub + (((4 * u + e) & 7) ^ swz) * 16, v[0], v[1], v[2], v[3]);
+                        }
+                        continue;
+                    }
                     uint32_t v[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -1282,7 +1342,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kFp8>::kThreads, 1)
             j.valid = valid;
             j.m = m;
             j.l = l;
-            join_results<DP, kBf16, kFp8>(p, w, j, abort_flag);
+            join_results<DP, kBf16, kForm>(p, w, j, abort_flag);
         }
     }
 
@@ -1318,13 +1378,14 @@ EncodeTiledFn encode_tiled() {
 }
 
 // Tensor map over one half of a paged cache: (value, slot, head, page), boxes of
-// box_inner values x box_slots slots, 128-byte swizzle (64 for 64-byte boxes).
+// box_inner values (4 bits: bytes) x box_slots slots, 128-byte swizzle (64 or 32 for
+// boxes of so many bytes).
 bool encode_pages(CUtensorMap* map, const fp8w_kv_cache& c, const void* base, uint32_t box_inner, uint32_t box_slots) {
     EncodeTiledFn fn = encode_tiled();
     if (!fn) return false;
-    const bool codes = c.dtype == FP8W_E4M3;
+    const bool codes = c.dtype == FP8W_E4M3 || c.dtype == FP8W_E2M1;
     const cuuint64_t es = codes ? 1 : 2;
-    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.page_size),
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.dtype == FP8W_E2M1 ? c.head_dim / 2 : c.head_dim), static_cast<cuuint64_t>(c.page_size),
                                 static_cast<cuuint64_t>(c.kv_heads), static_cast<cuuint64_t>(c.num_pages)};
     const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.token_stride) * es, static_cast<cuuint64_t>(c.head_stride) * es,
                                    static_cast<cuuint64_t>(c.page_stride) * es};
@@ -1332,14 +1393,16 @@ bool encode_pages(CUtensorMap* map, const fp8w_kv_cache& c, const void* base, ui
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     return fn(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(base), dims,
               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              box_inner * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+              box_inner * es == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+              : box_inner * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                     : CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DP, bool kBf16, bool kFp8>
+template <int DP, bool kBf16, int kForm>
 cudaError_t launch_attn(const AttentionArgs& a, cudaStream_t st) {
-    using L = AttnSmem<DP, kFp8>;
-    auto kern = attention_kernel<DP, kBf16, kFp8>;
+    using L = AttnSmem<DP, kForm>;
+    auto kern = attention_kernel<DP, kBf16, kForm>;
     static std::once_flag attr_once[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1360,7 +1423,8 @@ cudaError_t launch_attn(const AttentionArgs& a, cudaStream_t st) {
     const int group = a.q_heads / c.kv_heads;
     CUtensorMap map_k, map_v;
     const uint32_t box = static_cast<uint32_t>(c.page_size < kKeys ? c.page_size : kKeys);
-    if (!encode_pages(&map_k, c, c.k, kFp8 ? DP : 64, box) || !encode_pages(&map_v, c, c.v, kFp8 ? DP : 64, box))
+    constexpr uint32_t kInner = L::kFp8 ? L::kRawRow : 64;
+    if (!encode_pages(&map_k, c, c.k, kInner, box) || !encode_pages(&map_v, c, c.v, kInner, box))
         return cudaErrorInvalidValue;
 
     const int64_t tiles = attention_row_tiles(a, group, 2 * kRows), items = tiles * c.kv_heads;
@@ -1394,16 +1458,18 @@ cudaError_t launch_attn(const AttentionArgs& a, cudaStream_t st) {
 template <int DP>
 cudaError_t launch_dim(const AttentionArgs& a, cudaStream_t st) {
     const bool bf16 = a.act == FP8W_BF16;
+    if (a.cache->dtype == FP8W_E2M1)
+        return bf16 ? launch_attn<DP, true, kFormFp4>(a, st) : launch_attn<DP, false, kFormFp4>(a, st);
     if (a.cache->dtype == FP8W_E4M3)
-        return bf16 ? launch_attn<DP, true, true>(a, st) : launch_attn<DP, false, true>(a, st);
-    return bf16 ? launch_attn<DP, true, false>(a, st) : launch_attn<DP, false, false>(a, st);
+        return bf16 ? launch_attn<DP, true, kFormE4m3>(a, st) : launch_attn<DP, false, kFormE4m3>(a, st);
+    return bf16 ? launch_attn<DP, true, kForm16>(a, st) : launch_attn<DP, false, kForm16>(a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t st) {
     const int64_t most_new = a.starts ? (a.max_new > 0 ? a.max_new : a.tokens) : 1;
-    if (most_new * (a.q_heads / a.cache->kv_heads) <= (a.cache->dtype == FP8W_E4M3 ? kFewRowsCodes : kFewRows))
+    if (most_new * (a.q_heads / a.cache->kv_heads) <= (a.cache->dtype == FP8W_E4M3 || a.cache->dtype == FP8W_E2M1 ? kFewRowsCodes : kFewRows))
         return launch_attention_few(a, st);
     return a.cache->head_dim <= 64 ? launch_dim<64>(a, st) : launch_dim<128>(a, st);
 }

@@ -11,6 +11,10 @@ namespace fp8w {
 constexpr float kLog2e = 1.4426950408889634f;
 #define kNegInf __int_as_float(0xff800000)
 
+// Forms of a cache: 16-bit values, e4m3 codes with a scale a slot and head, or the
+// 4-bit form (fp4.cuh) with a scale a slot and head.
+constexpr int kForm16 = 0, kFormE4m3 = 1, kFormFp4 = 2;
+
 struct AttnParams {
     const uint16_t* q;
     uint16_t* out;
@@ -24,6 +28,8 @@ struct AttnParams {
     int64_t page_stride, head_stride, token_stride;
     const float* k_scales;
     const float* v_scales;
+    const uint8_t* k_blocks;  // 4 bits: scales of blocks
+    const uint8_t* v_blocks;
     int64_t num_pages;
     int seqs, kv_heads, group, head_dim, page_size, log_page;
     uint32_t group_inverse;  // 2^32 / group rounded up (0 for 1)
@@ -154,6 +160,8 @@ inline AttnParams attention_params(const AttentionArgs& a) {
     p.token_stride = c.token_stride;
     p.k_scales = c.k_scales;
     p.v_scales = c.v_scales;
+    p.k_blocks = c.k_blocks;
+    p.v_blocks = c.v_blocks;
     p.num_pages = c.num_pages;
     p.seqs = static_cast<int>(a.seqs);
     p.kv_heads = c.kv_heads;

@@ -33,8 +33,10 @@
 // pairs of at most 16 CTAs are 1.7 CTAs an SM.
 // One short sequence: 8 us, four dependent reads of memory and a launch.
 #include <mutex>
+#include <type_traits>
 
 #include "attention.cuh"
+#include "fp4.cuh"
 
 namespace fp8w {
 
@@ -66,13 +68,15 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-template <int DP, bool kFp8, int NT>
+// kForm: the cache's (attention.cuh).
+template <int DP, int kForm, int NT>
 struct FewShape {
+    static constexpr bool kFp8 = kForm != kForm16, kFp4 = kForm == kFormFp4;
     static constexpr int kTile = 8 * NT;                               // rows
     static constexpr int kSubs = (DP == 64 ? 2 : 1) * (kFp8 && NT == 1 ? 2 : 1);  // 16-key parts a step of the loop
     static constexpr int kStepKeys = 16 * kSubs;
-    static constexpr int kKeyPieces = kFp8 ? DP / 64 : DP / 32;        // 16-byte pieces of a key row a thread
-    static constexpr int kValuePieces = kFp8 ? 1 : DP / 64;            // pieces of a value row: 16 bytes (8 with codes, DP 64)
+    static constexpr int kKeyPieces = kFp4 ? 1 : kFp8 ? DP / 64 : DP / 32;  // 16-byte pieces of a key row a thread (4 bits, DP 64: 8 bytes)
+    static constexpr int kValuePieces = kFp8 ? 1 : DP / 64;            // pieces of a value row: 16 bytes (DP / 8 with codes, DP / 16 with 4 bits)
     static constexpr uint32_t kStageOff = 0;                           // fp32 [warps][rows][DP]
     static constexpr uint32_t kMlOff = kFewWarps * kTile * DP * 4;
     static constexpr uint32_t kJoinedOff = kMlOff + kFewWarps * kTile * 8;
@@ -87,22 +91,27 @@ struct FewShape {
 };
 
 // What a thread holds of one step's keys (g = lane / 4, t = lane % 4).
-template <int DP, bool kFp8, int NT>
+template <int DP, int kForm, int NT>
 struct Step {
-    using S = FewShape<DP, kFp8, NT>;
+    using S = FewShape<DP, kForm, NT>;
+    static constexpr bool kFp8 = S::kFp8;
     uint4 k[S::kSubs][2][S::kKeyPieces];    // key rows g and g + 8
     uint4 v[S::kSubs][4][S::kValuePieces];  // value rows 2t, 2t + 1, 2t + 8, 2t + 9
     float ks[kFp8 ? S::kSubs : 1][2], vs[kFp8 ? S::kSubs : 1][2];  // scales of keys g and g + 8
+    // 4 bits, bytes of blocks' scales: those of this thread's part of key rows g and
+    // g + 8 (two, DP 64: one), and of its part of the four value rows (one each)
+    uint32_t kb[S::kFp4 ? S::kSubs : 1][2], vb[S::kFp4 ? S::kSubs : 1][4];
 };
 
 }  // namespace
 
-template <int DP, bool kBf16, bool kFp8, int NT>
+template <int DP, bool kBf16, int kForm, int NT>
 __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const __grid_constant__ AttnParams p) {
-    using S = FewShape<DP, kFp8, NT>;
-    using H = Step<DP, kFp8, NT>;
+    using S = FewShape<DP, kForm, NT>;
+    using H = Step<DP, kForm, NT>;
+    constexpr bool kFp8 = S::kFp8, kFp4 = S::kFp4;  // codes; of 4 bits
     constexpr int kSubs = S::kSubs, kStepKeys = S::kStepKeys, kTile = S::kTile;
-    constexpr int kEl = kFp8 ? 1 : 2;  // bytes a value
+    constexpr int kEl = kFp8 ? 1 : 2;  // bytes an element of the cache (4 bits: two values)
     // Codes are multiplied as fp16 whatever the activations' type: one conversion
     // instruction makes two of them, and the weights round to 11 bits.  bf16
     // queries go over exactly but for a power of two a row (below).
@@ -141,7 +150,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int s = 0; s < DP / 16; ++s) {
-            const int d = kFp8 ? (s >> 2) * 64 + t * 16 + (s & 3) * 4 : (s >> 1) * 32 + t * 8 + (s & 1) * 4;
+            const int d = kFp4 ? t * (DP / 4) + s * 4 : kFp8 ? (s >> 2) * 64 + t * 16 + (s & 3) * 4 : (s >> 1) * 32 + t * 8 + (s & 1) * 4;
             uint2 y = make_uint2(0u, 0u);
             if (8 * n + g < rows && d < p.head_dim) y = *reinterpret_cast<const uint2*>(p.q + row_at(8 * n + g, p.q_stride) + d);
             if constexpr (!S::kQShared)
@@ -207,11 +216,15 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
     const uint8_t* kbase = static_cast<const uint8_t*>(p.k) + static_cast<int64_t>(head) * p.head_stride * kEl;
     const uint8_t* vbase = static_cast<const uint8_t*>(p.v) + static_cast<int64_t>(head) * p.head_stride * kEl;
     // this thread's part of a 16-key block: key rows g and g + 8, value rows 2t, 2t + 1 and + 8
-    const uint8_t* kthread = kbase + g * token_bytes + t * 16;
-    const uint8_t* vthread = vbase + 2 * t * token_bytes + g * (kFp8 ? DP / 8 : 16);
-    auto load_codes = [&](const uint8_t* at) {  // a value row's codes of this thread
+    constexpr int kKeyBytes = kFp4 ? DP / 8 : 16, kValueBytes = kFp4 ? DP / 16 : kFp8 ? DP / 8 : 16;  // of a piece
+    const uint8_t* kthread = kbase + g * token_bytes + t * kKeyBytes;
+    const uint8_t* vthread = vbase + 2 * t * token_bytes + g * kValueBytes;
+    const int row_bytes = kFp4 ? p.head_dim >> 1 : p.head_dim * kEl, row_blocks = p.head_dim >> 4;
+    auto load_codes = [&](const uint8_t* at, auto bytes) {  // a row's codes of this thread
         uint4 y = make_uint4(0u, 0u, 0u, 0u);
-        if constexpr (DP == 128) {
+        if constexpr (bytes.value == 4) {
+            y.x = *reinterpret_cast<const uint32_t*>(at);
+        } else if constexpr (bytes.value == 16) {
             y = ld_stream_v4(at);
         } else {
             const uint2 z = *reinterpret_cast<const uint2*>(at);
@@ -246,12 +259,24 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
 #pragma unroll
                 for (int j = 0; j < S::kKeyPieces; ++j) {
                     if constexpr (!S::kKeeps) x.k[i][r][j] = make_uint4(0u, 0u, 0u, 0u);
-                    if (in && j * 64 + t * 16 < p.head_dim * kEl) x.k[i][r][j] = ld_stream_v4(kthread + at + 8 * r * token_bytes + j * 64);
+                    if constexpr (kFp4) {
+                        if (in && t * kKeyBytes < row_bytes)
+                            x.k[i][r][j] = load_codes(kthread + at + 8 * r * token_bytes, std::integral_constant<int, kKeyBytes>{});
+                    } else {
+                        if (in && j * 64 + t * 16 < row_bytes) x.k[i][r][j] = ld_stream_v4(kthread + at + 8 * r * token_bytes + j * 64);
+                    }
                 }
                 if constexpr (kFp8) {
                     const int64_t sc = (static_cast<int64_t>(e[i]) * p.kv_heads + head) * p.page_size + slot + g + 8 * r;
                     x.ks[i][r] = in ? p.k_scales[sc] : 0.0f;
                     x.vs[i][r] = in ? p.v_scales[sc] : 0.0f;
+                    if constexpr (kFp4) {
+                        x.kb[i][r] = 0u;
+                        if (in && t * kKeyBytes < row_bytes) {
+                            const uint8_t* b = p.k_blocks + sc * row_blocks + t * (DP / 64);
+                            x.kb[i][r] = DP == 128 ? *reinterpret_cast<const uint16_t*>(b) : *b;
+                        }
+                    }
                 }
             }
 #pragma unroll
@@ -263,7 +288,15 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
                 for (int h = 0; h < S::kValuePieces; ++h) {
                     if constexpr (!S::kKeeps) x.v[i][j][h] = make_uint4(0u, 0u, 0u, 0u);
                     if constexpr (kFp8) {
-                        if (in && g * (DP / 8) < p.head_dim) x.v[i][j][h] = load_codes(row);
+                        const bool here = in && g * (DP / 8) < p.head_dim;
+                        if (here) x.v[i][j][h] = load_codes(row, std::integral_constant<int, kValueBytes>{});
+                        if constexpr (kFp4) {
+                            x.vb[i][j] = 0u;
+                            if (here) {
+                                const int64_t sc = (static_cast<int64_t>(e[i]) * p.kv_heads + head) * p.page_size + slot + 2 * t + r;
+                                x.vb[i][j] = p.v_blocks[sc * row_blocks + g * (DP / 8) / 16];
+                            }
+                        }
                     } else {
                         if (in && h * 64 + g * 8 < p.head_dim) x.v[i][j][h] = ld_stream_v4(row + h * 128);
                     }
@@ -300,7 +333,17 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
 #pragma unroll
             for (int i = 0; i < kSubs; ++i) {
                 uint4 a;
-                if constexpr (kFp8) {
+                if constexpr (kFp4) {
+                    // half k & 1 of a word: four codes
+                    const uint4 w = x.k[i][0][0], u = x.k[i][1][0];
+                    const int q = k >> 1;
+                    const uint32_t f = block_pair_f16(x.kb[i][0]), h = block_pair_f16(x.kb[i][1]);
+                    const bool second = DP == 128 && q >= 2;  // of the thread's blocks
+                    uint32_t c[4], d[4];
+                    fp4_operands<false>(q == 0 ? w.x : q == 1 ? w.y : q == 2 ? w.z : w.w, second ? both_hi(f) : both_lo(f), c);
+                    fp4_operands<false>(q == 0 ? u.x : q == 1 ? u.y : q == 2 ? u.z : u.w, second ? both_hi(h) : both_lo(h), d);
+                    a = (k & 1) ? make_uint4(c[2], d[2], c[3], d[3]) : make_uint4(c[0], d[0], c[1], d[1]);
+                } else if constexpr (kFp8) {
                     const uint4 w = x.k[i][0][k >> 2], u = x.k[i][1][k >> 2];
                     e4m3x4_to_f16x2((k & 3) == 0 ? w.x : (k & 3) == 1 ? w.y : (k & 3) == 2 ? w.z : w.w, a.x, a.z);
                     e4m3x4_to_f16x2((k & 3) == 0 ? u.x : (k & 3) == 1 ? u.y : (k & 3) == 2 ? u.z : u.w, a.y, a.w);
@@ -359,7 +402,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const uint4 y = x.v[i][j][0];
-                        if ((y.x | y.y | y.z | y.w) & 0x7F7F7F7Fu) any |= 1u << (2 * t + (j >> 1) * 8 + (j & 1));
+                        if ((y.x | y.y | y.z | y.w) & (kFp4 ? 0x77777777u : 0x7F7F7F7Fu)) any |= 1u << (2 * t + (j >> 1) * 8 + (j & 1));
                     }
                     any = __reduce_or_sync(0xffffffffu, any);
 #pragma unroll
@@ -419,8 +462,33 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
             }
             // 16 values a product: this thread's values 2 j and 2 j + 1 of its four rows
 #pragma unroll
-            for (int j = 0; j < DP / 16; j += kFp8 ? 2 : 1) {
-                if constexpr (kFp8) {
+            for (int j = 0; j < DP / 16; j += kFp4 ? 4 : kFp8 ? 2 : 1) {
+                if constexpr (kFp4) {
+                    // a word of 8 codes of each row, paired row by row: even values in
+                    // the bytes of lo[], odd ones in those of hi[]
+                    uint32_t lo[2], hi[2], f[2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const uint4 y = x.v[i][2 * r][0], z = x.v[i][2 * r + 1][0];
+                        const uint32_t a = j / 4 == 0 ? y.x : y.y, b = j / 4 == 0 ? z.x : z.y;
+                        lo[r] = (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u);
+                        hi[r] = ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u);
+                        f[r] = block_pair_f16(x.vb[i][2 * r] | (x.vb[i][2 * r + 1] << 8));
+                    }
+                    uint32_t v[2][2][4];  // [rows 2t or 2t + 8][even or odd value][pair of values]
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        e2m1x8_to_f16x2(lo[r], v[r][0][0], v[r][0][1], v[r][0][2], v[r][0][3]);
+                        e2m1x8_to_f16x2(hi[r], v[r][1][0], v[r][1][1], v[r][1][2], v[r][1][3]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint4 a = make_uint4(f16x2_mul(v[0][0][e], f[0]), f16x2_mul(v[0][1][e], f[0]), f16x2_mul(v[1][0][e], f[1]),
+                                                   f16x2_mul(v[1][1][e], f[1]));
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma16816<kMmaBf16>(o[j + e][n], a, b[n][0], b[n][1]);
+                    }
+                } else if constexpr (kFp8) {
                     uint32_t c[4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
@@ -595,10 +663,10 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
 
 namespace {
 
-template <int DP, bool kBf16, bool kFp8, int NT>
+template <int DP, bool kBf16, int kForm, int NT>
 cudaError_t launch_few(const AttentionArgs& a, cudaStream_t st) {
-    using S = FewShape<DP, kFp8, NT>;
-    auto kern = attention_few_kernel<DP, kBf16, kFp8, NT>;
+    using S = FewShape<DP, kForm, NT>;
+    auto kern = attention_few_kernel<DP, kBf16, kForm, NT>;
     static std::once_flag attr_once[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -638,8 +706,9 @@ cudaError_t launch_few(const AttentionArgs& a, cudaStream_t st) {
 template <int DP, int NT>
 cudaError_t launch_few_dim(const AttentionArgs& a, cudaStream_t st) {
     const bool bf16 = a.act == FP8W_BF16;
-    if (a.cache->dtype == FP8W_E4M3) return bf16 ? launch_few<DP, true, true, NT>(a, st) : launch_few<DP, false, true, NT>(a, st);
-    return bf16 ? launch_few<DP, true, false, NT>(a, st) : launch_few<DP, false, false, NT>(a, st);
+    if (a.cache->dtype == FP8W_E2M1) return bf16 ? launch_few<DP, true, kFormFp4, NT>(a, st) : launch_few<DP, false, kFormFp4, NT>(a, st);
+    if (a.cache->dtype == FP8W_E4M3) return bf16 ? launch_few<DP, true, kFormE4m3, NT>(a, st) : launch_few<DP, false, kFormE4m3, NT>(a, st);
+    return bf16 ? launch_few<DP, true, kForm16, NT>(a, st) : launch_few<DP, false, kForm16, NT>(a, st);
 }
 
 }  // namespace

@@ -22,7 +22,20 @@ struct LinearArgs {
     bool e8m0 = false;  // with group 32: scales are E8M0 bytes, not fp32
     bool early = false; // the weights were complete before the preceding kernel
                         // started: their copies may begin before it finishes
+    const uint8_t* blocks = nullptr;  // 4-bit codes[n, k / 2]: e4m3 scales[n, k / 16] of their blocks
 };
+
+// The 4-bit form (fp4.cuh): e2m1 codes[n, k / 2], e4m3 blocks[n, k / 16], fp32
+// scales[n]; k % 32 == 0.  w_dtype FP8W_F32, FP8W_BF16 or FP8W_F16; out_dtype as
+// launch_dequantize.
+cudaError_t launch_quantize_fp4(const void* w, int w_dtype, int64_t n, int64_t k, uint8_t* codes, uint8_t* blocks, float* scales,
+                                cudaStream_t st);
+cudaError_t launch_dequantize_fp4(const uint8_t* codes, const uint8_t* blocks, const float* scales, int64_t n, int64_t k,
+                                  int out_dtype, void* w, cudaStream_t st);
+
+// K9: the linear layer on 4-bit weights for few tokens (any m: 32 a slab).
+// LinearArgs with blocks; group 0.
+cudaError_t launch_fp4_few(const LinearArgs& a, cudaStream_t st);
 
 // K1: codes/scales from fp32 weights.
 cudaError_t launch_quantize(const float* w, int64_t n, int64_t k, uint8_t* codes, float* scales,

@@ -33,7 +33,7 @@
 
 #include <mutex>
 
-#include "fp8w_device.cuh"
+#include "fp4.cuh"
 #include "fp8w_internal.h"
 
 namespace fp8w {
@@ -102,6 +102,10 @@ __device__ __forceinline__ void prefill_error(int code, volatile int* abort_flag
 //                eight epilogue warps (two per TMEM lane quarter, 64 tokens
 //                each) add every group's sums times its scale into fp32 totals
 //                held in registers.
+//  kModeFp4      4-bit codes with an e4m3 byte per 16 of them (fp4.cuh),
+//                blocks[n, k / 16] passed as e8: folded into the dequantised
+//                weight, exactly; scales[n] in the epilogue.  A code stage is
+//                256 codes of a row, four k-blocks (k % 32 == 0).
 template <int BN, bool kBf16, int kMode>
 __global__ void __launch_bounds__(kMode == kModeGrouped ? kPThreadsGrouped : kPThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_constant__ CUtensorMap map_x,
@@ -109,6 +113,8 @@ __global__ void __launch_bounds__(kMode == kModeGrouped ? kPThreadsGrouped : kPT
                    uint16_t* __restrict__ y, int64_t m, int64_t n, int64_t k, int early, int gsz) {
     constexpr bool kMx = kMode == kModeMxFold;
     constexpr bool kGrp = kMode == kModeGrouped;
+    constexpr bool kFp4 = kMode == kModeFp4;
+    constexpr int kStageK = kFp4 ? 2 * kPCodeK : kPCodeK;  // k of a code stage
     static_assert(!kMx || kBf16, "MX-style scales fold into bf16 weights only");
     static_assert(!kGrp || BN == 128, "per-group form: 128-token tiles");
     using L = PrefillSmem<BN>;
@@ -137,7 +143,7 @@ __global__ void __launch_bounds__(kMode == kModeGrouped ? kPThreadsGrouped : kPT
     const int64_t token_tiles = (m + BN - 1) / BN;
     const int64_t tiles = ((n + kPM - 1) / kPM) * token_tiles;
     const int nkb = static_cast<int>((k + kPK - 1) / kPK);          // k-blocks a tile
-    const int ncs = static_cast<int>((k + kPCodeK - 1) / kPCodeK);  // code stages a tile
+    const int ncs = static_cast<int>((k + kStageK - 1) / kStageK);  // code stages a tile
 
     if (warp == 0) {
         if (lane == 0) {
@@ -447,6 +453,88 @@ __global__ void __launch_bounds__(kMode == kModeGrouped ? kPThreadsGrouped : kPT
             __syncwarp();
             if (lane == 0) mbar_arrive(dempty(d));
         }
+    } else if (kFp4 && warp >= kPFirstDqWarp && warp < kPFirstDqWarp + 8) {
+        // ----------------------------------------- dequantising, 4 bits --
+        // A stage's k-blocks h and h + 2 (two 16-byte chunks of a row each) are this
+        // warpgroup's, and their four blocks' scales (two 16-bit loads each) are
+        // read a stage ahead.
+        const int h = (warp - kPFirstDqWarp) >> 2;
+        const int r = (warp & 3) * 32 + lane;
+        const uint32_t swz = static_cast<uint32_t>(r & 7);
+        if (!early) pdl_wait();  // the blocks' scales may come from the previous kernel
+        uint32_t next[2] = {0u, 0u};
+        int64_t b_t = blockIdx.x;
+        int b_cs = 0;
+        auto ask = [&] {  // the scales of stage (b_t, b_cs), and on to the one after it
+            next[0] = next[1] = 0u;
+            const int64_t wrow = (b_t / token_tiles) * kPM + r;
+            if (b_t < tiles && wrow < n) {
+                const uint8_t* row = e8 + wrow * (k >> 4);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int64_t k0 = (static_cast<int64_t>(b_cs) * 4 + 2 * i + h) * kPK;
+                    if (k0 < k) next[i] = *reinterpret_cast<const uint16_t*>(row + (k0 >> 4));
+                    if (k0 + 32 < k) next[i] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(row + (k0 >> 4) + 2)) << 16;
+                }
+            }
+            if (++b_cs == ncs) {
+                b_cs = 0;
+                b_t += gridDim.x;
+            }
+        };
+        ask();
+        int64_t cs_n = 0, kb_base = 0;
+        bool ok = true;
+        for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x, kb_base += nkb) {
+            for (int cs = 0; cs < ncs && ok; ++cs, ++cs_n) {
+                const int s = static_cast<int>(cs_n % kPCS);
+                const uint32_t scale4[2] = {next[0], next[1]};
+                ask();
+                if (!mbar_wait_warp(cfull(s), static_cast<uint32_t>((cs_n / kPCS) & 1), abort_flag)) {
+                    if (lane == 0) prefill_error(kErrWaitTma, abort_flag);
+                    ok = false;
+                    break;
+                }
+                uint4 cw[4];  // chunks of k-block h, then h + 2
+                const uint32_t row = sbase + L::kCodesOff + s * kPCodeBytes + static_cast<uint32_t>(r) * 128u;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) cw[q] = lds128(row + (((2u * h + (q & 1) + 4u * (q >> 1)) ^ swz) << 4));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(cempty(s));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int j = 4 * cs + 2 * i + h;
+                    if (j >= nkb) break;
+                    const int64_t kb = kb_base + j;
+                    const int as = static_cast<int>(kb % kPAS);
+                    if (!mbar_wait_warp(aempty(as), static_cast<uint32_t>((kb / kPAS) & 1) ^ 1u, abort_flag)) {
+                        if (lane == 0) prefill_error(kErrWaitMma, abort_flag);
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t arow = sbase + L::kAOff + as * kPABytes + static_cast<uint32_t>(r) * 128u;
+                    uint32_t f[2];  // factors of blocks 0, 1 and 2, 3
+                    if constexpr (kBf16) {
+                        block_quad_bf16(scale4[i], f[0], f[1]);
+                    } else {
+                        f[0] = block_pair_f16(scale4[i]);
+                        f[1] = block_pair_f16(scale4[i] >> 16);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {  // words of 8 codes: 16-byte chunk q of the A row
+                        const uint4 c = cw[2 * i + (q >> 2)];
+                        const uint32_t w = (q & 3) == 0 ? c.x : (q & 3) == 1 ? c.y : (q & 3) == 2 ? c.z : c.w;
+                        const uint32_t pair = f[q >> 2];
+                        uint32_t v[4];
+                        fp4_operands<kBf16>(w, (q & 2) ? both_hi(pair) : both_lo(pair), v);
+                        sts128(arow + ((static_cast<uint32_t>(q) ^ swz) << 4), v[0], v[1], v[2], v[3]);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(afull(as));
+                }
+            }
+        }
     } else if (warp >= kPFirstDqWarp && warp < kPFirstDqWarp + 8) {
         // ---------------------------------------------------- dequantising --
         const int h = (warp - kPFirstDqWarp) >> 2;  // warpgroup: k-blocks with j % 2 == h
@@ -574,8 +662,9 @@ static cudaError_t launch_bn(const LinearArgs& a, cudaStream_t st) {
     e = device_sm_count(sms);
     if (e != cudaSuccess) return e;
     CUtensorMap map_codes, map_x;
-    if (!encode_2d(&map_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.codes, static_cast<uint64_t>(a.k),
-                   static_cast<uint64_t>(a.n), static_cast<uint64_t>(a.k), kPCodeK, kPM))
+    const int64_t row_bytes = kMode == kModeFp4 ? a.k / 2 : a.k;  // of codes
+    if (!encode_2d(&map_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.codes, static_cast<uint64_t>(row_bytes),
+                   static_cast<uint64_t>(a.n), static_cast<uint64_t>(row_bytes), kPCodeK, kPM))
         return cudaErrorInvalidValue;
     if (!encode_2d(&map_x, CU_TENSOR_MAP_DATA_TYPE_UINT16, a.x, static_cast<uint64_t>(a.k),
                    static_cast<uint64_t>(a.m), static_cast<uint64_t>(a.k) * 2, kPK, BN))
@@ -594,13 +683,18 @@ static cudaError_t launch_bn(const LinearArgs& a, cudaStream_t st) {
     cfg.numAttrs = 1;
     const bool bytes = kMx || (kGrp && a.e8m0);
     const float* sc = bytes ? nullptr : a.scales;
-    const uint8_t* e8 = bytes ? reinterpret_cast<const uint8_t*>(a.scales) : nullptr;
+    const uint8_t* e8 = kMode == kModeFp4 ? a.blocks : bytes ? reinterpret_cast<const uint8_t*>(a.scales) : nullptr;
     return cudaLaunchKernelEx(&cfg, kern, map_codes, map_x, sc, e8, a.bias, static_cast<uint16_t*>(a.y), a.m, a.n,
                               a.k, a.early ? 1 : 0, kGrp ? static_cast<int>(a.group) : 0);
 }
 
 cudaError_t launch_prefill(const LinearArgs& a, cudaStream_t st) {
     const bool bf16 = a.act == 1;
+    if (a.blocks) {
+        if (a.k % 32 != 0) return cudaErrorInvalidValue;
+        if (a.m <= 128) return bf16 ? launch_bn<128, true, kModeFp4>(a, st) : launch_bn<128, false, kModeFp4>(a, st);
+        return bf16 ? launch_bn<256, true, kModeFp4>(a, st) : launch_bn<256, false, kModeFp4>(a, st);
+    }
     if (a.group != 0 && (!a.e8m0 || !bf16)) {
         // per-group scales (fp32, or E8M0 bytes with fp16 activations)
         if (a.k % a.group != 0 || (a.group != 32 && a.group != 64 && a.group != 128) || (a.e8m0 && a.group != 32))

@@ -22,7 +22,7 @@
 // 16384 tokens of 40 heads of 128, three axes: 59.3 us, 5.8 TB/s (87% of the
 // measured copy rate), one axis 54.8 us; 8192 tokens appended 34.6 us (88%), as
 // codes 42.4 us (66%: sixteen IEEE divisions a lane); one token 1.7 us.
-#include "fp8w_device.cuh"
+#include "fp4.cuh"
 #include "fp8w_internal.h"
 
 namespace fp8w {
@@ -58,6 +58,8 @@ struct RopeParams {
     uint8_t* vc;
     float* ks;
     float* vs;
+    uint8_t* kb;  // 4 bits: scales of blocks
+    uint8_t* vb;
     int64_t num_pages, page_stride, head_stride, token_stride;
     int page_size, log_page;
     int parts, per_part;  // warps a token, steps of each
@@ -86,15 +88,16 @@ __device__ __forceinline__ uint4 narrow(const float* f) {
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// What a call does: rotate, or also append to a 16-bit cache or one of codes.
-constexpr int kRotate = 0, kAppend16 = 1, kAppendCodes = 2;
+// What a call does: rotate, or also append to a 16-bit cache, one of e4m3 codes or
+// one of 4 bits.
+constexpr int kRotate = 0, kAppend16 = 1, kAppendCodes = 2, kAppendFp4 = 3;
 
 // P lanes (a power of two >= head_dim / 16) work on a head.
 template <int P, bool kBf16, int kKind, bool kDense>
-__global__ void __launch_bounds__(kRopeWarps * 32, !kDense ? 1 : kKind == kAppendCodes ? kDenseBlocksCodes : kDenseBlocks) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeWarps * 32, !kDense ? 1 : kKind >= kAppendCodes ? kDenseBlocksCodes : kDenseBlocks) rope_kernel(const __grid_constant__ RopeParams p) {
     pdl_launch_dependents();
     constexpr int kHeads = 32 / P;  // heads a step
-    constexpr bool kAppend = kKind != kRotate, kFp8 = kKind == kAppendCodes;
+    constexpr bool kAppend = kKind != kRotate, kFp8 = kKind == kAppendCodes, kFp4 = kKind == kAppendFp4;
     const int lane = threadIdx.x & 31, item = lane & (P - 1);
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * kRopeWarps + (threadIdx.x >> 5);
     // a token's parts are few where there are more than one: 32 bits
@@ -235,6 +238,59 @@ __global__ void __launch_bounds__(kRopeWarps * 32, !kDense ? 1 : kKind == kAppen
                 *reinterpret_cast<uint2*>(dst + s1) = make_uint2(c[2], c[3]);
                 if (item == 0) (is_k ? p.ks : p.vs)[(page * p.kv_heads + kvh) * p.page_size + off] = s;
             }
+        } else if constexpr (kFp4) {
+            if (__all_sync(0xffffffffu, is_q)) return;
+            float amax = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(f[e]));
+#pragma unroll
+            for (int d = P / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+            const float s = fp4_scale(amax), inverse = __frcp_rn(s);
+            float top[2] = {0.0f, 0.0f};  // of the lane's two chunks
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                f[e] = __fmul_rn(f[e], inverse);
+                top[e >> 3] = fmaxf(top[e >> 3], fabsf(f[e]));
+            }
+            // A block is chunks 2 b and 2 b + 1 of the head.  Those are a lane's own
+            // two, but for rotated halves, where lane i has chunks i and hb + i: the
+            // other chunk of each of its blocks is another lane's.
+            const bool halves = p.positions && !p.interleaved;
+            if (halves) {
+                const int hb = half >> 3;  // chunks of a half
+                const int ca = item ^ 1, cb = (hb + item) ^ 1;
+                const bool a_second = ca >= hb, b_second = cb >= hb;
+                const int base = lane & ~(P - 1);
+                const int la = base + ((a_second ? ca - hb : ca) & (P - 1)), lb = base + ((b_second ? cb - hb : cb) & (P - 1));
+                const float a0 = __shfl_sync(0xffffffffu, top[0], la), a1 = __shfl_sync(0xffffffffu, top[1], la);
+                const float b0 = __shfl_sync(0xffffffffu, top[0], lb), b1 = __shfl_sync(0xffffffffu, top[1], lb);
+                if (turns && is_k) {
+                    top[0] = fmaxf(top[0], a_second ? a1 : a0);
+                    top[1] = fmaxf(top[1], b_second ? b1 : b0);
+                } else {
+                    top[0] = top[1] = fmaxf(top[0], top[1]);
+                }
+            } else {
+                top[0] = top[1] = fmaxf(top[0], top[1]);
+            }
+            if (!is_q && work) {
+                const uint32_t byte0 = fp4_block(top[0]), byte1 = fp4_block(top[1]);
+                const float i0 = fp4_block_inverse(byte0), i1 = fp4_block_inverse(byte1);
+                float g0[8], g1[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    g0[e] = __fmul_rn(f[e], i0);
+                    g1[e] = __fmul_rn(f[8 + e], i1);
+                }
+                uint8_t* dst = (is_k ? p.kc : p.vc) + page * p.page_stride + kvh * p.head_stride + off * p.token_stride;
+                *reinterpret_cast<uint32_t*>(dst + (s0 >> 1)) = f32x8_to_e2m1(g0);
+                *reinterpret_cast<uint32_t*>(dst + (s1 >> 1)) = f32x8_to_e2m1(g1);
+                const int64_t at = (page * p.kv_heads + kvh) * p.page_size + off;
+                uint8_t* blocks = (is_k ? p.kb : p.vb) + at * (p.head_dim >> 4);
+                if ((s0 & 8) == 0) blocks[s0 >> 4] = static_cast<uint8_t>(byte0);
+                if ((s1 & 8) == 0) blocks[s1 >> 4] = static_cast<uint8_t>(byte1);
+                if (item == 0) (is_k ? p.ks : p.vs)[at] = s;
+            }
         } else if (kAppend && !is_q && work) {
             uint16_t* dst = reinterpret_cast<uint16_t*>(is_k ? p.kc : p.vc) + page * p.page_stride +
                             kvh * p.head_stride + off * p.token_stride;
@@ -254,8 +310,13 @@ __global__ void __launch_bounds__(kRopeWarps * 32, !kDense ? 1 : kKind == kAppen
 }
 
 template <int P, bool kDense>
-cudaError_t launch_form(const cudaLaunchConfig_t& cfg, const RopeParams& p, bool bf16, bool fp8) {
-    if (fp8)
+cudaError_t launch_form(const cudaLaunchConfig_t& cfg, const RopeParams& p, bool bf16, bool codes) {
+    if constexpr (P >= 2 && P <= 8) {  // heads of 32 to 128
+        if (p.kb)
+            return bf16 ? cudaLaunchKernelEx(&cfg, rope_kernel<P, true, kAppendFp4, kDense>, p)
+                        : cudaLaunchKernelEx(&cfg, rope_kernel<P, false, kAppendFp4, kDense>, p);
+    }
+    if (codes)
         return bf16 ? cudaLaunchKernelEx(&cfg, rope_kernel<P, true, kAppendCodes, kDense>, p)
                     : cudaLaunchKernelEx(&cfg, rope_kernel<P, false, kAppendCodes, kDense>, p);
     if (p.kv_heads)
@@ -266,7 +327,7 @@ cudaError_t launch_form(const cudaLaunchConfig_t& cfg, const RopeParams& p, bool
 }
 
 template <int P>
-cudaError_t launch_p(RopeParams p, bool bf16, bool fp8, cudaStream_t st) {
+cudaError_t launch_p(RopeParams p, bool bf16, bool codes, cudaStream_t st) {
     int sms = 0;
     cudaError_t e = device_sm_count(sms);
     if (e != cudaSuccess) return e;
@@ -288,8 +349,8 @@ cudaError_t launch_p(RopeParams p, bool bf16, bool fp8, cudaStream_t st) {
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (p.parts > 1) return launch_form<P, false>(cfg, p, bf16, fp8);
-    return launch_form<P, true>(cfg, p, bf16, fp8);
+    if (p.parts > 1) return launch_form<P, false>(cfg, p, bf16, codes);
+    return launch_form<P, true>(cfg, p, bf16, codes);
 }
 
 }  // namespace
@@ -312,7 +373,7 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
         p.axes = a.spec->axes;
         for (int i = 0, sum = 0; i < 4; ++i) p.bound[i] = sum += a.spec->sections[i];
     }
-    bool fp8 = false;
+    bool codes = false;
     if (a.cache) {
         const fp8w_kv_cache& c = *a.cache;
         p.k = static_cast<const uint16_t*>(a.k);
@@ -331,15 +392,17 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
         p.token_stride = c.token_stride;
         p.page_size = c.page_size;
         while ((1 << p.log_page) < c.page_size) ++p.log_page;
-        fp8 = c.dtype == FP8W_E4M3;
+        codes = c.dtype == FP8W_E4M3;
+        p.kb = c.k_blocks;
+        p.vb = c.v_blocks;
     }
     const bool bf16 = a.act == FP8W_BF16;
     const int items = a.head_dim / 16;
-    if (items <= 1) return launch_p<1>(p, bf16, fp8, st);
-    if (items <= 2) return launch_p<2>(p, bf16, fp8, st);
-    if (items <= 4) return launch_p<4>(p, bf16, fp8, st);
-    if (items <= 8) return launch_p<8>(p, bf16, fp8, st);
-    return launch_p<16>(p, bf16, fp8, st);
+    if (items <= 1) return launch_p<1>(p, bf16, codes, st);
+    if (items <= 2) return launch_p<2>(p, bf16, codes, st);
+    if (items <= 4) return launch_p<4>(p, bf16, codes, st);
+    if (items <= 8) return launch_p<8>(p, bf16, codes, st);
+    return launch_p<16>(p, bf16, codes, st);
 }
 
 int read_rope_device_error() {

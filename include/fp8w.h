@@ -46,7 +46,7 @@
 extern "C" {
 #endif
 
-#define FP8W_ABI_VERSION 13
+#define FP8W_ABI_VERSION 14
 
 #if defined(__GNUC__)
 #define FP8W_API __attribute__((visibility("default")))
@@ -66,8 +66,9 @@ typedef enum fp8w_status {
 } fp8w_status;
 
 /* Activation / output dtypes (FP8W_F32: fp8w_dequantize's output and
- * fp8w_quantize_ex's weights only; FP8W_E4M3: a cache's codes only). */
-enum { FP8W_BF16 = 1, FP8W_F16 = 2, FP8W_F32 = 3, FP8W_E4M3 = 4 };
+ * fp8w_quantize_ex's weights only; FP8W_E4M3 and
+ * FP8W_E2M1: a cache's codes only). */
+enum { FP8W_BF16 = 1, FP8W_F16 = 2, FP8W_F32 = 3, FP8W_E4M3 = 4, FP8W_E2M1 = 5 };
 
 /* Largest supported reduction length and row count. */
 #define FP8W_MAX_K 65536
@@ -346,6 +347,61 @@ FP8W_API fp8w_status fp8w_linear_w8a8(const uint8_t *x_codes, const float *x_sca
                              void *y, int out_dtype, int flags, void *stream);
 
 /*
+ * The 4-bit form: weights, or rows of a paged cache, in 4.5 bits a value.  A row
+ * of k values (k % 32 == 0) is
+ *   codes  [k / 2] bytes: e2m1 codes, value 2 i in the low half of byte i, value
+ *          2 i + 1 in the high half.  Code c stands for (0, 0.5, 1, 1.5, 2, 3, 4,
+ *          6)[c & 7], negative where c & 8.
+ *   blocks [k / 16] e4m3 bytes: the scales of 16 values each.
+ *   scale  one fp32.
+ * value = scale * e4m3(block) * e2m1(code).  The product of a block's scale and a
+ * code is exact in fp16 and bf16, so kernels that multiply in 16 bits lose
+ * nothing to the form.  The pages have no counterpart; they name the precision
+ * (page "11. Inference with NVFP4/MXFP8").
+ *
+ * fp8w_quantize_fp4 -- each row by this rule, every step in fp32 with one rounding:
+ *   scale = max(amax * fp32(1 / 2688), 2^-126), 1.0 where amax is 0  (2688 = 6 * 448)
+ *   y     = x * fp32(1 / scale)
+ *   block = e4m3(max over the block's |y| * fp32(1 / 6)), nearest even, saturated
+ *   code  = e2m1(y * fp32(1 / block)), nearest even, saturated; 0 where the block
+ *           byte is 0
+ * so codes, blocks and scales are exact functions of w.
+ *   w      [n, k] of w_dtype (FP8W_F32, FP8W_BF16 or FP8W_F16), device, 16-byte
+ *          aligned, finite.
+ *   codes  [n, k / 2], blocks [n, k / 16] uint8, device, 16-byte aligned (outputs).
+ *   scales [n] fp32, device, 4-byte aligned (output).
+ *   1 <= n <= FP8W_MAX_DIM, 32 <= k <= FP8W_MAX_K, k % 32 == 0.
+ */
+FP8W_API fp8w_status fp8w_quantize_fp4(const void *w, int w_dtype, int64_t n, int64_t k, uint8_t *codes,
+                              uint8_t *blocks, float *scales, void *stream);
+
+/*
+ * fp8w_dequantize_fp4 -- the values of n rows in the 4-bit form, each the exact
+ * product rounded once to out_dtype (as fp8w_dequantize).  The rows may be a
+ * weight's, or the slots of a cache laid out densely head by head ([pages,
+ * kv_heads, page_size] as n, head_dim as k).  w [n, k] of out_dtype, device, 16-byte
+ * aligned (output); other arguments and checks as fp8w_quantize_fp4.
+ */
+FP8W_API fp8w_status fp8w_dequantize_fp4(const uint8_t *codes, const uint8_t *blocks, const float *scales, int64_t n,
+                                int64_t k, int out_dtype, void *w, void *stream);
+
+/*
+ * fp8w_linear_fp4 -- fp8w_linear for weights in the 4-bit form:
+ *   y[i, r] = round_act( scales[r] * sum_c x[i, c] * e4m3(blocks[r, c / 16]) * e2m1(codes[r, c]) + bias[r] ).
+ *   codes  [n, k / 2], blocks [n, k / 16] uint8, device, 16-byte aligned.
+ *   flags  0 or FP8W_FLAG_WEIGHTS_READY (for codes, blocks and scales).
+ *   k % 32 == 0.  Other arguments as fp8w_linear.
+ * fp32 accumulation, scale and bias applied in fp32 with one rounding.  Up to 64
+ * tokens the codes are streamed into registers and multiplied there (bf16
+ * activations as fp16 times a power of two a token, which is exact but for values
+ * below 2^-28 of a token's largest, off by at most 2^-39 of that); beyond, the
+ * prefill GEMM.  One launch and no workspace.
+ */
+FP8W_API fp8w_status fp8w_linear_fp4(const void *x, int act_dtype, int64_t m, int64_t k, const uint8_t *codes,
+                            const uint8_t *blocks, const float *scales, const float *bias, int64_t n, void *y,
+                            int flags, void *stream);
+
+/*
  * What stands between the q, k and v linears of a decoder block and its o
  * linear: the rotation of queries and keys by their positions, a paged cache
  * of keys and values, and the attention of new tokens over it.  The pages
@@ -393,8 +449,13 @@ typedef struct fp8w_rope_spec {
  *              FP8W_E4M3: codes with one fp32 scale per slot and head in
  *              k_scales, v_scales [num_pages, kv_heads, page_size] (dense;
  *              NULL for the other types), scale = amax / 448 (1.0 if that is
- *              0), as fp8w_quantize gives a row.
- *   head_dim   a multiple of 16, 16..128.
+ *              0), as fp8w_quantize gives a row; or
+ *              FP8W_E2M1: the 4-bit form, rows as fp8w_quantize_fp4 gives them.
+ *              k and v are bytes of two codes, and the strides count bytes;
+ *              k_scales, v_scales as above; k_blocks, v_blocks uint8 [num_pages,
+ *              kv_heads, page_size, head_dim / 16] (dense, 16-byte aligned; NULL
+ *              for the other types).
+ *   head_dim   a multiple of 16, 16..128; with FP8W_E2M1 a multiple of 32.
  *   page_size  16, 32, 64, 128 or 256.
  * Pointers are 16-byte aligned (scales 4) and strides multiples of 16 bytes.
  * The struct itself is read during the call only.
@@ -404,6 +465,7 @@ typedef struct fp8w_kv_cache {
     float *k_scales, *v_scales;
     int64_t num_pages, page_stride, head_stride, token_stride;
     int dtype, kv_heads, head_dim, page_size;
+    uint8_t *k_blocks, *v_blocks;
 } fp8w_kv_cache;
 
 /*
@@ -436,8 +498,9 @@ FP8W_API fp8w_status fp8w_rope(const void *x, int act_dtype, int64_t tokens, int
  *              and is recorded (fp8w_device_error).
  *   q_out      like q, with q_out_stride; may be q (same stride).
  * A 16-bit cache gets the fp32 results rounded once (v: its own bits).  An
- * e4m3 cache gets the codes and scales that fp8w_quantize gives the fp32 rows:
- * the rotated key is not rounded to 16 bits in between.
+ * e4m3 cache gets the codes and scales that fp8w_quantize gives the fp32 rows, one
+ * of 4 bits those (and the blocks) that fp8w_quantize_fp4 gives them: the rotated
+ * key is not rounded to 16 bits in between.
  */
 FP8W_API fp8w_status fp8w_rope_append(const void *q, const void *k, const void *v, int act_dtype,
                              int64_t tokens, int q_heads, int64_t q_stride, int64_t k_stride,
@@ -477,8 +540,8 @@ FP8W_API fp8w_status fp8w_rope_append(const void *q, const void *k, const void *
  *   out          like q, with out_stride (output); it may not overlap q.
  * Scores, softmax and sums are fp32; the softmax weights are rounded to 16 bits
  * for the second product: to act_dtype, or with codes and few rows to fp16.
- * e4m3 scales multiply scores and weights in fp32, the weights before they are
- * rounded.  Below its normal numbers fp16 takes at most 2^-32 of the largest
+ * The scales of slots multiply scores and weights in fp32, the weights before they are
+ * rounded; those of 4-bit blocks go into the 16-bit operands, which is exact.  Below its normal numbers fp16 takes at most 2^-32 of the largest
  * from a weight (with codes: of the largest weight times value scale, rows of
  * zeros left out).  One rounding at the end.
  * Cached values of positions below len are finite, in act_dtype's range (a
