@@ -298,8 +298,12 @@ fp8w_status fp8w_linear_fp4(const void* x, int act_dtype, int64_t m, int64_t k, 
     a.blocks = blocks;
     a.early = (flags & FP8W_FLAG_WEIGHTS_READY) != 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // codes streamed into registers up to 8 tokens (14336 x 4096, 8 tokens: 12.9 us,
+    // 16.7 by the skinny kernel; 16: 17.4 with a wider form of it, 16.8), the skinny
+    // kernel up to 64, the prefill GEMM beyond
+    if (m <= fp8w::fp4_few_most) return cuda_status(fp8w::launch_fp4_few(a, s), "fp8w_linear_fp4 launch");
     if (use_prefill(m)) return cuda_status(fp8w::launch_prefill(a, s), "fp8w_linear_fp4 prefill launch");
-    return cuda_status(fp8w::launch_fp4_few(a, s), "fp8w_linear_fp4 launch");
+    return cuda_status(fp8w::launch_skinny(a, nullptr, s), "fp8w_linear_fp4 tensor-core launch");
 }
 
 fp8w_status fp8w_rope(const void* x, int act_dtype, int64_t tokens, int heads, int head_dim, int64_t x_stride,

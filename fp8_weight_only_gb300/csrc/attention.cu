@@ -943,8 +943,6 @@ __global__ void __launch_bounds__(AttnSmem<DP, kForm>::kThreads, 1)
                     // 128-, 64- or 32-byte swizzle
                     c[u] = lds128(src + ((L::kRawRow == 128 ? u ^ swz : L::kRawRow == 64 ? u ^ (swz >> 1) : u ^ (swz >> 2)) << 4));
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(rawempty(s));
                 if (i >= kStages && i + 1 >= kStages + 2 * static_cast<int>(freed)) {
                     if (!mbar_wait_warp(empty(fs), fphase, abort_flag)) {
                         if (lane == 0) attn_error(kErrWaitMma, abort_flag);
@@ -958,18 +956,12 @@ __global__ void __launch_bounds__(AttnSmem<DP, kForm>::kThreads, 1)
                 for (uint32_t u = 0; u < kChunks; ++u) {
                     const uint32_t w4[4] = {live ? c[u].x : 0u, live ? c[u].y : 0u, live ? c[u].z : 0u, live ? c[u].w : 0u};
                     if constexpr (kFp4) {  // 32 values: 16-byte chunks 4 u .. 4 u + 3 of the row
-                        uint32_t f[2];
-                        if constexpr (kBf16) {
-                            uint32_t f23;
-                            block_quad_bf16(blocks.two[u], f[0], f23);
-                        } else {
-                            f[0] = block_pair_f16(blocks.two[u]);
-                        }
+                        const uint32_t f = block_pair_f16(blocks.two[u]);
                         const uint32_t sub = dst + (u >> 1) * (kKeys * 128);
 #pragma unroll
                         for (uint32_t e = 0; e < 4; ++e) {
                             uint32_t v[4];
-                            fp4_operands<kBf16>(w4[e], e < 2 ? both_lo(f[0]) : both_hi(f[0]), v);
+                            fp4_operands<kBf16>(w4[e], e < 2 ? both_lo(f) : both_hi(f), v);
                             sts128(sub + (((4 * u + e) & 7) ^ swz) * 16, v[0], v[1], v[2], v[3]);
                         }
                         continue;
@@ -1003,7 +995,12 @@ __global__ void __launch_bounds__(AttnSmem<DP, kForm>::kThreads, 1)
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(full(d));
+                if (lane == 0) {
+                    mbar_arrive(full(d));
+                    // behind the stores of what was read from the slot: the reads are done
+                    // (an arrival right behind the loads can overtake them)
+                    mbar_arrive(rawempty(s));
+                }
                 if (++s == kRaw) s = 0, phase ^= 1u;
                 if (++d == kStages) d = 0;
             }

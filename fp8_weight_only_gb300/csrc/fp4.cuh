@@ -14,15 +14,12 @@ namespace fp8w {
 
 // 8 codes (one word) -> four f16x2, in order.  The conversion runs at 48 lanes a
 // cycle and SM (measured); placing the bits by shifts and masks at half of that.
+// One statement a byte: all four out of one unpacking take a move each.
 __device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t& p0, uint32_t& p1, uint32_t& p2, uint32_t& p3) {
-    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-        "mov.b32 {a, b, c, d}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-        : "=r"(p0), "=r"(p1), "=r"(p2), "=r"(p3)
-        : "r"(w));
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(p0) : "r"(w));
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(p1) : "r"(w));
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}" : "=r"(p2) : "r"(w));
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, d;\n\t}" : "=r"(p3) : "r"(w));
 }
 
 // Eight fp32 values -> their nearest-even, saturated codes in order.
@@ -55,30 +52,36 @@ __device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b) {
     return d;
 }
 
-// e2m1 values as fp16 pairs -> the same as bf16 pairs times 2^-112, exact: fp16's
-// exponent field moved to bf16's place is worth 2^(15 - 127) (and 0 stays 0; a
-// code's mantissa bit is fp16's highest, so the shift drops nothing).
-__device__ __forceinline__ uint32_t e2m1_f16x2_to_bf16x2(uint32_t p) { return ((p >> 3) & 0x0FFF0FFFu) | (p & 0x80008000u); }
-constexpr uint32_t kBf16x2Pow2_112 = 0x77807780u;  // bf16 2^112 in both halves
-
-// Scales of blocks as factors of the decoded codes, two blocks a word: of fp16
-// pairs, or (with what takes back the 2^-112) of bf16 pairs.
+// Scales of two blocks as a factor of decoded codes (fp16 pairs).
 __device__ __forceinline__ uint32_t block_pair_f16(uint32_t two) { return e4m3x2_to_f16x2(static_cast<uint16_t>(two)); }
-__device__ __forceinline__ void block_quad_bf16(uint32_t four, uint32_t& p01, uint32_t& p23) {
-    e4m3x4_to_bf16x2(four, p01, p23);
-    p01 = bf16x2_mul(p01, kBf16x2Pow2_112);
-    p23 = bf16x2_mul(p23, kBf16x2Pow2_112);
-}
 __device__ __forceinline__ uint32_t both_lo(uint32_t pair) { return __byte_perm(pair, pair, 0x1010); }
 __device__ __forceinline__ uint32_t both_hi(uint32_t pair) { return __byte_perm(pair, pair, 0x3232); }
 
-// Eight codes as 16-bit operands, in order, times their block's factor (above).
+// fp16 pair -> bf16 pair (exact where the values have 8 significant bits), by
+// fp32: two instructions of the FMA pipe and one of the ALU's, which the codes'
+// conversion keeps busy.  (Moving the exponent's bits by a shift and two masks, and
+// 2^-112 into the block's factor: 32 tokens on 14336 x 4096 PENDING.)
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t p) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 a, b;\n\t.reg .f32 x, y;\n\t"
+        "mov.b32 {a, b}, %1;\n\t"
+        "cvt.f32.f16 x, a;\n\tcvt.f32.f16 y, b;\n\t"
+        "cvt.rn.bf16x2.f32 %0, y, x;\n\t}"
+        : "=r"(r)
+        : "r"(p));
+    return r;
+}
+
+// Eight codes as 16-bit operands, in order, times their block's scale (both halves
+// of `factor`).
 template <bool kBf16>
 __device__ __forceinline__ void fp4_operands(uint32_t w, uint32_t factor, uint32_t* v) {
-    uint32_t p[4];
-    e2m1x8_to_f16x2(w, p[0], p[1], p[2], p[3]);
+    e2m1x8_to_f16x2(w, v[0], v[1], v[2], v[3]);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = kBf16 ? bf16x2_mul(e2m1_f16x2_to_bf16x2(p[e]), factor) : f16x2_mul(p[e], factor);
+    for (int e = 0; e < 4; ++e) {
+        v[e] = f16x2_mul(v[e], factor);
+        if constexpr (kBf16) v[e] = f16x2_to_bf16x2(v[e]);
+    }
 }
 
 // The quantiser's rule, all steps in fp32 with one rounding each:

@@ -35,13 +35,15 @@ namespace fp8w {
 
 namespace {
 
-constexpr int kWarps = 16, kThreads = 32 * kWarps;
+constexpr int kTokens = 8;         // columns of a product: the most tokens of a CTA
+constexpr int kWarps = 24, kThreads = 32 * kWarps;  // of a CTA (one an SM)
+constexpr int kDepth = 2;          // steps of codes that a warp holds or awaits
 constexpr int kRowsTile = 16;      // output channels a tile
+constexpr int kPitch = 20;         // of a token's sums of a tile in shared memory (words): no two lanes of a store share a bank
 constexpr int kStepK = 128;        // inputs a step
 constexpr int kMaxSplit = 8;       // CTAs a cluster
 constexpr uint32_t kSmemMost = 224 * 1024;
-constexpr uint32_t kPartialMost = 48 * 1024;  // a CTA's sums kept for its cluster, about
-constexpr int kHeld = 4;           // 16-byte pieces of activations a thread keeps between its two looks at them
+constexpr int kHeld = 4;           // 16-byte pieces of activations that a thread has in flight (bf16: and keeps between its two looks at them)
 
 struct Fp4Params {
     const uint16_t* x;
@@ -50,12 +52,15 @@ struct Fp4Params {
     const float* scales;
     const float* bias;
     uint16_t* y;
-    int64_t m, n, k, tiles;
+    int64_t m, n, k;
+    int slab;      // tokens of a CTA, at most
+    int tiles;     // of 16 channels
+    int rounds;    // of tiles, of each cluster
     int steps;     // of all inputs
-    int per_rank;  // of a rank
-    int cl;        // CTAs a cluster
-    int g;         // warps a tile
-    int batch;     // rounds of tiles between two joins of a cluster
+    int per_rank;  // of a rank, at most (rank r: from r steps / cl on)
+    int cl, cl_log2;         // CTAs a cluster
+    int g, j;      // warps a tile, tiles at a time
+    uint32_t piece_inverse, tile_inverse, g_inverse, j_inverse;  // 2^32 / (16 per_rank), / results a tile, / g, / j, rounded up
     int early;
 };
 
@@ -84,18 +89,23 @@ __device__ __forceinline__ void group_bar(int group, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(threads) : "memory");
 }
 
+// x / d by d's rounded-up reciprocal: exact for x d < 2^32 (0 stands for 2^32, d = 1).
+__device__ __forceinline__ int divide(int x, uint32_t inverse) {
+    return inverse ? static_cast<int>(__umulhi(static_cast<uint32_t>(x), inverse)) : x;
+}
+__host__ inline uint32_t inverse_of(int64_t d) { return static_cast<uint32_t>(((1ull << 32) + d - 1) / d); }
+
 // Shared memory of a launch, in bytes from its start.
 struct Fp4Layout {
     uint32_t x, red, part, top, total;
 };
-__host__ __device__ inline Fp4Layout fp4_layout(int nt, int tokens, int per_rank, int batch, int j, bool cluster) {
+__host__ __device__ inline Fp4Layout fp4_layout(int tokens, int per_rank, int rounds, int j, bool cluster) {
     Fp4Layout l;
-    const uint32_t rows = nt == 1 ? tokens : 8 * nt;           // tokens stored of a step
     l.x = 0;
-    l.red = l.x + static_cast<uint32_t>(per_rank) * rows * (kStepK * 2);
-    l.part = l.red + 2 * kWarps * static_cast<uint32_t>(tokens) * kRowsTile * 4;  // [2][warp][token][channel]
-    l.top = l.part + (cluster ? static_cast<uint32_t>(batch) * j * tokens * kRowsTile * 4 : 0);
-    l.total = l.top + 8 * nt * 4 * 2;                           // largest bits, factor back
+    l.red = l.x + static_cast<uint32_t>(per_rank) * tokens * (kStepK * 2);
+    l.part = l.red + 2 * kWarps * static_cast<uint32_t>(tokens) * kPitch * 4;  // [2][warp][token][channel]
+    l.top = l.part + (cluster ? static_cast<uint32_t>(rounds) * j * tokens * kRowsTile * 4 : 0);
+    l.total = l.top + kTokens * 4 * 2;                           // largest bits, factor back
     return l;
 }
 
@@ -105,86 +115,59 @@ struct Fp4Step {
     uint32_t b0, b1;
 };
 
-// The sums of `count` rounds of tiles from round `first` on, over the ranks in
-// order, to the output.  Every CTA of the cluster calls it with the same rounds.
-template <bool kBf16>
-__device__ __noinline__ void join_ranks(const Fp4Params& p, uint32_t part, int first, int count, int J, int cluster, int clusters, int rank,
-                                        int64_t m0, int slab, int tokens) {
-    cluster_sync_all();
-    const int per_tile = slab * kRowsTile, all = count * J * per_tile;
-    for (int o = rank * kThreads + static_cast<int>(threadIdx.x); o < all; o += p.cl * kThreads) {
-        const int n = o / per_tile, in = o - n * per_tile, token = in / kRowsTile, i = n / J;
-        const int64_t row = ((static_cast<int64_t>(first + i) * clusters + cluster) * J + (n - i * J)) * kRowsTile + (in & (kRowsTile - 1));
-        if (row >= p.n || token >= tokens) continue;
-        float v[kMaxSplit], sum = 0.0f;
-#pragma unroll
-        for (int r = 0; r < kMaxSplit; ++r) v[r] = r < p.cl ? ld_shared_cluster_f32(mapa_shared(part + static_cast<uint32_t>(o) * 4, r)) : 0.0f;
-#pragma unroll
-        for (int r = 0; r < kMaxSplit; ++r) sum += v[r];
-        p.y[(m0 + token) * p.n + row] = round_out<kBf16>(fmaf(sum, p.scales[row], p.bias ? p.bias[row] : 0.0f));
-    }
-    cluster_sync_all();  // the sums have been read: they may be written over, and CTAs may leave
-}
-
 }  // namespace
 
-// NT: 8-token tiles of a slab.
-template <int NT, bool kBf16, int kDepth>
+template <bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1) fp4_few_kernel(const __grid_constant__ Fp4Params p) {
     extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int rank = p.cl > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-    const int cluster = static_cast<int>(blockIdx.x) / p.cl, clusters = static_cast<int>(gridDim.x) / p.cl;
-    const int64_t m0 = static_cast<int64_t>(blockIdx.y) * (8 * NT);
-    const int tokens = p.m - m0 < 8 * NT ? static_cast<int>(p.m - m0) : 8 * NT;
-    const int G = p.g, J = kWarps / G, group = warp / G, wk = warp - group * G;
-    const int64_t span = static_cast<int64_t>(clusters) * J;
-    const int rounds = static_cast<int>((p.tiles + span - 1) / span);
+    const int cluster = static_cast<int>(blockIdx.x) >> p.cl_log2, clusters = static_cast<int>(gridDim.x) >> p.cl_log2;
+    const int64_t m0 = static_cast<int64_t>(blockIdx.y) * p.slab;
+    const int tokens = p.m - m0 < p.slab ? static_cast<int>(p.m - m0) : p.slab;
+    const int G = p.g, J = p.j, group = divide(warp, p.g_inverse), wk = warp - group * G, rounds = p.rounds;
     // sizes by a full slab, so that all slabs and ranks have the same places
-    const int slab = p.m < 8 * NT ? static_cast<int>(p.m) : 8 * NT;
-    const Fp4Layout L = fp4_layout(NT, slab, p.per_rank, p.batch, J, p.cl > 1);
-    const int rows = NT == 1 ? slab : 8 * NT;  // token rows of a step in shared memory (a tile of 8 at a time beyond 8)
-    const int step0 = rank * p.per_rank;
-    const int mine = p.steps - step0 < p.per_rank ? (p.steps > step0 ? p.steps - step0 : 0) : p.per_rank;
-    const int S = (mine + G - 1) / G;          // steps of a warp a tile
+    const int slab = p.slab;
+    const Fp4Layout L = fp4_layout(slab, p.per_rank, rounds, J, p.cl > 1);
+    const int step0 = rank * p.steps >> p.cl_log2, mine = ((rank + 1) * p.steps >> p.cl_log2) - step0;
+    const int S = divide(mine - wk + G - 1, p.g_inverse);  // this warp's steps of a tile: 1 at least (the launch sees to it)
 
     pdl_launch_dependents();
     if (!p.early) pdl_wait();
 
     // ---------------------------------------------------------------- loads --
-    const int64_t code_row = p.k >> 1, block_row = p.k >> 4;
-    // tile round i of this warp's group
-    auto tile_at = [&](int i) { return (static_cast<int64_t>(i) * clusters + cluster) * J + group; };
-    int li = 0, ls = 0;  // the load stream: round and step in it
-    const uint8_t *c_at = nullptr, *b_at = nullptr;
-    int64_t c_8 = 0, b_8 = 0;  // from row g to row g + 8 (0 where that is past the last)
-    bool l_live = false;
+    // tile of this warp's group in round i
+    auto tile_at = [&](int i) { return (i * clusters + cluster) * J + group; };
+    // Rounds of this group.  With a cluster all groups go through all rounds, for they
+    // join, and one without a tile takes the last again, for nothing.
+    const int my_rounds = p.cl > 1 || tile_at(rounds - 1) < p.tiles ? rounds : rounds - 1;
+    // A lane's bytes of codes in a row: from here on, G steps apart, and none past the
+    // row's last (there it takes the last again: the activations are zeros).
+    const int o_first = (step0 + wk) * (kStepK / 2) + t * 16, o_last = static_cast<int>(p.k >> 1) - 16, o_step = G * (kStepK / 2);
+    int li = 0, ls = S, lo = o_first;  // the load stream: round, steps to come of it, offset
+    const uint8_t *c0, *c1, *b0, *b1;  // rows g and g + 8 of its tile
     auto open = [&] {
-        const int64_t tile = tile_at(li);
-        l_live = li < rounds && tile < p.tiles;
-        if (!l_live) return;
         // channels past the last read the last's: their sums go nowhere
-        const int64_t r0 = tile * kRowsTile + g, a = r0 < p.n ? r0 : p.n - 1, b = r0 + 8 < p.n ? r0 + 8 : p.n - 1;
-        c_at = p.codes + a * code_row;
-        b_at = p.blocks + a * block_row;
-        c_8 = (b - a) * code_row;
-        b_8 = (b - a) * block_row;
+        const int64_t r0 = static_cast<int64_t>(min(tile_at(li), p.tiles - 1)) * kRowsTile + g;
+        const int64_t a = r0 < p.n ? r0 : p.n - 1, b = r0 + 8 < p.n ? r0 + 8 : p.n - 1;
+        c0 = p.codes + a * (p.k >> 1);
+        c1 = p.codes + b * (p.k >> 1);
+        b0 = p.blocks + a * (p.k >> 4);
+        b1 = p.blocks + b * (p.k >> 4);
     };
     open();
     auto load = [&](Fp4Step& s) {
-        const int step = wk + ls * G;
-        const int64_t k0 = static_cast<int64_t>(step0 + step) * kStepK + t * 32;
-        s.c0 = s.c1 = make_uint4(0u, 0u, 0u, 0u);
-        s.b0 = s.b1 = 0u;
-        if (l_live && step < mine && k0 < p.k) {
-            s.c0 = ld_once_v4(c_at + (k0 >> 1));
-            s.c1 = ld_once_v4(c_at + c_8 + (k0 >> 1));
-            s.b0 = ld_u16(b_at + (k0 >> 4));
-            s.b1 = ld_u16(b_at + b_8 + (k0 >> 4));
-        }
-        if (++ls >= S) {
-            ls = 0;
+        if (li >= my_rounds) return;
+        const uint32_t o = static_cast<uint32_t>(min(lo, o_last));
+        s.c0 = ld_once_v4(c0 + o);
+        s.c1 = ld_once_v4(c1 + o);
+        s.b0 = ld_u16(b0 + (o >> 3));
+        s.b1 = ld_u16(b1 + (o >> 3));
+        lo += o_step;
+        if (--ls == 0) {
+            ls = S;
+            lo = o_first;
             ++li;
             open();
         }
@@ -195,102 +178,114 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_few_kernel(const __grid_const
 
     // ---------------------------------------------------------- activations --
     if (p.early) pdl_wait();  // x may come from the kernel before, y may still be read by it
+    uint32_t* top = reinterpret_cast<uint32_t*>(smem + L.top);
+    float* back = reinterpret_cast<float*>(smem + L.top) + kTokens;
     {
-        const int pieces = mine * (kStepK / 8), total = slab * pieces;  // 8 values each; rows past the last are zeros
+        // pieces of 8 values, a rank's share of each token; beyond the inputs and the
+        // tokens they are zeros
+        const int pieces = p.per_rank * (kStepK / 8), total = slab * pieces;
         const uint16_t* x = p.x + m0 * p.k + static_cast<int64_t>(step0) * kStepK;
-        const int64_t k_left = p.k - static_cast<int64_t>(step0) * kStepK;
-        auto fetch = [&](int token, int piece) {
+        const int inputs = static_cast<int>(p.k) - step0 * kStepK;
+        auto token_of = [&](int i) { return divide(i, p.piece_inverse); };
+        auto fetch = [&](int i) {
+            const int token = token_of(i), piece = i - token * pieces;
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (token < tokens && piece * 8 < k_left) v = *reinterpret_cast<const uint4*>(x + token * p.k + piece * 8);
+            if (token < tokens && piece * 8 < inputs) v = *reinterpret_cast<const uint4*>(x + token * p.k + piece * 8);
             return v;
         };
         // piece: inputs 8 (piece % 4) .. of lane t's 32 in step piece / 16
         auto put = [&](int token, int piece, const uint4& v) {
             const int step = piece >> 4, w = piece & 3, tt = (piece >> 2) & 3;
-            const int part = NT == 1 ? rows : 8, tile = NT == 1 ? 0 : token >> 3, at = NT == 1 ? token : token & 7;
-            sts128(sbase + L.x + ((((step * NT + tile) * 4 + w) * part + at) * 4 + tt) * 16, v.x, v.y, v.z, v.w);
+            sts128(sbase + L.x + (((step * 4 + w) * slab + token) * 4 + tt) * 16, v.x, v.y, v.z, v.w);
         };
-        uint32_t* top = reinterpret_cast<uint32_t*>(smem + L.top);
-        float* back = reinterpret_cast<float*>(smem + L.top) + 8 * NT;
         if constexpr (kBf16) {
-            if (tid < 8 * NT) top[tid] = 0u;
+            if (tid < kTokens) top[tid] = 0u;
             __syncthreads();
-            uint4 kept[kHeld];
-            auto look = [&](int i, const uint4& v) {
-                const int token = i / pieces;
-                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-                uint32_t mx = 0u;
+        }
+        uint4 kept[kHeld];
+        // a batch of pieces in flight, the first kept for the second look
+        auto fetch_batch = [&](int i0) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mx = max(mx, max(u[e] & 0x7FFFu, (u[e] >> 16) & 0x7FFFu));
-                if (mx) atomicMax(top + token, mx);
-            };
-            int u = 0;
-#pragma unroll
-            for (; u < kHeld; ++u) {
-                const int i = tid + u * kThreads;
-                kept[u] = make_uint4(0u, 0u, 0u, 0u);
-                if (i < total) kept[u] = fetch(i / pieces, i % pieces);
+            for (int e = 0; e < kHeld; ++e) {
+                const int i = i0 + tid + e * kThreads;
+                kept[e] = make_uint4(0u, 0u, 0u, 0u);
+                if (i < total) kept[e] = fetch(i);
             }
+        };
+        if constexpr (kBf16) {
+            auto look = [&](int i0) {
 #pragma unroll
-            for (int e = 0; e < kHeld; ++e)
-                if (tid + e * kThreads < total) look(tid + e * kThreads, kept[e]);
-            for (int i = tid + kHeld * kThreads; i < total; i += kThreads) look(i, fetch(i / pieces, i % pieces));
+                for (int e = 0; e < kHeld; ++e) {
+                    const int i = i0 + tid + e * kThreads;
+                    if (i - lane >= total) break;  // the warp's first piece
+                    const uint4 v = kept[e];
+                    uint32_t mx = 0u;  // largest magnitude of a lane's four pairs
+                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) mx = max(mx, max(u[q] & 0x7FFFu, (u[q] >> 16) & 0x7FFFu));
+                    const int first = token_of(i - lane), last = token_of(min(i - lane + 31, total - 1));
+                    if (first == last) {
+                        mx = __reduce_max_sync(0xffffffffu, mx);
+                        if (lane == 0 && mx) atomicMax(top + first, mx);
+                    } else if (i < total && mx) {
+                        atomicMax(top + token_of(i), mx);
+                    }
+                }
+            };
+            for (int i0 = kHeld * kThreads; i0 < total; i0 += kHeld * kThreads) {
+                fetch_batch(i0);
+                look(i0);
+            }
+            fetch_batch(0);
+            look(0);
             __syncthreads();
             // exponent of the factor, 14 - (e - 127), within fp32's normal numbers
             auto up_of = [&](int token) { return min(max(127 + 14 - (static_cast<int>(top[token] >> 7) - 127), 1), 253); };
-            if (tid < 8 * NT) back[tid] = __int_as_float((254 - up_of(tid)) << 23);
-            auto turn = [&](int i, const uint4& v) {
-                const int token = i / pieces;
-                const float f = __int_as_float(up_of(token) << 23);
-                auto two = [&](uint32_t w) {
-                    uint32_t r;
-                    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(bf16_hi_to_f32(w) * f), "f"(bf16_lo_to_f32(w) * f));
-                    return r;
-                };
-                put(token, i - token * pieces, make_uint4(two(v.x), two(v.y), two(v.z), two(v.w)));
-            };
-#pragma unroll
-            for (int e = 0; e < kHeld; ++e)
-                if (tid + e * kThreads < total) turn(tid + e * kThreads, kept[e]);
-            for (int i = tid + kHeld * kThreads; i < total; i += kThreads) turn(i, fetch(i / pieces, i % pieces));
-        } else {
-            for (int i0 = tid; i0 < total; i0 += kHeld * kThreads) {
-                uint4 kept[kHeld];
+            if (tid < kTokens) back[tid] = __int_as_float((254 - up_of(tid)) << 23);
+            for (int i0 = 0; i0 < total; i0 += kHeld * kThreads) {
+                if (i0 > 0) fetch_batch(i0);
 #pragma unroll
                 for (int e = 0; e < kHeld; ++e) {
-                    const int i = i0 + e * kThreads;
-                    if (i < total) kept[e] = fetch(i / pieces, i % pieces);
-                }
-#pragma unroll
-                for (int e = 0; e < kHeld; ++e) {
-                    const int i = i0 + e * kThreads;
-                    if (i < total) put(i / pieces, i % pieces, kept[e]);
+                    const int i = i0 + tid + e * kThreads;
+                    if (i >= total) break;
+                    const int token = token_of(i);
+                    const float f = __int_as_float(up_of(token) << 23);
+                    auto two = [&](uint32_t w) {
+                        uint32_t r;
+                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(bf16_hi_to_f32(w) * f), "f"(bf16_lo_to_f32(w) * f));
+                        return r;
+                    };
+                    put(token, i - token * pieces, make_uint4(two(kept[e].x), two(kept[e].y), two(kept[e].z), two(kept[e].w)));
                 }
             }
-            if (tid < 8 * NT) back[tid] = 1.0f;
-        }
-        if constexpr (NT > 1) {
-            // the last tile's rows past the slab
-            const int spare = 8 * NT - slab;
-            for (int i = tid; i < spare * pieces; i += kThreads) put(slab + i / pieces, i % pieces, make_uint4(0u, 0u, 0u, 0u));
+        } else {
+            for (int i0 = 0; i0 < total; i0 += kHeld * kThreads) {
+                fetch_batch(i0);
+#pragma unroll
+                for (int e = 0; e < kHeld; ++e) {
+                    const int i = i0 + tid + e * kThreads;
+                    if (i >= total) break;
+                    const int token = token_of(i);
+                    put(token, i - token * pieces, kept[e]);
+                }
+            }
+            if (tid < kTokens) back[tid] = 1.0f;
         }
     }
     __syncthreads();
 
     // -------------------------------------------------------------- compute --
-    float acc[NT][4];
+    float acc[4];  // channels g (0, 1) and g + 8 (2, 3), tokens 2 t and 2 t + 1
     auto clear = [&] {
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) acc[e] = 0.0f;
     };
     clear();
-    const bool reads = NT > 1 || g < rows;
-    const uint32_t x_lane = sbase + L.x + (NT == 1 ? (g * 4 + t) : lane) * 16;
-    const uint32_t x_word = (NT == 1 ? rows : 8) * 64, x_step = NT * 4 * x_word;
-    auto compute = [&](int step, const Fp4Step& s) {
-        const uint32_t at = x_lane + static_cast<uint32_t>(step) * x_step;
+    // Columns of tokens that are not there read another's: their sums go nowhere.
+    const uint32_t x_word = slab * 64, x_step = 4 * x_word;
+    const uint32_t x_first = sbase + L.x + (min(g, slab - 1) * 4 + t) * 16 + static_cast<uint32_t>(wk) * x_step;
+    uint32_t x_at = x_first;
+    auto compute = [&](const Fp4Step& s) {
         const uint32_t f0 = block_pair_f16(s.b0), f1 = block_pair_f16(s.b1);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -299,90 +294,107 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_few_kernel(const __grid_const
             uint32_t a[4], b[4];
             fp4_operands<false>(w0, q < 2 ? both_lo(f0) : both_hi(f0), a);
             fp4_operands<false>(w1, q < 2 ? both_lo(f1) : both_hi(f1), b);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (reads) x = lds128(at + (j * 4 + q) * x_word);
-                mma_f16(acc[j], a[0], b[0], a[1], b[1], x.x, x.y);
-                mma_f16(acc[j], a[2], b[2], a[3], b[3], x.z, x.w);
-            }
+            const uint4 x = lds128(x_at + q * x_word);
+            mma_f16(acc, a[0], b[0], a[1], b[1], x.x, x.y);
+            mma_f16(acc, a[2], b[2], a[3], b[3], x.z, x.w);
         }
     };
     // sums of a tile: [warp][token][channel]
     const int gt = G * 32, gtid = tid - group * gt;
-    const float* back = reinterpret_cast<const float*>(smem + L.top) + 8 * NT;
     const int channel = gtid & (kRowsTile - 1);  // of this thread's results in every tile (gt is a multiple of 16)
     float scale = 0.0f, bias = 0.0f;
     auto ask = [&](int i) {  // ahead of their use
-        const int64_t row = tile_at(i) * kRowsTile + channel;
-        if (p.cl == 1 && i < rounds && row < p.n) {
+        const int64_t row = static_cast<int64_t>(tile_at(i)) * kRowsTile + channel;
+        if (p.cl == 1 && gtid < slab * kRowsTile && i < rounds && row < p.n) {
             scale = p.scales[row];
             bias = p.bias ? p.bias[row] : 0.0f;
         }
     };
     ask(0);
     auto finish = [&](int i) {
-        const uint32_t buf = sbase + L.red + static_cast<uint32_t>((i & 1) * kWarps * slab * kRowsTile) * 4;
-        const uint32_t own = buf + static_cast<uint32_t>(warp * slab * kRowsTile) * 4;
+        const uint32_t pitch = slab * kPitch * 4;  // of a warp's sums
+        const uint32_t buf = sbase + L.red + static_cast<uint32_t>((i & 1) * kWarps) * pitch;
+        const uint32_t own = buf + warp * pitch + (2 * t * kPitch + g) * 4;
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int token = 8 * j + 2 * t + (e & 1), ch = g + 8 * (e >> 1);
-                if (token < slab) sts_f1(own + (token * kRowsTile + ch) * 4, acc[j][e]);
+        for (int e = 0; e < 2; ++e)
+            if (2 * t + e < slab) {
+                sts_f1(own + e * kPitch * 4, acc[e]);
+                sts_f1(own + e * kPitch * 4 + 32, acc[2 + e]);
             }
         clear();
         if (G > 1)
             group_bar(group, gt);  // groups of 1 warp have no number for one
         else
             __syncwarp();
-        const int64_t row = tile_at(i) * kRowsTile + channel;
+        const int64_t row = static_cast<int64_t>(tile_at(i)) * kRowsTile + channel;
         for (int o = gtid; o < slab * kRowsTile; o += gt) {
             const int token = o / kRowsTile;
+            const uint32_t from = buf + group * G * pitch + (token * kPitch + channel) * 4;
             float sum = 0.0f;
-            for (int w = 0; w < G; ++w) sum += lds_f1(buf + static_cast<uint32_t>((group * G + w) * slab * kRowsTile + o) * 4);
+#pragma unroll 4
+            for (int w = 0; w < G; ++w) sum += lds_f1(from + w * pitch);
             sum *= back[token];
             if (p.cl > 1)
-                sts_f1(sbase + L.part + static_cast<uint32_t>((i % p.batch * J + group) * slab * kRowsTile + o) * 4, sum);
+                sts_f1(sbase + L.part + static_cast<uint32_t>((i * J + group) * slab * kRowsTile + o) * 4, sum);
             else if (token < tokens && row < p.n)
                 p.y[(m0 + token) * p.n + row] = round_out<kBf16>(fmaf(sum, scale, bias));
         }
         ask(i + 1);
     };
-    {
-        int ci = 0, cs = 0;  // the compute stream
-        // with a cluster all groups go through all rounds, and join
-        auto goes_on = [&](int i) { return i < rounds && (p.cl > 1 || tile_at(i) < p.tiles); };
-        bool more = goes_on(0);
-        while (more) {
+    int cs = S;  // steps to come of round ci
+    for (int ci = 0; ci < my_rounds;) {
 #pragma unroll
-            for (int d = 0; d < kDepth; ++d) {
-                if (more) {
-                    const int step = wk + cs * G;
-                    const Fp4Step s = held[d];
-                    load(held[d]);
-                    if (step < mine) compute(step, s);
-                    if (++cs >= S) {
-                        finish(ci);
-                        cs = 0;
-                        ++ci;
-                        more = goes_on(ci);
-                        if (p.cl > 1 && (ci % p.batch == 0 || !more)) {
-                            const int first = (ci - 1) / p.batch * p.batch;
-                            join_ranks<kBf16>(p, sbase + L.part, first, ci - first, J, cluster, clusters, rank, m0, slab, tokens);
-                        }
-                    }
-                }
+        for (int d = 0; d < kDepth; ++d) {
+            compute(held[d]);
+            load(held[d]);
+            x_at += G * x_step;
+            if (--cs == 0) {
+                finish(ci);
+                cs = S;
+                x_at = x_first;
+                if (++ci == my_rounds) break;
             }
         }
     }
+    if (p.cl == 1) return;
+
+    // ----------------------------------------------------------------- join --
+    // the sums over the ranks in order, a share of them each
+    cluster_sync_all();
+    constexpr int kAtOnce = 4;  // results of a thread whose reads are in flight together
+    const int per_tile = slab * kRowsTile, all = rounds * J * per_tile, stride = p.cl * kThreads;
+    for (int o0 = rank * kThreads + tid; o0 < all; o0 += kAtOnce * stride) {
+        float v[kAtOnce][kMaxSplit], sc[kAtOnce], bi[kAtOnce];
+        int64_t at[kAtOnce];  // of the result, -1: none
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int o = o0 + u * stride;
+            const int n = divide(o, p.tile_inverse), in = o - n * per_tile, token = in / kRowsTile, i = divide(n, p.j_inverse);
+            const int64_t row = static_cast<int64_t>((i * clusters + cluster) * J + (n - i * J)) * kRowsTile + (in & (kRowsTile - 1));
+            const bool live = o < all && row < p.n && token < tokens;
+            at[u] = live ? (m0 + token) * p.n + row : -1;
+            sc[u] = live ? p.scales[row] : 0.0f;
+            bi[u] = live && p.bias ? p.bias[row] : 0.0f;
+#pragma unroll
+            for (int r = 0; r < kMaxSplit; ++r)
+                v[u][r] = live && r < p.cl ? ld_shared_cluster_f32(mapa_shared(sbase + L.part + static_cast<uint32_t>(o) * 4, r)) : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int r = 0; r < kMaxSplit; ++r) sum += v[u][r];
+            if (at[u] >= 0) p.y[at[u]] = round_out<kBf16>(fmaf(sum, sc[u], bi[u]));
+        }
+    }
+    cluster_sync_all();  // no CTA leaves while another may read its shared memory
 }
 
 namespace {
 
-template <int NT, bool kBf16>
-cudaError_t launch_form(const LinearArgs& a, cudaStream_t st) {
-    auto kern = fp4_few_kernel<NT, kBf16, 4>;
+template <bool kBf16>
+cudaError_t launch_slab(const LinearArgs& a, int most, cudaStream_t st) {
+    auto kern = fp4_few_kernel<kBf16>;
     static std::once_flag attr_once[64];
     static int active[64][4];  // clusters of 1, 2, 4, 8 CTAs that fit the device
     int dev = 0;
@@ -422,11 +434,12 @@ cudaError_t launch_form(const LinearArgs& a, cudaStream_t st) {
     p.m = a.m;
     p.n = a.n;
     p.k = a.k;
-    p.tiles = (a.n + kRowsTile - 1) / kRowsTile;
+    p.tiles = static_cast<int>((a.n + kRowsTile - 1) / kRowsTile);
     p.steps = static_cast<int>((a.k + kStepK - 1) / kStepK);
     p.early = a.early ? 1 : 0;
-    const int64_t slabs = (a.m + 8 * NT - 1) / (8 * NT);
-    const int slab = a.m < 8 * NT ? static_cast<int>(a.m) : 8 * NT;
+    const int slab = a.m < most ? static_cast<int>(a.m) : most;
+    const int64_t slabs = (a.m + slab - 1) / slab;
+    p.slab = slab;
     // Clusters and warps a tile that leave a warp the fewest steps, where the
     // activations fit; a tile's joins count as part of a step.
     double best = 1e30;
@@ -434,34 +447,41 @@ cudaError_t launch_form(const LinearArgs& a, cudaStream_t st) {
     uint32_t smem = 0;
     for (int c = 0; c < 4; ++c) {
         const int cl = 1 << c;
-        if (active[dev][c] < 1 || (cl > 1 && cl > p.steps)) continue;
+        if (active[dev][c] < 1) continue;
         const int per_rank = (p.steps + cl - 1) / cl;
-        for (int g = 1; g <= kWarps; g <<= 1) {
+        for (int g = 1; g <= kWarps && g <= p.steps / cl; ++g) {  // each warp has a step of each tile
+            if (kWarps % g != 0) continue;
             const int J = kWarps / g, S = (per_rank + g - 1) / g;
-            const int64_t want = (p.tiles + J - 1) / J;  // clusters of work
+            const int64_t want = (static_cast<int64_t>(p.tiles) + J - 1) / J;  // clusters of work
             int64_t clusters = active[dev][c] / slabs > 1 ? active[dev][c] / slabs : 1;
             if (clusters > want) clusters = want;
             const int64_t rounds = (want + clusters - 1) / clusters;
             if (rounds > 0x3fffffff) continue;
-            int64_t batch = static_cast<int64_t>(kPartialMost) / (static_cast<int64_t>(J) * slab * kRowsTile * 4);
-            batch = batch < 1 ? 1 : batch < rounds ? batch : rounds;
-            const Fp4Layout l = fp4_layout(NT, slab, per_rank, static_cast<int>(batch), J, cl > 1);
+            // (where that many sums take over half of it, they do not fit)
+            if (cl > 1 && rounds * J * slab * kRowsTile * 4 > kSmemMost / 2) continue;
+            const Fp4Layout l = fp4_layout(slab, per_rank, static_cast<int>(rounds), J, cl > 1);
             if (l.total > kSmemMost) continue;
             const double waves = static_cast<double>((slabs * clusters * cl + sms - 1) / sms);
-            const double joins = cl > 1 ? 1.5 * ((rounds + batch - 1) / batch) : 0.0;
-            const double cost = waves * (rounds * (S + 0.4) + joins);
+            const int pieces = (slab * per_rank * 16 + kThreads - 1) / kThreads, results = static_cast<int>((rounds * J * slab * kRowsTile / cl + kThreads - 1) / kThreads);
+            const double cost = waves * (rounds * (S * kWarps * 56 + 200 + slab * J * g) + pieces * 250 + (cl > 1 ? 1500 + results * 200 : 0));
             if (cost < best) {
                 best = cost;
                 p.cl = cl;
                 p.g = g;
+                p.cl_log2 = c;
+                p.j = J;
+                p.rounds = static_cast<int>(rounds);
                 p.per_rank = per_rank;
-                p.batch = static_cast<int>(batch);
                 grid = clusters * cl;
                 smem = l.total;
             }
         }
     }
     if (grid == 0) return cudaErrorNotSupported;
+    p.piece_inverse = inverse_of(16 * p.per_rank);
+    p.tile_inverse = inverse_of(slab * kRowsTile);
+    p.g_inverse = inverse_of(p.g);
+    p.j_inverse = inverse_of(p.j);
     if (slabs > 65535) return cudaErrorInvalidConfiguration;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -482,19 +502,13 @@ cudaError_t launch_form(const LinearArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// 8, 16 or 32 tokens a slab; fewer than there are where the activations of more
-// do not fit a cluster's shared memory (32: k beyond 19 thousand or so).
-template <bool kBf16>
-static cudaError_t launch_act(const LinearArgs& a, cudaStream_t st) {
-    cudaError_t e = cudaErrorNotSupported;
-    if (a.m > 16) e = launch_form<4, kBf16>(a, st);
-    if (e == cudaErrorNotSupported && a.m > 8) e = launch_form<2, kBf16>(a, st);
-    if (e == cudaErrorNotSupported) e = launch_form<1, kBf16>(a, st);
-    return e;
-}
-
+// Fewer than 8 tokens a CTA where the activations of so many, or a cluster's sums of
+// them, do not fit shared memory (8: k beyond 50 thousand or so; 1 fits always).
 cudaError_t launch_fp4_few(const LinearArgs& a, cudaStream_t st) {
-    return a.act == FP8W_BF16 ? launch_act<true>(a, st) : launch_act<false>(a, st);
+    cudaError_t e = cudaErrorNotSupported;
+    for (int most = kTokens; e == cudaErrorNotSupported && most >= 1; most /= 2)
+        e = a.act == FP8W_BF16 ? launch_slab<true>(a, most, st) : launch_slab<false>(a, most, st);
+    return e;
 }
 
 }  // namespace fp8w

@@ -33,8 +33,9 @@ cudaError_t launch_quantize_fp4(const void* w, int w_dtype, int64_t n, int64_t k
 cudaError_t launch_dequantize_fp4(const uint8_t* codes, const uint8_t* blocks, const float* scales, int64_t n, int64_t k,
                                   int out_dtype, void* w, cudaStream_t st);
 
-// K9: the linear layer on 4-bit weights for few tokens (any m: 32 a slab).
+// K9: the linear layer on 4-bit weights for few tokens (m <= fp4_few_most).
 // LinearArgs with blocks; group 0.
+constexpr int fp4_few_most = 8;
 cudaError_t launch_fp4_few(const LinearArgs& a, cudaStream_t st);
 
 // K1: codes/scales from fp32 weights.

@@ -49,6 +49,7 @@ constexpr uint32_t kPCodeBytes = kPM * kPCodeK;   // 16 KB
 constexpr uint32_t kPABytes = kPM * kPK * 2;      // 16 KB
 constexpr int kPThreads = 512;
 constexpr int kPThreadsGrouped = 640;             // + the second epilogue warpgroup
+constexpr int kPThreadsFp4 = 768;                 // + two dequantising warpgroups
 constexpr int kPMmaWarp = 1, kPXWarp = 2, kPFirstEpiWarp = 4, kPFirstDqWarp = 8, kPSecondEpiWarp = 16;
 constexpr int kPGAcc = 4;                         // per-group form: group accumulators (128 columns each)
 constexpr int kPBarTmem = 1;                      // named barrier: MMA warp + epilogue warps
@@ -107,7 +108,7 @@ __device__ __forceinline__ void prefill_error(int code, volatile int* abort_flag
 //                weight, exactly; scales[n] in the epilogue.  A code stage is
 //                256 codes of a row, four k-blocks (k % 32 == 0).
 template <int BN, bool kBf16, int kMode>
-__global__ void __launch_bounds__(kMode == kModeGrouped ? kPThreadsGrouped : kPThreads, 1)
+__global__ void __launch_bounds__(kMode == kModeGrouped ? kPThreadsGrouped : kMode == kModeFp4 ? kPThreadsFp4 : kPThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_constant__ CUtensorMap map_x,
                    const float* __restrict__ scales, const uint8_t* __restrict__ e8, const float* __restrict__ bias,
                    uint16_t* __restrict__ y, int64_t m, int64_t n, int64_t k, int early, int gsz) {
@@ -149,7 +150,7 @@ __global__ void __launch_bounds__(kMode == kModeGrouped ? kPThreadsGrouped : kPT
         if (lane == 0) {
             for (int s = 0; s < kPCS; ++s) {
                 mbar_init(cfull(s), 1);
-                mbar_init(cempty(s), 8);  // the eight dequantising warps
+                mbar_init(cempty(s), kFp4 ? 16 : 8);  // the dequantising warps
             }
             for (int s = 0; s < kPAS; ++s) {
                 mbar_init(afull(s), 4);   // the four warps of one warpgroup
@@ -453,29 +454,25 @@ __global__ void __launch_bounds__(kMode == kModeGrouped ? kPThreadsGrouped : kPT
             __syncwarp();
             if (lane == 0) mbar_arrive(dempty(d));
         }
-    } else if (kFp4 && warp >= kPFirstDqWarp && warp < kPFirstDqWarp + 8) {
+    } else if (kFp4 && warp >= kPFirstDqWarp) {
         // ----------------------------------------- dequantising, 4 bits --
-        // A stage's k-blocks h and h + 2 (two 16-byte chunks of a row each) are this
-        // warpgroup's, and their four blocks' scales (two 16-bit loads each) are
-        // read a stage ahead.
+        // Four warpgroups, for the four k-blocks of a code stage: two 16-byte chunks
+        // of a row each.  Their four blocks' scales (two 16-bit loads) are read a
+        // stage ahead.
         const int h = (warp - kPFirstDqWarp) >> 2;
         const int r = (warp & 3) * 32 + lane;
         const uint32_t swz = static_cast<uint32_t>(r & 7);
         if (!early) pdl_wait();  // the blocks' scales may come from the previous kernel
-        uint32_t next[2] = {0u, 0u};
+        uint32_t next = 0u;
         int64_t b_t = blockIdx.x;
         int b_cs = 0;
         auto ask = [&] {  // the scales of stage (b_t, b_cs), and on to the one after it
-            next[0] = next[1] = 0u;
-            const int64_t wrow = (b_t / token_tiles) * kPM + r;
-            if (b_t < tiles && wrow < n) {
-                const uint8_t* row = e8 + wrow * (k >> 4);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int64_t k0 = (static_cast<int64_t>(b_cs) * 4 + 2 * i + h) * kPK;
-                    if (k0 < k) next[i] = *reinterpret_cast<const uint16_t*>(row + (k0 >> 4));
-                    if (k0 + 32 < k) next[i] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(row + (k0 >> 4) + 2)) << 16;
-                }
+            next = 0u;
+            const int64_t wrow = (b_t / token_tiles) * kPM + r, k0 = (static_cast<int64_t>(b_cs) * 4 + h) * kPK;
+            if (b_t < tiles && wrow < n && k0 < k) {
+                const uint8_t* at = e8 + wrow * (k >> 4) + (k0 >> 4);
+                next = *reinterpret_cast<const uint16_t*>(at);
+                if (k0 + 32 < k) next |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(at + 2)) << 16;
             }
             if (++b_cs == ncs) {
                 b_cs = 0;
@@ -486,52 +483,47 @@ __global__ void __launch_bounds__(kMode == kModeGrouped ? kPThreadsGrouped : kPT
         int64_t cs_n = 0, kb_base = 0;
         bool ok = true;
         for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x, kb_base += nkb) {
-            for (int cs = 0; cs < ncs && ok; ++cs, ++cs_n) {
+            for (int cs = 0; cs < ncs; ++cs, ++cs_n) {
                 const int s = static_cast<int>(cs_n % kPCS);
-                const uint32_t scale4[2] = {next[0], next[1]};
+                const uint32_t scale4 = next;
                 ask();
                 if (!mbar_wait_warp(cfull(s), static_cast<uint32_t>((cs_n / kPCS) & 1), abort_flag)) {
                     if (lane == 0) prefill_error(kErrWaitTma, abort_flag);
                     ok = false;
                     break;
                 }
-                uint4 cw[4];  // chunks of k-block h, then h + 2
+                const int j = 4 * cs + h;
                 const uint32_t row = sbase + L::kCodesOff + s * kPCodeBytes + static_cast<uint32_t>(r) * 128u;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) cw[q] = lds128(row + (((2u * h + (q & 1) + 4u * (q >> 1)) ^ swz) << 4));
-                __syncwarp();
-                if (lane == 0) mbar_arrive(cempty(s));
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int j = 4 * cs + 2 * i + h;
-                    if (j >= nkb) break;
-                    const int64_t kb = kb_base + j;
-                    const int as = static_cast<int>(kb % kPAS);
-                    if (!mbar_wait_warp(aempty(as), static_cast<uint32_t>((kb / kPAS) & 1) ^ 1u, abort_flag)) {
-                        if (lane == 0) prefill_error(kErrWaitMma, abort_flag);
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t arow = sbase + L::kAOff + as * kPABytes + static_cast<uint32_t>(r) * 128u;
-                    uint32_t f[2];  // factors of blocks 0, 1 and 2, 3
-                    if constexpr (kBf16) {
-                        block_quad_bf16(scale4[i], f[0], f[1]);
-                    } else {
-                        f[0] = block_pair_f16(scale4[i]);
-                        f[1] = block_pair_f16(scale4[i] >> 16);
-                    }
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {  // words of 8 codes: 16-byte chunk q of the A row
-                        const uint4 c = cw[2 * i + (q >> 2)];
-                        const uint32_t w = (q & 3) == 0 ? c.x : (q & 3) == 1 ? c.y : (q & 3) == 2 ? c.z : c.w;
-                        const uint32_t pair = f[q >> 2];
-                        uint32_t v[4];
-                        fp4_operands<kBf16>(w, (q & 2) ? both_hi(pair) : both_lo(pair), v);
-                        sts128(arow + ((static_cast<uint32_t>(q) ^ swz) << 4), v[0], v[1], v[2], v[3]);
-                    }
-                    fence_proxy_async_smem();
+                const uint4 c0 = lds128(row + (((2u * h) ^ swz) << 4)), c1 = lds128(row + (((2u * h + 1u) ^ swz) << 4));
+                if (j >= nkb) {
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(afull(as));
+                    if (lane == 0) mbar_arrive(cempty(s));
+                    continue;
+                }
+                const uint32_t w8[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+                const uint32_t f[2] = {block_pair_f16(scale4), block_pair_f16(scale4 >> 16)};  // blocks 0, 1 | 2, 3
+                uint32_t v[8][4];  // 16-byte chunks of the A row
+#pragma unroll
+                for (int q = 0; q < 8; ++q) fp4_operands<kBf16>(w8[q], (q & 2) ? both_hi(f[q >> 2]) : both_lo(f[q >> 2]), v[q]);
+                const int64_t kb = kb_base + j;
+                const int as = static_cast<int>(kb % kPAS);
+                if (!mbar_wait_warp(aempty(as), static_cast<uint32_t>((kb / kPAS) & 1) ^ 1u, abort_flag)) {
+                    if (lane == 0) prefill_error(kErrWaitMma, abort_flag);
+                    ok = false;
+                    break;
+                }
+                const uint32_t arow = sbase + L::kAOff + as * kPABytes + static_cast<uint32_t>(r) * 128u;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) sts128(arow + ((static_cast<uint32_t>(q) ^ swz) << 4), v[q][0], v[q][1], v[q][2], v[q][3]);
+                fence_proxy_async_smem();
+                __syncwarp();
+                // The codes' slot goes back here and no sooner: behind these stores,
+                // which hold what was read from it, the reads are done for sure.  (An
+                // arrival right behind the loads can overtake them where shared memory
+                // is busy: with it a slot was filled again before all had read it.)
+                if (lane == 0) {
+                    mbar_arrive(afull(as));
+                    mbar_arrive(cempty(s));
                 }
             }
         }
@@ -580,9 +572,11 @@ __global__ void __launch_bounds__(kMode == kModeGrouped ? kPThreadsGrouped : kPT
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     cw[q] = mine ? lds128(row + (((4u * h + q) ^ swz) << 4)) : make_uint4(0u, 0u, 0u, 0u);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(cempty(s));
-                if (!mine) continue;
+                if (!mine) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(cempty(s));
+                    continue;
+                }
                 const int64_t kb = kb_base + j;
                 const int as = static_cast<int>(kb % kPAS);
                 if (!mbar_wait_warp(aempty(as), static_cast<uint32_t>((kb / kPAS) & 1) ^ 1u, abort_flag)) {
@@ -631,7 +625,10 @@ __global__ void __launch_bounds__(kMode == kModeGrouped ? kPThreadsGrouped : kPT
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(afull(as));
+                if (lane == 0) {
+                    mbar_arrive(afull(as));
+                    mbar_arrive(cempty(s));  // behind these stores, as above
+                }
             }
         }
     }
@@ -676,7 +673,7 @@ static cudaError_t launch_bn(const LinearArgs& a, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(kGrp ? kPThreadsGrouped : kPThreads);
+    cfg.blockDim = dim3(kGrp ? kPThreadsGrouped : kMode == kModeFp4 ? kPThreadsFp4 : kPThreads);
     cfg.dynamicSmemBytes = L::kAlloc;
     cfg.stream = st;
     cfg.attrs = attr;

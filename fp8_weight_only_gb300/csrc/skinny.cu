@@ -68,7 +68,7 @@
 #include <mutex>
 #include <type_traits>
 
-#include "fp8w_device.cuh"
+#include "fp4.cuh"
 #include "fp8w_internal.h"
 #include "../../include/fp8w.h"
 
@@ -93,14 +93,15 @@ constexpr uint32_t kBarEpilogue = 1, kBarTmem = 2, kBarStart = 3;
 constexpr int kTmemCols = 512;              // one CTA per SM
 constexpr int kAColsPerSlot = kBlockK / 2;  // two 16-bit values per column
 constexpr int kDCol0 = kLanes * kASlots * kAColsPerSlot;  // 384: accumulators after the A slots
-constexpr uint32_t kCodeStageBytes = kTileN * kBlockK;  // 16 KB
 constexpr int kMaxNT = 64;
 
-template <int NT>
+template <int NT, bool kFp4 = false>
 struct SkinnySmem {
+    static constexpr uint32_t kCodeStageBytes = kFp4 ? kTileN * kBlockK / 2 : kTileN * kBlockK;  // 16 KB (4 bits: 8)
     // per warpgroup: freed as soon as read (9 tiles in flight per SM: deeper
-    // rings on every SM make the HBM stream slower, not faster)
-    static constexpr int kCodeSlots = NT <= 32 ? 3 : 2;
+    // rings on every SM make the HBM stream slower, not faster; 4-bit tiles
+    // are half as large)
+    static constexpr int kCodeSlots = kFp4 ? (NT <= 32 ? 5 : 4) : NT <= 32 ? 3 : 2;
     static constexpr int kXSlots = NT == 16 ? 12 : 8;  // activation ring (freed when the unit's MMAs are done)
     // accumulator buffers per MMA warp: two (the epilogue drains one tile
     // while the next accumulates) where TMEM has room, one for 64 tokens
@@ -281,6 +282,10 @@ struct SharedTile {
 //                known the hand-off loops unroll), and where the ring holds
 //                the groups of two units or more the hand-off goes once a
 //                unit rather than once a group.
+//  kModeFp4      4-bit codes with an e4m3 byte per 16 of them (fp4.cuh),
+//                blocks[n, k / 16] passed as e8: they enter the dequantised
+//                weight, exactly; scales[n] in the epilogue.  A unit's codes are
+//                64 bytes of each channel (64-byte swizzle).
 template <int NT, bool kBf16, int kMode = kModeRow, int kGpu = 1>
 __global__ void __launch_bounds__(kThreads, 1)
     skinny_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_constant__ CUtensorMap map_x,
@@ -289,9 +294,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                   int early, int gsz) {
     constexpr bool kMx = kMode == kModeMxFold;
     constexpr bool kGrp = kMode == kModeGrouped;
+    constexpr bool kFp4 = kMode == kModeFp4;
     static_assert(!kMx || kBf16, "MX-style scales fold into bf16 weights only");
     static_assert(!kGrp || NT <= 32, "per-group totals are held in registers: at most 32 tokens");
-    using L = SkinnySmem<NT>;
+    using L = SkinnySmem<NT, kFp4>;
+    constexpr uint32_t kCodeStageBytes = L::kCodeStageBytes;
     constexpr int kCS = L::kCodeSlots, kXS = L::kXSlots;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -439,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 mbar_arrive_expect_tx(cfull(g, s), kCodeStageBytes);
-                tma_load_2d(sbase + code_smem(g, s), &map_codes, cu.kb * kBlockK, cu.tile * kTileN, cfull(g, s),
+                tma_load_2d(sbase + code_smem(g, s), &map_codes, cu.kb * (kFp4 ? kBlockK / 2 : kBlockK), cu.tile * kTileN, cfull(g, s),
                             pol_stream);
                 ++issued;
                 if (++g == kLanes) {
@@ -914,6 +921,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < group; ++i) mcu.next();
             if (group < iters) mx_next = mx_load(mcu.tile, mcu.kb);
         }
+        // 4 bits: the scales of this thread's row's eight blocks of a unit, loaded a
+        // unit ahead in the same way
+        uint2 b_next = make_uint2(0u, 0u);
+        auto blocks_load = [&](int64_t tile, int kb) {
+            const int64_t row = tile * kTileN + (warp & 3) * 32 + lane;
+            uint2 b = make_uint2(0u, 0u);
+            if (row >= n) return b;
+            const uint8_t* at = e8 + row * (k >> 4) + kb * 8;
+            if ((k & 127) == 0) return *reinterpret_cast<const uint2*>(at);
+            uint32_t two[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                two[i] = kb * kBlockK + 32 * i < k ? *reinterpret_cast<const uint16_t*>(at + 2 * i) : 0u;
+            b.x = two[0] | (two[1] << 16), b.y = two[2] | (two[3] << 16);
+            return b;
+        };
+        if constexpr (kFp4) {
+            if (!early) pdl_wait();
+            for (int i = 0; i < group; ++i) mcu.next();
+            if (group < iters) b_next = blocks_load(mcu.tile, mcu.kb);
+        }
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;
         const uint32_t a_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -930,12 +958,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < kLanes; ++i) mcu.next();
                 if (it + kLanes < iters) mx_next = mx_load(mcu.tile, mcu.kb);
             }
-            const uint32_t row = sbase + code_smem(group, s) + r * 128;
-            uint4 cw[8];
+            uint2 blocks = make_uint2(0u, 0u);
+            if constexpr (kFp4) {
+                blocks = b_next;
+                for (int i = 0; i < kLanes; ++i) mcu.next();
+                if (it + kLanes < iters) b_next = blocks_load(mcu.tile, mcu.kb);
+            }
+            const uint32_t row = sbase + code_smem(group, s) + r * (kFp4 ? 64 : 128);
+            uint4 cw[kFp4 ? 4 : 8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) cw[q] = lds128(row + ((q ^ (r & 7)) << 4));
-            __syncwarp();
-            if (lane == 0) mbar_arrive(cempty(group, s));
+            for (int q = 0; q < (kFp4 ? 4 : 8); ++q) cw[q] = lds128(row + ((kFp4 ? q ^ ((r >> 1) & 3) : q ^ (r & 7)) << 4));
+            const uint32_t taken = cempty(group, s);
             if (++s == kCS) {
                 s = 0;
                 ph ^= 1u;
@@ -965,9 +998,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             };
+            // 4 bits: block q of the unit, words 2 (q % 2) and 2 (q % 2) + 1 of chunk q / 2
+            uint32_t factor[4] = {0u, 0u, 0u, 0u};  // of blocks 0, 1 | 2, 3 | 4, 5 | 6, 7
+            if constexpr (kFp4) {
+                factor[0] = block_pair_f16(blocks.x), factor[1] = block_pair_f16(blocks.x >> 16);
+                factor[2] = block_pair_f16(blocks.y), factor[3] = block_pair_f16(blocks.y >> 16);
+            }
+            auto fp4_block16 = [&](int q, uint32_t (&v)[8]) {
+                const uint4 c = cw[q >> 1];
+                const uint32_t f = (q & 1) ? both_hi(factor[q >> 1]) : both_lo(factor[q >> 1]);
+                fp4_operands<kBf16>((q & 1) ? c.z : c.x, f, v);
+                fp4_operands<kBf16>((q & 1) ? c.w : c.y, f, v + 4);
+            };
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                if constexpr (kMx) {
+                if constexpr (kFp4) {
+                    fp4_block16(q, v0[q]);
+                } else if constexpr (kMx) {
                     dequant16_mx(cw[q], v0[q], mul[q >> 1]);
                     mx_fix(v0[q], q);
                 } else {
@@ -988,7 +1035,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int q = 4; q < 8; ++q) {
                 uint32_t v[8];
-                if constexpr (kMx) {
+                if constexpr (kFp4) {
+                    fp4_block16(q, v);
+                } else if constexpr (kMx) {
                     dequant16_mx(cw[q], v, mul[q >> 1]);
                     mx_fix(v, q);
                 } else {
@@ -999,7 +1048,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(aready(r));
+            if (lane == 0) {
+                mbar_arrive(aready(r));
+                // behind the stores of what was read from the slot: the reads are done
+                // (an arrival right behind the loads can overtake them)
+                mbar_arrive(taken);
+            }
         }
     }
 
@@ -1099,6 +1153,20 @@ bool encode_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint6
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The codes of 4-bit weights: `inner` bytes x `outer` rows, boxes of 64 bytes x
+// box_outer rows, 64-byte swizzle.
+static bool encode_2d_64(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint32_t box_outer) {
+    EncodeTiledFn fn = get_encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {inner, outer};
+    const cuuint64_t strides[1] = {inner};
+    const cuuint32_t box[2] = {64, box_outer};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_3d_blocks(CUtensorMap* map, const void* base, uint64_t rows, uint64_t k, uint32_t box_rows,
                       uint32_t box_blocks) {
     EncodeTiledFn fn = get_encode_fn();
@@ -1182,7 +1250,7 @@ bool skinny_shape_valid(const SkinnyShape& sh, int64_t m, int64_t k, bool groupe
 
 template <int NT, bool kBf16, int kMode = kModeRow, int kGpu = 1>
 static cudaError_t launch_nt(const LinearArgs& a, const SkinnyShape* forced, cudaStream_t st) {
-    using L = SkinnySmem<NT>;
+    using L = SkinnySmem<NT, kMode == kModeFp4>;
     constexpr bool kMx = kMode == kModeMxFold;
     constexpr bool kGrp = kMode == kModeGrouped;
     auto kern = skinny_kernel<NT, kBf16, kMode, kGpu>;
@@ -1226,8 +1294,9 @@ static cudaError_t launch_nt(const LinearArgs& a, const SkinnyShape* forced, cud
     if (attr_err != cudaSuccess) return attr_err;
 
     CUtensorMap map_codes, map_x;
-    if (!encode_2d(&map_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.codes, static_cast<uint64_t>(a.k),
-                   static_cast<uint64_t>(a.n), static_cast<uint64_t>(a.k), kBlockK, kTileN))
+    if (kMode == kModeFp4 ? !encode_2d_64(&map_codes, a.codes, static_cast<uint64_t>(a.k / 2), static_cast<uint64_t>(a.n), kTileN)
+                          : !encode_2d(&map_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.codes, static_cast<uint64_t>(a.k),
+                                       static_cast<uint64_t>(a.n), static_cast<uint64_t>(a.k), kBlockK, kTileN))
         return cudaErrorInvalidValue;
     if (!encode_2d(&map_x, CU_TENSOR_MAP_DATA_TYPE_UINT16, a.x, static_cast<uint64_t>(a.k),
                    static_cast<uint64_t>(a.m), static_cast<uint64_t>(a.k) * 2, 64, NT))
@@ -1260,7 +1329,7 @@ static cudaError_t launch_nt(const LinearArgs& a, const SkinnyShape* forced, cud
         const int rows = static_cast<int>(a.m - m0 < NT ? a.m - m0 : NT);
         const bool bytes = kMx || (kGrp && a.e8m0);
         const float* sc = bytes ? nullptr : a.scales;
-        const uint8_t* e8 = bytes ? reinterpret_cast<const uint8_t*>(a.scales) : nullptr;
+        const uint8_t* e8 = kMode == kModeFp4 ? a.blocks : bytes ? reinterpret_cast<const uint8_t*>(a.scales) : nullptr;
         e = cudaLaunchKernelEx(&cfg, kern, map_codes, map_x, sc, e8, a.bias, yp + m0 * a.n, rows,
                                static_cast<int>(m0), a.n, a.k, shape.cl, static_cast<int>(shape.tpc),
                                a.early ? 1 : 0, kGrp ? static_cast<int>(a.group) : 0);
@@ -1275,6 +1344,12 @@ cudaError_t launch_skinny(const LinearArgs& a, const SkinnyShape* forced, cudaSt
     // per-group form, 16 or 32 tokens a launch (32-row slabs beyond)
     const bool grouped = a.group != 0 && (!a.e8m0 || !bf16);
     if (forced && !skinny_shape_valid(*forced, a.m, a.k, grouped)) return cudaErrorInvalidConfiguration;
+    if (a.blocks) {
+        if (a.k % 32 != 0) return cudaErrorInvalidValue;
+        if (a.m <= 16) return bf16 ? launch_nt<16, true, kModeFp4>(a, forced, st) : launch_nt<16, false, kModeFp4>(a, forced, st);
+        if (a.m <= 32) return bf16 ? launch_nt<32, true, kModeFp4>(a, forced, st) : launch_nt<32, false, kModeFp4>(a, forced, st);
+        return bf16 ? launch_nt<64, true, kModeFp4>(a, forced, st) : launch_nt<64, false, kModeFp4>(a, forced, st);
+    }
     if (grouped) {
         if (a.k % a.group != 0 || (a.group != 32 && a.group != 64 && a.group != 128) || (a.e8m0 && a.group != 32))
             return cudaErrorInvalidValue;
