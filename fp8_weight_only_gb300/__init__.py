@@ -332,53 +332,6 @@ def linear_w8a8(x_codes, x_scales, codes, scales, bias=None, out=None, out_dtype
     return out
 
 
-def quantize_fp4(w, codes=None, blocks=None, scales=None):
-    """W[N, K] (CUDA, contiguous; float32, bfloat16 or float16; K % 32 == 0) -> the
-    4-bit form (codes uint8 [N, K / 2], blocks uint8 [N, K / 16], scales fp32 [N]):
-    two e2m1 codes a byte (the first in the low half), an e4m3 scale per 16 of a
-    row and one fp32 a row."""
-    import torch
-    kind = {torch.float32: FP8W_F32, torch.bfloat16: FP8W_BF16, torch.float16: FP8W_F16}.get(w.dtype)
-    if kind is None or not w.is_cuda or w.dim() != 2 or not w.is_contiguous():
-        raise TypeError("w must be a contiguous 2-D float32, bfloat16 or float16 CUDA tensor")
-    n, k = w.shape
-    got = []
-    for name, t, dt, shape in (("codes", codes, torch.uint8, (n, k // 2)), ("blocks", blocks, torch.uint8, (n, k // 16)),
-                               ("scales", scales, torch.float32, (n,))):
-        if t is None:
-            t = torch.empty(shape, dtype=dt, device=w.device)
-        elif t.dtype != dt or t.device != w.device or not t.is_contiguous() or t.shape != shape:
-            raise TypeError("%s must be a contiguous %s %s tensor on w's device" % (name, dt, list(shape)))
-        got.append(t)
-    _check(lib().fp8w_quantize_fp4(_ptr(w), kind, n, k, _ptr(got[0]), _ptr(got[1]), _ptr(got[2]), _stream(w)))
-    return tuple(got)
-
-
-def dequantize_fp4(codes, blocks, scales, dtype=None, out=None):
-    """The values of the 4-bit form, each product rounded once to `dtype`
-    (torch.float32, bfloat16 or float16; default bfloat16): codes uint8 [.., K / 2],
-    blocks uint8 [.., K / 16], scales fp32 [..] -> [.., K].  The rows may be a
-    weight's, or a cache's slots ([pages, kv_heads, page_size], contiguous)."""
-    import torch
-    if dtype is None:
-        dtype = out.dtype if out is not None else torch.bfloat16
-    kind = {torch.float32: FP8W_F32, torch.bfloat16: FP8W_BF16, torch.float16: FP8W_F16}.get(dtype)
-    if kind is None:
-        raise TypeError("dequantize_fp4: dtype must be float32, bfloat16 or float16, got %s" % dtype)
-    for name, t, dt in (("codes", codes, torch.uint8), ("blocks", blocks, torch.uint8), ("scales", scales, torch.float32)):
-        if t.dtype != dt or not t.is_cuda or t.device != codes.device or not t.is_contiguous():
-            raise TypeError("%s must be a contiguous %s CUDA tensor on the operands' device" % (name, dt))
-    rows, k = tuple(codes.shape[:-1]), 2 * codes.shape[-1] if codes.dim() else 0
-    if scales.shape != rows or blocks.shape != rows + (k // 16,):
-        raise ValueError("shape mismatch: codes %s, blocks %s, scales %s" % (tuple(codes.shape), tuple(blocks.shape), tuple(scales.shape)))
-    if out is None:
-        out = torch.empty(rows + (k,), dtype=dtype, device=codes.device)
-    elif out.shape != rows + (k,) or out.dtype != dtype or out.device != codes.device or not out.is_contiguous():
-        raise ValueError("out must be a contiguous [.., K] tensor of the requested dtype")
-    _check(lib().fp8w_dequantize_fp4(_ptr(codes), _ptr(blocks), _ptr(scales), scales.numel(), k, kind, _ptr(out), _stream(codes)))
-    return out
-
-
 class Rope:
     """Rotary positions for rope and rope_append: table fp32 [max_pos, rot_dim]
     (CUDA, contiguous), each row the cosines of rot_dim / 2 angles and then
@@ -449,13 +402,14 @@ class KVCache:
 # out what was wrong.
 
 _torch = _stream_of = _empty_like = _dense = _int32 = _int64 = _empty = _uint8 = _float32 = None
-_ACT = {}
+_ACT, _FLOAT = {}, {}
 
 
 def _load_torch():
     global _torch, _stream_of, _empty_like, _dense, _int32, _int64, _empty, _uint8, _float32
     import torch
     _ACT.update({torch.bfloat16: FP8W_BF16, torch.float16: FP8W_F16})
+    _FLOAT.update({torch.float32: FP8W_F32, **_ACT})
     # the stream's handle without a Stream object around it, where torch has it
     _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -501,6 +455,71 @@ def _index(name, t, dtype, shape, index):
     return t.data_ptr()
 
 
+def _given(name, t, dtype, shape, index):
+    """An output that the caller brought."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise TypeError("%s must be a contiguous %s %s tensor on w's device" % (name, dtype, list(shape)))
+
+
+def quantize_fp4(w, codes=None, blocks=None, scales=None):
+    """W[N, K] (CUDA, contiguous; float32, bfloat16 or float16; K % 32 == 0) -> the
+    4-bit form (codes uint8 [N, K / 2], blocks uint8 [N, K / 16], scales fp32 [N]):
+    two e2m1 codes a byte (the first in the low half), an e4m3 scale per 16 of a
+    row and one fp32 a row."""
+    if _torch is None:
+        _load_torch()
+    dev, shape = w.get_device(), w.shape
+    kind = _FLOAT.get(w.dtype)
+    if kind is None or dev < 0 or len(shape) != 2 or not w.is_contiguous():
+        raise TypeError("w must be a contiguous 2-D float32, bfloat16 or float16 CUDA tensor")
+    n, k = shape
+    if codes is None:
+        codes = _empty((n, k >> 1), dtype=_uint8, device=dev)
+    else:
+        _given("codes", codes, _uint8, (n, k >> 1), dev)
+    if blocks is None:
+        blocks = _empty((n, k >> 4), dtype=_uint8, device=dev)
+    else:
+        _given("blocks", blocks, _uint8, (n, k >> 4), dev)
+    if scales is None:
+        scales = _empty((n,), dtype=_float32, device=dev)
+    else:
+        _given("scales", scales, _float32, (n,), dev)
+    st = _lib.fp8w_quantize_fp4(w.data_ptr(), kind, n, k, codes.data_ptr(), blocks.data_ptr(), scales.data_ptr(), _stream_of(dev))
+    if st:
+        _check(st)
+    return codes, blocks, scales
+
+
+def dequantize_fp4(codes, blocks, scales, dtype=None, out=None):
+    """The values of the 4-bit form, each product rounded once to `dtype`
+    (torch.float32, bfloat16 or float16; default bfloat16): codes uint8 [.., K / 2],
+    blocks uint8 [.., K / 16], scales fp32 [..] -> [.., K].  The rows may be a
+    weight's, or a cache's slots ([pages, kv_heads, page_size], contiguous)."""
+    if _torch is None:
+        _load_torch()
+    if dtype is None:
+        dtype = out.dtype if out is not None else _torch.bfloat16
+    kind = _FLOAT.get(dtype)
+    if kind is None:
+        raise TypeError("dequantize_fp4: dtype must be float32, bfloat16 or float16, got %s" % dtype)
+    dev, shape = codes.get_device(), tuple(codes.shape)
+    if dev < 0 or not shape:
+        raise TypeError("codes must be a CUDA tensor of one dimension at least")
+    rows, k = shape[:-1], 2 * shape[-1]
+    cp = _index("codes", codes, _uint8, shape, dev)
+    bp = _index("blocks", blocks, _uint8, rows + (k >> 4,), dev)
+    sp = _index("scales", scales, _float32, rows, dev)
+    if out is None:
+        out = _empty(rows + (k,), dtype=dtype, device=dev)
+    elif out.shape != rows + (k,) or out.dtype is not dtype or out.get_device() != dev or not out.is_contiguous():
+        raise ValueError("out must be a contiguous [.., K] tensor of the requested dtype")
+    st = _lib.fp8w_dequantize_fp4(cp, bp, sp, scales.numel(), k, kind, out.data_ptr(), _stream_of(dev))
+    if st:
+        _check(st)
+    return out
+
+
 def linear_fp4(x, codes, blocks, scales, bias=None, out=None, weights_ready=False):
     """y[M, N] = round(scales[n] * sum_k x[m, k] * e4m3(blocks[n, k / 16]) * e2m1(codes[n, k]) + bias[n]):
     x [M, K] bf16/fp16 on weights in the 4-bit form (quantize_fp4).  weights_ready as in linear."""
@@ -517,7 +536,7 @@ def linear_fp4(x, codes, blocks, scales, bias=None, out=None, weights_ready=Fals
     sp = _index("scales", scales, _float32, (n,), dev)
     ap = None if bias is None else _index("bias", bias, _float32, (n,), dev)
     if out is None:
-        out = _empty((m, n), dtype=dtype, device=x.device)
+        out = _empty((m, n), dtype=dtype, device=dev)
     elif out.shape != (m, n) or out.dtype is not dtype or out.get_device() != dev or not out.is_contiguous():
         raise ValueError("out must be a contiguous [M, N] tensor of x's dtype")
     st = _lib.fp8w_linear_fp4(x.data_ptr(), act, m, k, cp, bp, sp, ap, n, out.data_ptr(), FLAG_WEIGHTS_READY if weights_ready else 0,

@@ -241,7 +241,57 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
             e[i] = st < steps && key < end && key + 16 > first ? table[key >> p.log_page] : -1;
         }
     };
+    // 4 bits: this thread's places in the scales and the blocks' scales of page 0, slot 0
+    const bool k_here = t * kKeyBytes < row_bytes, v_here = g * (DP / 8) < p.head_dim;
+    const int64_t head_slot = static_cast<int64_t>(head) * p.page_size;
+    const float* const ks_thread = kFp4 ? p.k_scales + head_slot + g : nullptr;
+    const float* const vs_thread = kFp4 ? p.v_scales + head_slot + g : nullptr;
+    const uint8_t* const kb_thread = kFp4 ? p.k_blocks + (head_slot + g) * row_blocks + t * (DP / 64) : nullptr;
+    const uint8_t* const vb_thread = kFp4 ? p.v_blocks + (head_slot + 2 * t) * row_blocks + g * (DP / 8) / 16 : nullptr;
+    const uint32_t page_slots = static_cast<uint32_t>(p.kv_heads) * static_cast<uint32_t>(p.page_size);
     auto load = [&](int st, const int (&e)[kSubs], H& x) {
+        if constexpr (kFp4) {
+            // Whole steps of keys that are all wanted, the most of a long cache, without
+            // a test a load: instructions bound this form (a decode batch: 128 us, 167
+            // without this).
+            bool whole = st < steps && st * kStepKeys >= first && (st + 1) * kStepKeys <= end;
+#pragma unroll
+            for (int i = 0; i < kSubs; ++i) whole = whole && static_cast<uint32_t>(e[i]) < static_cast<uint32_t>(p.num_pages);
+            if (whole) {
+#pragma unroll
+                for (int i = 0; i < kSubs; ++i) {
+                    const int slot = (st * kStepKeys + 16 * i) & (p.page_size - 1);
+                    const int64_t at = e[i] * page_bytes + slot * token_bytes;
+                    const uint64_t sc = static_cast<uint64_t>(static_cast<uint32_t>(e[i])) * page_slots + static_cast<uint32_t>(slot);
+                    const uint8_t *kr = kthread + at, *vr = vthread + at, *kb = kb_thread + sc * row_blocks, *vb = vb_thread + sc * row_blocks;
+                    const float *ks = ks_thread + sc, *vs = vs_thread + sc;
+                    if (k_here) {
+                        x.k[i][0][0] = load_codes(kr, std::integral_constant<int, kKeyBytes>{});
+                        x.k[i][1][0] = load_codes(kr + 8 * token_bytes, std::integral_constant<int, kKeyBytes>{});
+                        if constexpr (DP == 128) {
+                            x.kb[i][0] = *reinterpret_cast<const uint16_t*>(kb);
+                            x.kb[i][1] = *reinterpret_cast<const uint16_t*>(kb + 8 * row_blocks);
+                        } else {
+                            x.kb[i][0] = *kb;
+                            x.kb[i][1] = kb[8 * row_blocks];
+                        }
+                    }
+                    x.ks[i][0] = ks[0];
+                    x.ks[i][1] = ks[8];
+                    x.vs[i][0] = vs[0];
+                    x.vs[i][1] = vs[8];
+                    if (v_here) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int r = (j >> 1) * 8 + (j & 1);
+                            x.v[i][j][0] = load_codes(vr + r * token_bytes, std::integral_constant<int, kValueBytes>{});
+                            x.vb[i][j] = vb[r * row_blocks];
+                        }
+                    }
+                }
+                return;
+            }
+        }
         // Slots at or past `end` may hold anything and are not read: zeros instead, or
         // (kKeeps) what an earlier step left in the registers, finite values whose
         // weights are 0.

@@ -143,69 +143,84 @@ cudaError_t quantize_type(const void* w, int64_t n, int64_t k, uint8_t* codes, u
 }
 
 // ------------------------------------------------------------ dequantise --
-// The exact product of scale and e4m3 * e2m1 (fp32, 6 significant bits), rounded
-// once: 16-bit results as in quantize.cu by hi = fp32(c * s) and its remainder.
-// A thread makes 16 bytes a store, kFp4Unroll of them in flight; a word of codes
-// lies in one block and one row.  Bytes a value: 9 / 16 read, 2 or 4 written.
+// The exact product of scale and e4m3 * e2m1 (6 significant bits, exact in fp16),
+// rounded once.  16 bits: the fp32 product is taken towards zero with its last bit
+// set where that dropped anything, so that the second rounding sees on which side of
+// a middle the product lies (three instructions, and half of one for the pair).
+// A thread takes a block of 16 values at a time, kFp4Unroll of them in flight.
+// Bytes a value: 9 / 16 read, 2 or 4 written.
 constexpr int kFp4Unroll = 4;
 
-template <int OUT>
-__device__ __forceinline__ uint32_t fp4_round(float c, float s) {
-    const float hi = __fmul_rn(c, s);
-    if constexpr (OUT == 0) return __float_as_uint(hi);
-    return OUT == 1 ? exact_to_bf16(hi, c, s) : exact_to_f16(hi, c, s);
+// hi and a sticky last bit: rounds to fewer bits as the exact product does.
+__device__ __forceinline__ float mul_sticky(float c, float s) {
+    const float hi = __fmul_rz(c, s);
+    return fmaf(c, s, -hi) != 0.0f ? __uint_as_float(__float_as_uint(hi) | 1u) : hi;
 }
+
+struct Fp4Walk {        // blocks of 16 values, a grid of threads apart
+    int64_t blocks;     // of all rows
+    int64_t per_row;    // of a row
+    int64_t step_row;   // a grid of threads: rows and blocks of a row
+    int64_t step_col;
+};
 
 // OUT: 0 fp32, 1 bf16, 2 fp16.
 template <int OUT>
 __global__ void __launch_bounds__(kFp4Threads) dequantize_fp4_kernel(const uint8_t* codes, const uint8_t* blocks, const float* scales,
-                                                                      int64_t k, int64_t nchunk, void* out) {
-    constexpr int U = kFp4Unroll, C = OUT == 0 ? 4 : 8;  // values a chunk
-    const int64_t cpr = k / C, P = static_cast<int64_t>(gridDim.x) * kFp4Threads, step = U * P;
-    const int64_t srow = step / cpr, scol = step - srow * cpr;
-    const int64_t i0 = blockIdx.x * static_cast<int64_t>(kFp4Threads) + threadIdx.x;
-    int64_t row[U], col[U];
+                                                                      void* out, const __grid_constant__ Fp4Walk w) {
+    const int64_t P = static_cast<int64_t>(gridDim.x) * kFp4Threads;
+    int64_t i = blockIdx.x * static_cast<int64_t>(kFp4Threads) + threadIdx.x;
+    // (one division, of 32 bits where that is enough)
+    int64_t row = (w.blocks >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(w.per_row)) : i / w.per_row;
+    int64_t col = i - row * w.per_row;
+    while (i < w.blocks) {
+        uint2 cw[kFp4Unroll];
+        uint32_t bl[kFp4Unroll];
+        float sc[kFp4Unroll];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        row[u] = (i0 + u * P) / cpr;
-        col[u] = i0 + u * P - row[u] * cpr;
-    }
-    for (int64_t i = i0; i < nchunk; i += step) {
-        uint32_t cw[U], bl[U];
-        float sc[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
+        for (int u = 0; u < kFp4Unroll; ++u) {
             const int64_t v = i + u * P;
-            if (v >= nchunk) break;
-            cw[u] = C == 8 ? __ldcs(reinterpret_cast<const uint32_t*>(codes) + v) : __ldcs(reinterpret_cast<const uint16_t*>(codes) + v);
-            bl[u] = blocks[v / (16 / C)];
-            sc[u] = scales[row[u]];
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t v = i + u * P;
-            if (v >= nchunk) break;
-            uint32_t p[4], o[8];
-            e2m1x8_to_f16x2(cw[u], p[0], p[1], p[2], p[3]);
-            const uint32_t factor = both_lo(block_pair_f16(bl[u]));
-#pragma unroll
-            for (int e = 0; e < C / 2; ++e) {
-                p[e] = f16x2_mul(p[e], factor);  // exact
-                o[2 * e] = fp4_round<OUT>(f16_lo_to_f32(p[e]), sc[u]);
-                o[2 * e + 1] = fp4_round<OUT>(f16_hi_to_f32(p[e]), sc[u]);
+            if (v < w.blocks) {
+                cw[u] = __ldcs(reinterpret_cast<const uint2*>(codes) + v);
+                bl[u] = blocks[v];
+                sc[u] = scales[row];
             }
-            uint4* dst = static_cast<uint4*>(out) + v;
-            if constexpr (OUT == 0)
-                __stcs(dst, make_uint4(o[0], o[1], o[2], o[3]));
-            else
-                __stcs(dst, make_uint4(o[0] | (o[1] << 16), o[2] | (o[3] << 16), o[4] | (o[5] << 16), o[6] | (o[7] << 16)));
+            row += w.step_row;
+            col += w.step_col;
+            if (col >= w.per_row) col -= w.per_row, ++row;
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            row[u] += srow;
-            col[u] += scol;
-            if (col[u] >= cpr) col[u] -= cpr, ++row[u];
+        for (int u = 0; u < kFp4Unroll; ++u) {
+            const int64_t v = i + u * P;
+            if (v >= w.blocks) break;
+            const uint32_t factor = both_lo(block_pair_f16(bl[u]));
+            constexpr int kWords = OUT == 0 ? 16 : 8;
+            uint32_t o[kWords];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t p[4];
+                e2m1x8_to_f16x2(h ? cw[u].y : cw[u].x, p[0], p[1], p[2], p[3]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    p[e] = f16x2_mul(p[e], factor);  // exact
+                    const float x = f16_lo_to_f32(p[e]), y = f16_hi_to_f32(p[e]);
+                    if constexpr (OUT == 0) {
+                        o[8 * h + 2 * e] = __float_as_uint(__fmul_rn(x, sc[u]));
+                        o[8 * h + 2 * e + 1] = __float_as_uint(__fmul_rn(y, sc[u]));
+                    } else {
+                        const float a = mul_sticky(x, sc[u]), b = mul_sticky(y, sc[u]);
+                        if constexpr (OUT == 1)
+                            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[4 * h + e]) : "f"(b), "f"(a));
+                        else
+                            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[4 * h + e]) : "f"(b), "f"(a));
+                    }
+                }
+            }
+            uint4* dst = static_cast<uint4*>(out) + v * (kWords / 4);
+#pragma unroll
+            for (int q = 0; q < kWords; q += 4) __stcs(dst + q / 4, make_uint4(o[q], o[q + 1], o[q + 2], o[q + 3]));
         }
+        i += kFp4Unroll * P;
     }
 }
 
@@ -219,20 +234,26 @@ cudaError_t launch_quantize_fp4(const void* w, int w_dtype, int64_t n, int64_t k
 }
 
 cudaError_t launch_dequantize_fp4(const uint8_t* codes, const uint8_t* blocks, const float* scales, int64_t n, int64_t k,
-                                  int out_dtype, void* w, cudaStream_t st) {
+                                  int out_dtype, void* w_out, cudaStream_t st) {
     int sms = 0;
     cudaError_t e = device_sm_count(sms);
     if (e != cudaSuccess) return e;
-    const int64_t nchunk = n * (k / (out_dtype == 0 ? 4 : 8));
-    int64_t grid = (nchunk + kFp4Threads * kFp4Unroll - 1) / (kFp4Threads * kFp4Unroll);
+    Fp4Walk w;
+    w.per_row = k / 16;
+    w.blocks = n * w.per_row;
+    int64_t grid = (w.blocks + kFp4Threads * kFp4Unroll - 1) / (kFp4Threads * kFp4Unroll);
+    if (w.blocks <= static_cast<int64_t>(sms) * kFp4Threads * 2) grid = (w.blocks + kFp4Threads - 1) / kFp4Threads;  // few: one each
     if (grid > sms * 8) grid = sms * 8;
+    const int64_t threads = grid * kFp4Threads;
+    w.step_row = threads / w.per_row;
+    w.step_col = threads - w.step_row * w.per_row;
     const unsigned g = static_cast<unsigned>(grid);
     if (out_dtype == 1)
-        dequantize_fp4_kernel<1><<<g, kFp4Threads, 0, st>>>(codes, blocks, scales, k, nchunk, w);
+        dequantize_fp4_kernel<1><<<g, kFp4Threads, 0, st>>>(codes, blocks, scales, w_out, w);
     else if (out_dtype == 2)
-        dequantize_fp4_kernel<2><<<g, kFp4Threads, 0, st>>>(codes, blocks, scales, k, nchunk, w);
+        dequantize_fp4_kernel<2><<<g, kFp4Threads, 0, st>>>(codes, blocks, scales, w_out, w);
     else
-        dequantize_fp4_kernel<0><<<g, kFp4Threads, 0, st>>>(codes, blocks, scales, k, nchunk, w);
+        dequantize_fp4_kernel<0><<<g, kFp4Threads, 0, st>>>(codes, blocks, scales, w_out, w);
     return cudaGetLastError();
 }
 

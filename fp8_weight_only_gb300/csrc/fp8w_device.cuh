@@ -521,50 +521,4 @@ __device__ __forceinline__ uint16_t round_out(float v) {
     }
 }
 
-// bf16 nearest-even of the exact product c * s, hi = fp32(c * s).  The
-// hardware rounds hi; only when hi sits exactly on a bf16 midpoint (its low
-// 16 bits are 0x8000) does the remainder lo = c * s - hi decide.
-__device__ __forceinline__ uint16_t exact_to_bf16(float hi, float c, float s) {
-    const uint32_t t = __float_as_uint(hi);
-    uint16_t r = __bfloat16_as_ushort(__float2bfloat16_rn(hi));
-    if ((t & 0xFFFFu) == 0x8000u) {
-        const float lo = fmaf(c, s, -hi);
-        // on lo's side of the midpoint: away from zero when lo has hi's sign
-        if (lo != 0.0f) r = static_cast<uint16_t>((t >> 16) + (((__float_as_uint(lo) ^ t) >> 31) ^ 1u));
-    }
-    return r;
-}
-
-// fp16 nearest-even of the exact product c * s, hi = fp32(c * s).  The
-// hardware rounds hi; only when hi may sit exactly on a midpoint (its 12 low
-// mantissa bits are zero, a necessary condition in fp16's normal and
-// subnormal ranges) and the remainder lo = c * s - hi is not zero does the
-// exact product need a look.
-__device__ __forceinline__ uint16_t exact_to_f16(float hi, float c, float s) {
-    const uint16_t r = __half_as_ushort(__float2half_rn(hi));
-    const uint32_t t = __float_as_uint(hi);
-    if ((t & 0xFFFu) != 0u || (t & 0x7FFFFFFFu) >= 0x7F800000u) return r;
-    const float lo = fmaf(c, s, -hi);
-    if (lo == 0.0f) return r;
-    const uint16_t sign = static_cast<uint16_t>(r & 0x8000u), rm = static_cast<uint16_t>(r & 0x7FFFu);
-    const float a = fabsf(hi);
-    float back, other;
-    uint16_t om;  // the other candidate's magnitude bits
-    if (rm == 0x7C00u) {  // rounded to inf: the candidates are 65504 and inf, the midpoint 65520
-        back = 65536.0f;
-        om = 0x7BFFu;
-        other = 65504.0f;
-    } else {
-        back = __half2float(__ushort_as_half(rm));
-        if (back == a) return r;  // hi itself is an fp16 value
-        om = static_cast<uint16_t>(a > back ? rm + 1u : rm - 1u);
-        other = om == 0x7C00u ? 65536.0f : __half2float(__ushort_as_half(om));
-    }
-    if (a != 0.5f * (back + other)) return r;  // not a midpoint: hi's rounding is the exact one
-    // on the midpoint: the exact product lies on lo's side (away from zero when lo has hi's sign)
-    const bool away = (lo > 0.0f) == (hi > 0.0f);
-    const uint16_t lower = back < other ? rm : om, upper = back < other ? om : rm;
-    return static_cast<uint16_t>(sign | (away ? upper : lower));
-}
-
 }  // namespace fp8w
