@@ -298,11 +298,21 @@ fp8w_status fp8w_linear_fp4(const void* x, int act_dtype, int64_t m, int64_t k, 
     a.blocks = blocks;
     a.early = (flags & FP8W_FLAG_WEIGHTS_READY) != 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // codes streamed into registers up to 8 tokens (14336 x 4096, 8 tokens: 12.9 us,
-    // 16.7 by the skinny kernel; 16: 17.4 with a wider form of it, 16.8), the skinny
-    // kernel up to 64, the prefill GEMM beyond
+    // Codes streamed into registers up to 8 tokens (14336 x 4096, 8 tokens: 13.0 us, 15.1
+    // by the skinny kernel; 16 with a wider form of it: 17.4), the skinny kernel up to 64.
+    // Beyond, the prefill GEMM, whose CTA takes about half a microsecond for 64 inputs of
+    // its tile, or slabs of 64 by the skinny kernel, about 7 us and one for each of its
+    // CTA's units of 128 x 256: these where few channels leave the GEMM few CTAs (4096 x
+    // 14336, 128 tokens: 38 us against 103; 14336 x 4096: 37 against 35).
     if (m <= fp8w::fp4_few_most) return cuda_status(fp8w::launch_fp4_few(a, s), "fp8w_linear_fp4 launch");
-    if (use_prefill(m)) return cuda_status(fp8w::launch_prefill(a, s), "fp8w_linear_fp4 prefill launch");
+    int sms = 0;
+    const cudaError_t e = fp8w::device_sm_count(sms);
+    if (e != cudaSuccess) return cuda_status(e, "fp8w_linear_fp4 device");
+    const int64_t channel_tiles = (n + 127) / 128, slabs = (m + 63) / 64;
+    const int64_t gemm_tiles = channel_tiles * (m <= 128 ? 1 : (m + 255) / 256);
+    const double gemm_us = 2.0 + static_cast<double>((gemm_tiles + sms - 1) / sms) * static_cast<double>((k + 63) / 64) * 0.5;
+    const double slabs_us = static_cast<double>(slabs) * (7.0 + static_cast<double>(channel_tiles * ((k + 255) / 256)) / sms);
+    if (use_prefill(m) && gemm_us <= slabs_us) return cuda_status(fp8w::launch_prefill(a, s), "fp8w_linear_fp4 prefill launch");
     return cuda_status(fp8w::launch_skinny(a, nullptr, s), "fp8w_linear_fp4 tensor-core launch");
 }
 

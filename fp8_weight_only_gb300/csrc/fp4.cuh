@@ -60,7 +60,8 @@ __device__ __forceinline__ uint32_t both_hi(uint32_t pair) { return __byte_perm(
 // fp16 pair -> bf16 pair (exact where the values have 8 significant bits), by
 // fp32: two instructions of the FMA pipe and one of the ALU's, which the codes'
 // conversion keeps busy.  (Moving the exponent's bits by a shift and two masks, and
-// 2^-112 into the block's factor: 32 tokens on 14336 x 4096 PENDING.)
+// 2^112 into the block's factor: 32 tokens on 14336 x 4096 20.2 us when this took 17.7,
+// a prompt 204 against 195, attention of chunks 887 against 818.)
 __device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t p) {
     uint32_t r;
     asm("{\n\t.reg .b16 a, b;\n\t.reg .f32 x, y;\n\t"

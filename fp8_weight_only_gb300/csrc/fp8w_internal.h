@@ -76,7 +76,7 @@ struct SkinnyShape {
 };
 cudaError_t launch_skinny(const LinearArgs& a, const SkinnyShape* forced, cudaStream_t st);
 // grouped: the per-group form (a CTA shares at most one tile)
-SkinnyShape skinny_shape(int64_t n, int64_t k, const int* active, int nt, bool grouped = false);
+SkinnyShape skinny_shape(int64_t n, int64_t k, const int* active, int nt, bool grouped = false, int unit = 128);  // k a unit
 bool skinny_shape_valid(const SkinnyShape& sh, int64_t m, int64_t k, bool grouped = false);
 cudaError_t device_sm_count(int& sms);
 // 2-D tiled tensor map with 128-byte swizzle: `inner` x `outer` elements,

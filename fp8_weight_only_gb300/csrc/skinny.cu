@@ -77,9 +77,9 @@ namespace fp8w {
 static __device__ int g_skinny_error;
 
 constexpr int kTileN = 128;                 // output channels per tile (MMA M)
-constexpr int kBlockK = 128;                // k per unit
+constexpr int kUnitK = 128;                 // k per unit (4 bits: twice as much)
 constexpr int kLanes = 3;                   // dequantising warpgroups
-constexpr int kASlots = 2;                  // TMEM A slots per warpgroup
+constexpr int kACols = 384;                 // TMEM columns of the A slots
 // warps: 0 code TMA, 1 activation TMA, 2-3 MMA (warp 2 also owns TMEM),
 // 4..7 epilogue, 8..19 the dequantising warpgroups (4 warps each)
 constexpr int kXWarp = 1;
@@ -91,25 +91,29 @@ constexpr int kThreads = 32 * (kFirstDequantWarp + 4 * kLanes);  // 640
 // named barriers: 0 __syncthreads, 1 epilogue, 2 TMEM ready, 3 start-up
 constexpr uint32_t kBarEpilogue = 1, kBarTmem = 2, kBarStart = 3;
 constexpr int kTmemCols = 512;              // one CTA per SM
-constexpr int kAColsPerSlot = kBlockK / 2;  // two 16-bit values per column
-constexpr int kDCol0 = kLanes * kASlots * kAColsPerSlot;  // 384: accumulators after the A slots
+constexpr int kDCol0 = kACols;              // accumulators after the A slots
 constexpr int kMaxNT = 64;
 
 template <int NT, bool kFp4 = false>
 struct SkinnySmem {
-    static constexpr uint32_t kCodeStageBytes = kFp4 ? kTileN * kBlockK / 2 : kTileN * kBlockK;  // 16 KB (4 bits: 8)
+    // A unit's codes are 128 bytes a channel, a line of the copy.  (4 bits with units of
+    // 128 k, 64 bytes a channel: 32 tokens on 14336 x 4096 17.8 us, 16.5 so; fp16 15.7
+    // and 13.7.)
+    static constexpr int kBlockK = kFp4 ? 2 * kUnitK : kUnitK;
+    static constexpr uint32_t kCodeStageBytes = kTileN * 128;                // 16 KB
+    static constexpr int kAColsPerSlot = kBlockK / 2;                        // two 16-bit values per column
+    static constexpr int kASlots = kACols / kLanes / kAColsPerSlot;          // TMEM A slots per warpgroup: 2 (4 bits: 1)
     // per warpgroup: freed as soon as read (9 tiles in flight per SM: deeper
-    // rings on every SM make the HBM stream slower, not faster; 4-bit tiles
-    // are half as large)
-    static constexpr int kCodeSlots = kFp4 ? (NT <= 32 ? 5 : 4) : NT <= 32 ? 3 : 2;
-    static constexpr int kXSlots = NT == 16 ? 12 : 8;  // activation ring (freed when the unit's MMAs are done)
+    // rings on every SM make the HBM stream slower, not faster)
+    static constexpr int kCodeSlots = NT <= 32 ? 3 : 2;
+    static constexpr int kXSlots = (NT == 16 ? 12 : 8) / (kFp4 ? 2 : 1);  // activation ring (freed when the unit's MMAs are done)
     // accumulator buffers per MMA warp: two (the epilogue drains one tile
     // while the next accumulates) where TMEM has room, one for 64 tokens
     static constexpr int kDBuf = NT <= 32 ? 2 : 1;
     static_assert(kDCol0 + kMmaWarps * kDBuf * NT <= kTmemCols, "TMEM columns");
-    static_assert(kXSlots % kMmaWarps == 0 && (kLanes * kASlots) % kMmaWarps == 0, "slots alternate between MMA warps");
+    static_assert(kXSlots % kMmaWarps == 0 && (kFp4 || (kLanes * kASlots) % kMmaWarps == 0), "slots alternate between MMA warps");
     static constexpr uint32_t kXBoxBytes = NT * 128;          // 64 k x NT rows x 2 B
-    static constexpr uint32_t kXStageBytes = 2 * kXBoxBytes;  // 128 k
+    static constexpr uint32_t kXStageBytes = kBlockK / 64 * kXBoxBytes;
     static constexpr uint32_t kCodesOff = 0;
     static constexpr uint32_t kXOff = kCodesOff + kLanes * kCodeSlots * kCodeStageBytes;
     static constexpr uint32_t kBarOff = kXOff + kXSlots * kXStageBytes;
@@ -284,8 +288,8 @@ struct SharedTile {
 //                unit rather than once a group.
 //  kModeFp4      4-bit codes with an e4m3 byte per 16 of them (fp4.cuh),
 //                blocks[n, k / 16] passed as e8: they enter the dequantised
-//                weight, exactly; scales[n] in the epilogue.  A unit's codes are
-//                64 bytes of each channel (64-byte swizzle).
+//                weight, exactly; scales[n] in the epilogue.  A unit is 256 k
+//                (128 bytes of codes a channel).
 template <int NT, bool kBf16, int kMode = kModeRow, int kGpu = 1>
 __global__ void __launch_bounds__(kThreads, 1)
     skinny_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_constant__ CUtensorMap map_x,
@@ -299,6 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     static_assert(!kGrp || NT <= 32, "per-group totals are held in registers: at most 32 tokens");
     using L = SkinnySmem<NT, kFp4>;
     constexpr uint32_t kCodeStageBytes = L::kCodeStageBytes;
+    constexpr int kBlockK = L::kBlockK, kAColsPerSlot = L::kAColsPerSlot;
     constexpr int kCS = L::kCodeSlots, kXS = L::kXSlots;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -446,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 mbar_arrive_expect_tx(cfull(g, s), kCodeStageBytes);
-                tma_load_2d(sbase + code_smem(g, s), &map_codes, cu.kb * (kFp4 ? kBlockK / 2 : kBlockK), cu.tile * kTileN, cfull(g, s),
+                tma_load_2d(sbase + code_smem(g, s), &map_codes, cu.kb * 128, cu.tile * kTileN, cfull(g, s),
                             pol_stream);
                 ++issued;
                 if (++g == kLanes) {
@@ -487,8 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int32_t kk = cu.kb * kBlockK;
                 const uint32_t xs = sbase + x_smem(s);
                 mbar_arrive_expect_tx(xfull(s), L::kXStageBytes);
-                tma_load_2d(xs, &map_x, kk, m_row0, xfull(s), pol_keep);
-                tma_load_2d(xs + L::kXBoxBytes, &map_x, kk + 64, m_row0, xfull(s), pol_keep);
+#pragma unroll
+                for (int b = 0; b < kBlockK / 64; ++b) tma_load_2d(xs + b * L::kXBoxBytes, &map_x, kk + 64 * b, m_row0, xfull(s), pol_keep);
                 ++issued;
                 if (++s == kXS) {
                     s = 0;
@@ -921,20 +926,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < group; ++i) mcu.next();
             if (group < iters) mx_next = mx_load(mcu.tile, mcu.kb);
         }
-        // 4 bits: the scales of this thread's row's eight blocks of a unit, loaded a
+        // 4 bits: the scales of this thread's row's sixteen blocks of a unit, loaded a
         // unit ahead in the same way
-        uint2 b_next = make_uint2(0u, 0u);
+        uint4 b_next = make_uint4(0u, 0u, 0u, 0u);
         auto blocks_load = [&](int64_t tile, int kb) {
             const int64_t row = tile * kTileN + (warp & 3) * 32 + lane;
-            uint2 b = make_uint2(0u, 0u);
+            uint4 b = make_uint4(0u, 0u, 0u, 0u);
             if (row >= n) return b;
-            const uint8_t* at = e8 + row * (k >> 4) + kb * 8;
-            if ((k & 127) == 0) return *reinterpret_cast<const uint2*>(at);
-            uint32_t two[4];
+            const uint8_t* at = e8 + row * (k >> 4) + kb * 16;
+            if ((k & 255) == 0) return *reinterpret_cast<const uint4*>(at);
+            uint32_t two[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 8; ++i)
                 two[i] = kb * kBlockK + 32 * i < k ? *reinterpret_cast<const uint16_t*>(at + 2 * i) : 0u;
             b.x = two[0] | (two[1] << 16), b.y = two[2] | (two[3] << 16);
+            b.z = two[4] | (two[5] << 16), b.w = two[6] | (two[7] << 16);
             return b;
         };
         if constexpr (kFp4) {
@@ -958,16 +964,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < kLanes; ++i) mcu.next();
                 if (it + kLanes < iters) mx_next = mx_load(mcu.tile, mcu.kb);
             }
-            uint2 blocks = make_uint2(0u, 0u);
+            uint4 blocks = make_uint4(0u, 0u, 0u, 0u);
             if constexpr (kFp4) {
                 blocks = b_next;
                 for (int i = 0; i < kLanes; ++i) mcu.next();
                 if (it + kLanes < iters) b_next = blocks_load(mcu.tile, mcu.kb);
             }
-            const uint32_t row = sbase + code_smem(group, s) + r * (kFp4 ? 64 : 128);
-            uint4 cw[kFp4 ? 4 : 8];
+            const uint32_t row = sbase + code_smem(group, s) + r * 128;
+            uint4 cw[8];
 #pragma unroll
-            for (int q = 0; q < (kFp4 ? 4 : 8); ++q) cw[q] = lds128(row + ((kFp4 ? q ^ ((r >> 1) & 3) : q ^ (r & 7)) << 4));
+            for (int q = 0; q < 8; ++q) cw[q] = lds128(row + ((q ^ (r & 7)) << 4));
             const uint32_t taken = cempty(group, s);
             if (++s == kCS) {
                 s = 0;
@@ -999,14 +1005,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             // 4 bits: block q of the unit, words 2 (q % 2) and 2 (q % 2) + 1 of chunk q / 2
-            uint32_t factor[4] = {0u, 0u, 0u, 0u};  // of blocks 0, 1 | 2, 3 | 4, 5 | 6, 7
-            if constexpr (kFp4) {
-                factor[0] = block_pair_f16(blocks.x), factor[1] = block_pair_f16(blocks.x >> 16);
-                factor[2] = block_pair_f16(blocks.y), factor[3] = block_pair_f16(blocks.y >> 16);
-            }
             auto fp4_block16 = [&](int q, uint32_t (&v)[8]) {
                 const uint4 c = cw[q >> 1];
-                const uint32_t f = (q & 1) ? both_hi(factor[q >> 1]) : both_lo(factor[q >> 1]);
+                const uint32_t word = q < 4 ? blocks.x : q < 8 ? blocks.y : q < 12 ? blocks.z : blocks.w;
+                const uint32_t pair = block_pair_f16((q & 2) ? word >> 16 : word), f = (q & 1) ? both_hi(pair) : both_lo(pair);
                 fp4_operands<kBf16>((q & 1) ? c.z : c.x, f, v);
                 fp4_operands<kBf16>((q & 1) ? c.w : c.y, f, v + 4);
             };
@@ -1021,8 +1023,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     dequant16<kBf16>(cw[q], v0[q]);
                 }
             }
-            // A slot of unit it = group + 3j: it % 6 = group + 3 (j % 2)
-            const int r = group + kLanes * (j & 1);
+            // A slot of unit it = group + 3j: it % 6 = group + 3 (j % 2) (one slot: it % 3)
+            const int r = group + kLanes * (L::kASlots == 2 ? j & 1 : 0);
             // the A slot's previous unit (it - 6) must be done
             if (it >= kAS && !mbar_wait_warp(done_bar(it - kAS), done_parity(it - kAS), abort_flag)) {
                 record_error(kErrWaitMma, abort_flag, done_bar(it - kAS), bar0);
@@ -1033,7 +1035,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q) tmem_st_x8(a_addr + q * 8, v0[q]);
 #pragma unroll
-            for (int q = 4; q < 8; ++q) {
+            for (int q = 4; q < kBlockK / 16; ++q) {
                 uint32_t v[8];
                 if constexpr (kFp4) {
                     fp4_block16(q, v);
@@ -1153,20 +1155,6 @@ bool encode_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint6
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The codes of 4-bit weights: `inner` bytes x `outer` rows, boxes of 64 bytes x
-// box_outer rows, 64-byte swizzle.
-static bool encode_2d_64(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint32_t box_outer) {
-    EncodeTiledFn fn = get_encode_fn();
-    if (!fn) return false;
-    const cuuint64_t dims[2] = {inner, outer};
-    const cuuint64_t strides[1] = {inner};
-    const cuuint32_t box[2] = {64, box_outer};
-    const cuuint32_t estr[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 bool encode_3d_blocks(CUtensorMap* map, const void* base, uint64_t rows, uint64_t k, uint32_t box_rows,
                       uint32_t box_blocks) {
     EncodeTiledFn fn = get_encode_fn();
@@ -1219,9 +1207,9 @@ constexpr int kSplitUnits = 6;
 constexpr int kSharedUnits = 9;
 constexpr int64_t kMaxClusterUnits = 1 << 24;  // cluster-local unit indices are 32-bit
 
-SkinnyShape skinny_shape(int64_t n, int64_t k, const int* active, int nt, bool grouped) {
+SkinnyShape skinny_shape(int64_t n, int64_t k, const int* active, int nt, bool grouped, int unit) {
     const int64_t tiles = (n + kTileN - 1) / kTileN;
-    const int64_t nkb = (k + kBlockK - 1) / kBlockK;
+    const int64_t nkb = (k + unit - 1) / unit;
     SkinnyShape best{1, (tiles + active[1] - 1) / active[1]};
     int64_t best_cost = best.tpc * nkb;
     for (int cl = 2; cl <= kMaxCluster && cl <= nkb; ++cl) {
@@ -1231,8 +1219,8 @@ SkinnyShape skinny_shape(int64_t n, int64_t k, const int* active, int nt, bool g
         if ((nt > 32 || grouped) && tpc > 1) continue;
         if (tpc * nkb >= kMaxClusterUnits) continue;
         const int64_t per_cta = (tpc * nkb + cl - 1) / cl;
-        if (per_cta < kMinUnitsPerCta) continue;
-        const int64_t cost = per_cta + (tpc == 1 ? kSplitUnits : kSharedUnits);
+        if (per_cta < kMinUnitsPerCta * kUnitK / unit) continue;
+        const int64_t cost = per_cta + (tpc == 1 ? kSplitUnits : kSharedUnits) * kUnitK / unit;
         if (cost < best_cost) {
             best_cost = cost;
             best = {cl, tpc};
@@ -1242,7 +1230,7 @@ SkinnyShape skinny_shape(int64_t n, int64_t k, const int* active, int nt, bool g
 }
 
 bool skinny_shape_valid(const SkinnyShape& sh, int64_t m, int64_t k, bool grouped) {
-    const int64_t nkb = (k + kBlockK - 1) / kBlockK;
+    const int64_t nkb = (k + kUnitK - 1) / kUnitK;
     const int nt = m <= 16 ? 16 : m <= 32 ? 32 : 64;
     return sh.cl >= 1 && sh.cl <= kMaxCluster && sh.tpc >= 1 && sh.cl <= nkb && sh.tpc * nkb < kMaxClusterUnits &&
            (sh.cl == 1 || (nt <= 32 && !grouped) || sh.tpc == 1);
@@ -1294,15 +1282,14 @@ static cudaError_t launch_nt(const LinearArgs& a, const SkinnyShape* forced, cud
     if (attr_err != cudaSuccess) return attr_err;
 
     CUtensorMap map_codes, map_x;
-    if (kMode == kModeFp4 ? !encode_2d_64(&map_codes, a.codes, static_cast<uint64_t>(a.k / 2), static_cast<uint64_t>(a.n), kTileN)
-                          : !encode_2d(&map_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.codes, static_cast<uint64_t>(a.k),
-                                       static_cast<uint64_t>(a.n), static_cast<uint64_t>(a.k), kBlockK, kTileN))
+    const uint64_t row_bytes = static_cast<uint64_t>(kMode == kModeFp4 ? a.k / 2 : a.k);  // of codes
+    if (!encode_2d(&map_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.codes, row_bytes, static_cast<uint64_t>(a.n), row_bytes, 128, kTileN))
         return cudaErrorInvalidValue;
     if (!encode_2d(&map_x, CU_TENSOR_MAP_DATA_TYPE_UINT16, a.x, static_cast<uint64_t>(a.k),
                    static_cast<uint64_t>(a.m), static_cast<uint64_t>(a.k) * 2, 64, NT))
         return cudaErrorInvalidValue;
 
-    const SkinnyShape shape = forced ? *forced : skinny_shape(a.n, a.k, active[dev], NT, kGrp);
+    const SkinnyShape shape = forced ? *forced : skinny_shape(a.n, a.k, active[dev], NT, kGrp, L::kBlockK);
     const int64_t tiles = (a.n + kTileN - 1) / kTileN;
     const int64_t clusters = (tiles + shape.tpc - 1) / shape.tpc;
     // programmatic dependent launch: this grid's prologue (barrier set-up,

@@ -391,11 +391,13 @@ FP8W_API fp8w_status fp8w_dequantize_fp4(const uint8_t *codes, const uint8_t *bl
  *   codes  [n, k / 2], blocks [n, k / 16] uint8, device, 16-byte aligned.
  *   flags  0 or FP8W_FLAG_WEIGHTS_READY (for codes, blocks and scales).
  *   k % 32 == 0.  Other arguments as fp8w_linear.
- * fp32 accumulation, scale and bias applied in fp32 with one rounding.  Up to 64
+ * fp32 accumulation, scale and bias applied in fp32 with one rounding.  Up to 8
  * tokens the codes are streamed into registers and multiplied there (bf16
  * activations as fp16 times a power of two a token, which is exact but for values
- * below 2^-28 of a token's largest, off by at most 2^-39 of that); beyond, the
- * prefill GEMM.  One launch and no workspace.
+ * below 2^-28 of a token's largest, off by at most 2^-39 of that); up to 64 the
+ * tensor-core kernel for few tokens; beyond, the prefill GEMM, or the former in
+ * slabs of 64 tokens (a launch each) where few channels make that shorter.  No
+ * workspace.
  */
 FP8W_API fp8w_status fp8w_linear_fp4(const void *x, int act_dtype, int64_t m, int64_t k, const uint8_t *codes,
                             const uint8_t *blocks, const float *scales, const float *bias, int64_t n, void *y,

@@ -168,6 +168,12 @@ def test_many_tokens(m, n, k, dtype):
     run(m, n, k, dtype, bias=n != 256, ready=n == 127)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("m,n,k", [(700, 2000, 4096), (257, 5000, 2080), (100, 20000, 1024), (129, 1000, 14336), (513, 300, 8192)])
+def test_many_tokens_of_larger_layers(m, n, k, dtype):
+    run(m, n, k, dtype)
+
+
 @pytest.mark.parametrize("m", [3, 20, 90])
 def test_activations_of_every_magnitude(m):
     # bf16 beyond fp16's range on both sides, in one token and between tokens
