@@ -474,15 +474,15 @@ def quantize_fp4(w, codes=None, blocks=None, scales=None):
         raise TypeError("w must be a contiguous 2-D float32, bfloat16 or float16 CUDA tensor")
     n, k = shape
     if codes is None:
-        codes = _empty((n, k >> 1), dtype=_uint8, device=dev)
+        codes = _empty((n, k >> 1), dtype=_uint8, device=w.device)
     else:
         _given("codes", codes, _uint8, (n, k >> 1), dev)
     if blocks is None:
-        blocks = _empty((n, k >> 4), dtype=_uint8, device=dev)
+        blocks = _empty((n, k >> 4), dtype=_uint8, device=w.device)
     else:
         _given("blocks", blocks, _uint8, (n, k >> 4), dev)
     if scales is None:
-        scales = _empty((n,), dtype=_float32, device=dev)
+        scales = _empty((n,), dtype=_float32, device=w.device)
     else:
         _given("scales", scales, _float32, (n,), dev)
     st = _lib.fp8w_quantize_fp4(w.data_ptr(), kind, n, k, codes.data_ptr(), blocks.data_ptr(), scales.data_ptr(), _stream_of(dev))
@@ -511,7 +511,7 @@ def dequantize_fp4(codes, blocks, scales, dtype=None, out=None):
     bp = _index("blocks", blocks, _uint8, rows + (k >> 4,), dev)
     sp = _index("scales", scales, _float32, rows, dev)
     if out is None:
-        out = _empty(rows + (k,), dtype=dtype, device=dev)
+        out = _empty(rows + (k,), dtype=dtype, device=codes.device)
     elif out.shape != rows + (k,) or out.dtype is not dtype or out.get_device() != dev or not out.is_contiguous():
         raise ValueError("out must be a contiguous [.., K] tensor of the requested dtype")
     st = _lib.fp8w_dequantize_fp4(cp, bp, sp, scales.numel(), k, kind, out.data_ptr(), _stream_of(dev))
@@ -536,7 +536,7 @@ def linear_fp4(x, codes, blocks, scales, bias=None, out=None, weights_ready=Fals
     sp = _index("scales", scales, _float32, (n,), dev)
     ap = None if bias is None else _index("bias", bias, _float32, (n,), dev)
     if out is None:
-        out = _empty((m, n), dtype=dtype, device=dev)
+        out = _empty((m, n), dtype=dtype, device=x.device)
     elif out.shape != (m, n) or out.dtype is not dtype or out.get_device() != dev or not out.is_contiguous():
         raise ValueError("out must be a contiguous [M, N] tensor of x's dtype")
     st = _lib.fp8w_linear_fp4(x.data_ptr(), act, m, k, cp, bp, sp, ap, n, out.data_ptr(), FLAG_WEIGHTS_READY if weights_ready else 0,

@@ -20,7 +20,7 @@
 //   warps 0-7, 8-15 softmax of pipe 0, 1: two threads a row, half its keys each
 //   warps 16, 18, 19 (with codes 16, 18) TMA producers of key and value tiles
 //   warp 17         MMA issue, one thread; owns TMEM
-//   warps 20-23     (e4m3 cache) codes -> 16-bit operand tiles
+//   warps 20-23     (a cache of codes) codes -> 16-bit operand tiles
 // What bounds it: 8192 new tokens, 32 query heads of 128, 16-slot pages take 387
 // us, 1421 TFLOP/s, 74% of the measured rate (calls back to back for longer: 407
 // us).  Per key tile of 256 rows the products need 2048 cycles of the 3100 it
@@ -34,6 +34,10 @@
 // softmax multiplies both scales too, and the conversion shares its schedulers
 // (bf16, whose conversion takes more instructions: 734); 17% is the last wave (352
 // row tiles on 152 SMs).
+// 4 bits (fp4.cuh): the converting warps fold the blocks' scales into the operands,
+// exactly, 32 codes and two scales a 16-byte chunk.  The products are of fp16 for bf16
+// activations too: the chunks 724 us (43%), 818 with products of bf16, whose codes take
+// five instructions a pair instead of two; fp16 activations 710 (44%).
 // Measured and not kept for the prompt: a pair of CTAs sharing products of 256
 // rows (cta_group::2, half of each key and value tile a CTA): 537 us when one CTA
 // took 455, each product waiting for both CTAs' softmax; scores of 64 keys at a
@@ -110,7 +114,8 @@ struct AttnSmem {
     // full, empty [kStages] | rawfull, rawempty [kRaw] | sfull, pfull, ofull [2] | qfull | joinfull, joinfree | drain | tail
     static constexpr uint32_t kNumBars = 2 * kStages + 2 * kRaw + 6 + 1 + 2 + 1 + 1;
     static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;
-    static constexpr uint32_t kBytes = kMiscOff + 16;
+    static constexpr uint32_t kTurnOff = kMiscOff + 16;          // (4 bits) factors of the two row tiles' queries
+    static constexpr uint32_t kBytes = kTurnOff + (kForm == kFormFp4 ? 2 * kRows * 4 : 0);
     static_assert(kBytes <= 227 * 1024 && kMlOff % 1024 == 0, "shared memory");
     static constexpr int kThreads = kSoftmaxThreads + 128 + (kFp8 ? 128 : 0);
     // registers a thread at launch and after the split
@@ -343,13 +348,14 @@ struct Join {
 };
 
 // The largest of a row's exponents plus log2 of the value scales, less m, over
-// `width` columns of scores from taddr on (ksc: their first key scale); top, bot:
-// the last and first column that the row sees.  Out of line, for the loop over the
+// `width` columns of scores from taddr on (ksc: their first key scale; turn: the
+// row's factor); top, bot: the last and first column that the row sees.  Out of line, for the loop over the
 // tiles has no registers to spare for it (773 us for the chunks of codes that take
 // 696 so).
-__device__ __noinline__ float scaled_peak(uint32_t taddr, uint32_t ksc, int width, float less_m, bool masked, int top, int bot) {
+template <bool kTurn>
+__device__ __noinline__ float scaled_peak(uint32_t taddr, uint32_t ksc, int width, float less_m, float turn, bool masked, int top, int bot) {
     float mx = kNegInf, my = kNegInf;
-    const uint64_t less_m2 = pack2(less_m, less_m);
+    const uint64_t less_m2 = pack2(less_m, less_m), turn2 = pack2(turn, turn);
 #pragma unroll 1
     for (int b = 0; b < width; b += 16) {
         uint32_t v[16];
@@ -357,8 +363,8 @@ __device__ __noinline__ float scaled_peak(uint32_t taddr, uint32_t ksc, int widt
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
             const float4 f = lds_f4(ksc + (b + i) * 4), g = lds_f4(ksc + (2 * kKeys + b + i) * 4);
-            uint64_t x = fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), pack2(f.x, f.y), less_m2);
-            uint64_t y = fma2(pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), pack2(f.z, f.w), less_m2);
+            uint64_t x = fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), kTurn ? mul2(pack2(f.x, f.y), turn2) : pack2(f.x, f.y), less_m2);
+            uint64_t y = fma2(pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), kTurn ? mul2(pack2(f.z, f.w), turn2) : pack2(f.z, f.w), less_m2);
             x = add2(x, pack2(g.x, g.y));
             y = add2(y, pack2(g.z, g.w));
             auto seen = [&](int e, float z) { return masked && (b + i + e > top || b + i + e < bot) ? kNegInf : z; };
@@ -580,6 +586,10 @@ __global__ void __launch_bounds__(AttnSmem<DP, kForm>::kThreads, 1)
                      const __grid_constant__ AttnParams p) {
     using L = AttnSmem<DP, kForm>;
     constexpr bool kFp8 = L::kFp8, kFp4 = kForm == kFormFp4;  // codes; of 4 bits
+    // With 4 bits the products are of fp16 whatever the activations' type: the codes
+    // take two instructions a pair instead of five, and the weights round to 11 bits.
+    // bf16 queries go over exactly but for a power of two a row.
+    constexpr bool kTurn = kFp4 && kBf16, kMmaBf16 = kBf16 && !kFp4;
     constexpr int kStages = L::kStages, kRaw = L::kRaw;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
@@ -597,8 +607,8 @@ __global__ void __launch_bounds__(AttnSmem<DP, kForm>::kThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr float kSlack = 8.0f, kLift = kBf16 ? 0.0f : kLiftF16;
-    constexpr bool kScaledF16 = kFp8 && !kBf16;  // m is the reference of weight times value scale
+    constexpr float kSlack = 8.0f, kLift = kMmaBf16 ? 0.0f : kLiftF16;
+    constexpr bool kScaledF16 = kFp8 && !kMmaBf16;  // m is the reference of weight times value scale
 
     if (warp == kMmaWarp) {
         tmem_alloc(smem_u32(tmem_slot), kAttnTmemCols);
@@ -751,8 +761,8 @@ __global__ void __launch_bounds__(AttnSmem<DP, kForm>::kThreads, 1)
             // scheduler with four softmax warps, and the tensor cores wait for it
             // (8192 tokens: a whole warp that elects for each statement 447 us, this 434).
             if (elect_one()) {
-                constexpr uint32_t idesc_s = idesc_f16(kBf16, kKeys);
-                constexpr uint32_t idesc_o = idesc_f16(kBf16, DP) | kIdescBNMajor;
+                constexpr uint32_t idesc_s = idesc_f16(kMmaBf16, kKeys);
+                constexpr uint32_t idesc_o = idesc_f16(kMmaBf16, DP) | kIdescBNMajor;
                 const uint64_t qd = smem_desc_sw128_kmajor(sbase + L::kQOff), kd = smem_desc_sw128_kmajor(sbase + L::kRingOff),
                                vd = smem_desc_sw128_nmajor(sbase + L::kRingOff);
                 const uint32_t q_lo = static_cast<uint32_t>(qd), k_lo = static_cast<uint32_t>(kd), v_lo = static_cast<uint32_t>(vd);
@@ -961,7 +971,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kForm>::kThreads, 1)
 #pragma unroll
                         for (uint32_t e = 0; e < 4; ++e) {
                             uint32_t v[4];
-                            fp4_operands<kBf16>(w4[e], e < 2 ? both_lo(f) : both_hi(f), v);
+                            fp4_operands<false>(w4[e], e < 2 ? both_lo(f) : both_hi(f), v);
                             sts128(sub + (((4 * u + e) & 7) ^ swz) * 16, v[0], v[1], v[2], v[3]);
                         }
                         continue;
@@ -1045,12 +1055,30 @@ __global__ void __launch_bounds__(AttnSmem<DP, kForm>::kThreads, 1)
                     const int f = split > 1 ? line / w.rows : 0, at = f * per_copy + line - f * w.rows;  // row of the two tiles
                     const uint32_t a = sbase + L::kQOff + (at >> 7) * L::kTileBytes + (ch >> 3) * (kRows * 128) +
                                        (at & 127) * 128 + (((ch & 7) ^ (at & 7)) << 4);
+                    if constexpr (kTurn) {
+                        // the row's largest value to [2^14, 2^15): what falls below fp16's
+                        // normal numbers then is less than 2^-28 of it, off by 2^-39 of it
+                        uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w}, top = 0u;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) top = max(top, max(u[e] & 0x7FFFu, (u[e] >> 16) & 0x7FFFu));
+                        // (the lanes of a row are here together)
+                        const unsigned lanes = static_cast<unsigned>((1ull << kChunks) - 1) << (lane & (32 - kChunks));
+#pragma unroll
+                        for (int d = 1; d < kChunks; d <<= 1) top = max(top, __shfl_xor_sync(lanes, top, d));
+                        const int up = min(max(127 + 14 - (static_cast<int>(top >> 7) - 127), 1), 253);
+                        const float factor = __int_as_float(up << 23);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) u[e] = pack16<false>(bf16_lo_to_f32(u[e]) * factor, bf16_hi_to_f32(u[e]) * factor);
+                        v[i] = make_uint4(u[0], u[1], u[2], u[3]);
+                        if (ch == 0) reinterpret_cast<float*>(smem + L::kTurnOff)[at] = __int_as_float((254 - up) << 23);
+                    }
                     sts128(a, v[i].x, v[i].y, v[i].z, v[i].w);
                 }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(qfull);
+            if constexpr (kTurn) softmax_bar();  // the rows' factors are there
         }
         const int R = w.row0 + qtile * kRows + rr;
         const bool valid = qtile * kRows + rr < w.rows;
@@ -1065,6 +1093,9 @@ __global__ void __launch_bounds__(AttnSmem<DP, kForm>::kThreads, 1)
         const uint32_t t_s = tmem + tq + pipe * kKeys, t_o = tmem + tq + 2 * kKeys + pipe * DP + half * (DP / 2);
         const float c = p.c;
         const uint64_t c2 = pack2(c, c);
+        // what the row's scores are multiplied by beside the keys' scales
+        const float turn = kTurn && n > 0 && valid ? reinterpret_cast<const float*>(smem + L::kTurnOff)[qtile * kRows + r] : 1.0f;
+        const uint64_t turn2 = pack2(turn, turn);
         float m = kNegInf, l = 0.0f;  // the row's reference, in exponents of two and less kLift, and its sum
         int done = 0;                 // tiles of this pipe
         bool ok = true;
@@ -1096,8 +1127,10 @@ __global__ void __launch_bounds__(AttnSmem<DP, kForm>::kThreads, 1)
                     uint64_t y = pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
                     if constexpr (kFp8) {
                         const float4 f = lds_f4(ksc + (b + i) * 4);
-                        x = fma2(x, pack2(f.x, f.y), less_m);
-                        y = fma2(y, pack2(f.z, f.w), less_m);
+                        uint64_t f0 = pack2(f.x, f.y), f1 = pack2(f.z, f.w);
+                        if constexpr (kTurn) f0 = mul2(f0, turn2), f1 = mul2(f1, turn2);
+                        x = fma2(x, f0, less_m);
+                        y = fma2(y, f1, less_m);
                     } else {
                         x = fma2(x, c2, less_m);
                         y = fma2(y, c2, less_m);
@@ -1123,7 +1156,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kForm>::kThreads, 1)
             float mx = kNegInf, my = kNegInf;
             // The maximum of what m is the reference of, less m.
             auto peak = [&](float less) {
-                if constexpr (kScaledF16) return scaled_peak(t_s + cbeg, ksc, W, less, masked, hi - key0, lo - key0);
+                if constexpr (kScaledF16) return scaled_peak<kTurn>(t_s + cbeg, ksc, W, less, turn, masked, hi - key0, lo - key0);
                 const uint64_t less2 = pack2(less, less);
 #pragma unroll 1
                 for (int b = 0; b < W; b += kStep) {
@@ -1171,8 +1204,8 @@ __global__ void __launch_bounds__(AttnSmem<DP, kForm>::kThreads, 1)
                             x = mul2(x, pack2(f.x, f.y));
                             y = mul2(y, pack2(f.z, f.w));
                         }
-                        o[(b + i) / 2] = pack16<kBf16>(lo2(x), hi2(x));
-                        o[(b + i) / 2 + 1] = pack16<kBf16>(lo2(y), hi2(y));
+                        o[(b + i) / 2] = pack16<kMmaBf16>(lo2(x), hi2(x));
+                        o[(b + i) / 2 + 1] = pack16<kMmaBf16>(lo2(y), hi2(y));
                     }
                     if constexpr (kFp8) asm volatile("" : "+r"(ksc));  // scales of one part at a time
                 }

@@ -7,7 +7,9 @@
 // of 16 bits, a block is 4 or 2 neighbouring lanes, and a row belongs to a warp
 // (up to 1024 values) or to a CTA of 256 threads; rows beyond the registers are
 // read a second time, from L2.
-// Bytes a value: 4 or 2 read, 9 / 16 written.
+// Bytes a value: 4 or 2 read, 9 / 16 written.  14336 x 4096 of fp32: 44.5 us, 6.0 TB/s
+// (89% of the measured copy rate); its values read back as bf16 32.5 us, 4.6 TB/s (68%:
+// conversions; 43 us with a division by the row and single 16-bit conversions).
 #include "fp4.cuh"
 #include "fp8w_internal.h"
 

@@ -1,4 +1,4 @@
-// fp4_linear.cu -- kernel K9: the linear layer on 4-bit weights for few tokens.
+// fp4_linear.cu -- kernel K9: the linear layer on 4-bit weights for up to 8 tokens.
 //
 //   y[m, n] = round(scale[n] * sum_k x[m, k] * e4m3(block) * e2m1(code) + bias[n])
 // (the form: fp4.cuh).  With few tokens the weight's bytes, 9 bits for two
@@ -21,11 +21,22 @@
 // CTA, which takes their largest to [2^14, 2^15): what falls below fp16's normal
 // numbers then is less than 2^-28 of the largest, and off by 2^-39 of it.
 //
-// Split.  G of a CTA's 16 warps share a tile's inputs and add their sums in shared
+// Split.  G of a CTA's 24 warps share a tile's inputs and add their sums in shared
 // memory in the warps' order; the CTAs of a cluster share the inputs too where
 // there are too few tiles for the SMs (or too many activations for shared
 // memory), and add theirs in distributed shared memory in rank order.  Each CTA
-// goes over its tiles with the activations in place.
+// goes over its tiles with the activations in place.  The launch takes the split of
+// which a model of the steps, the staging and the joins promises the least time.
+//
+// Measured (bf16, weights not in L2): 14336 x 4096, 33 MB, 1 token 10.0 us, 9.1 with
+// the weights ready (48 and 54% of the measured copy rate; e4m3 codes, 59 MB, take
+// 11.9); 8 tokens 13.0; 4096 x 14336 12.0 and 15.4; 1024 x 4096 3.8 and 6.4.  A
+// launch's start and end are 3 us of it.  Then instructions count as much as bytes: 80
+// of a step's 105 are conversions, multiplies and products, and set-up adds half again
+// (divisions on the device, a zeroing before each load and loads under a test each had
+// it at 256 a step and 14.8 us; 32 warps of 64 registers spilled: 19.9).  Tiles of 16, 24
+// and 32 tokens in the same way took 17.4, 22 and 32 us where the skinny kernel takes
+// 15 to 16.5: the products (10 cycles each on a scheduler) and the staging.
 #include <mutex>
 
 #include "fp4.cuh"
@@ -127,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_few_kernel(const __grid_const
     const int64_t m0 = static_cast<int64_t>(blockIdx.y) * p.slab;
     const int tokens = p.m - m0 < p.slab ? static_cast<int>(p.m - m0) : p.slab;
     const int G = p.g, J = p.j, group = divide(warp, p.g_inverse), wk = warp - group * G, rounds = p.rounds;
-    // sizes by a full slab, so that all slabs and ranks have the same places
+    // places by a full slab, the same for all slabs and ranks
     const int slab = p.slab;
     const Fp4Layout L = fp4_layout(slab, p.per_rank, rounds, J, p.cl > 1);
     const int step0 = rank * p.steps >> p.cl_log2, mine = ((rank + 1) * p.steps >> p.cl_log2) - step0;

@@ -26,6 +26,9 @@
 //               e4m3 -> bf16/fp16 exactly (value * 2^-120 by byte moves, then
 //               * 2^120, or the hardware e4m3 -> f16 conversion), written in
 //               the 128-byte swizzled K-major layout the descriptor reads
+//               (4 bits: four warpgroups, warps 8-23, one for each k-block of a
+//               code stage of 256 codes a row; 2048 tokens on 14336 x 4096 181 us,
+//               68% of the measured rate, 195 with two; e4m3 170)
 // Every wait is bounded; a CTA that gives up records a code, raises its abort
 // flag, lets its copies and MMAs land and frees TMEM.
 #include <cuda.h>

@@ -541,11 +541,15 @@ FP8W_API fp8w_status fp8w_rope_append(const void *q, const void *k, const void *
  *                how the work is split and nothing else.
  *   out          like q, with out_stride (output); it may not overlap q.
  * Scores, softmax and sums are fp32; the softmax weights are rounded to 16 bits
- * for the second product: to act_dtype, or with codes and few rows to fp16.
- * The scales of slots multiply scores and weights in fp32, the weights before they are
- * rounded; those of 4-bit blocks go into the 16-bit operands, which is exact.  Below its normal numbers fp16 takes at most 2^-32 of the largest
- * from a weight (with codes: of the largest weight times value scale, rows of
- * zeros left out).  One rounding at the end.
+ * for the second product: to act_dtype, or with codes to fp16 (e4m3: of few rows
+ * only).
+ * The scales of slots multiply scores and weights in fp32, the weights before they
+ * are rounded; those of 4-bit blocks go into the 16-bit operands, which is exact.
+ * bf16 queries on fp16 products are taken times a power of two a row, exact but for
+ * values below 2^-28 of the row's largest (off by 2^-39 of it).  Below its normal
+ * numbers fp16 takes at most 2^-32 of the largest from a weight (with codes: of the
+ * largest weight times value scale, rows of zeros left out).  One rounding at the
+ * end.
  * Cached values of positions below len are finite, in act_dtype's range (a
  * value that is not may reach other tokens of its sequence, none of another);
  * slots past them may hold anything.  A table entry outside the cache, a len beyond the table or

@@ -1,7 +1,17 @@
 """GPU tests of the 4-bit cache: rows appended bit for bit as the rule gives
 them, and attention against 64 bits on the values that the cache stands for
 (bounds: attention_reference.py; the products of a code and its block's scale are
-exact, so the form adds nothing to them)."""
+exact, so the form adds nothing to them).
+
+The weights are fp16 here whatever the activations' type, so the bounds of bf16 get
+what fp16 takes below its normal numbers, too:  keys 2^-32 max|v|.
+  A weight times its slot's scale, p_j s_j, is taken 2^7 times as large as its
+  reference, which lies at most 2^8 under the largest and never above it (but by
+  fp32 roundings): the largest is 2^7 in fp16 at least.  Below 2^-14 fp16 rounds by
+  2^-25 at most, 2^-32 of that largest.  Row j's values are s_j times 2688 at most,
+  and its largest is that (the rule's scale), so a weight's error adds at most
+  2^-32 max_j(p_j s_j) 2688 <= 2^-32 max|v| to an output (sum of the p at least the
+  largest), and `keys` weights that many times as much."""
 import numpy as np
 import pytest
 
@@ -23,6 +33,10 @@ POISON = 0x7FC1
 
 
 # ------------------------------------------------------------------ append --
+
+def bound(tol, v, length, dtype):
+    return tol + (length * 2.0 ** -32 * float(v.abs().max()) if dtype == "bf16" and length else 0.0)
+
 
 def empty_cache(pages, kv, page, dim, layout, fill=0xA5):
     shape = (pages, kv, page, dim // 2) if layout == "heads" else (pages, page, kv, dim // 2)
@@ -116,7 +130,7 @@ def run(new, lens, kv_heads, group, dim, page, dtype="bf16", layout="heads", win
     for b, n in enumerate(new):
         k, v = paged.rows[b]
         want, tol = attend(torch, q[first[b]:first[b + 1]].double(), k, v, n, lens[b], dim ** -0.5, window, dtype)
-        check(torch, out[first[b]:first[b + 1]], want, tol)
+        check(torch, out[first[b]:first[b + 1]], want, bound(tol, v, lens[b], dtype))
     return q, paged, out
 
 
@@ -191,6 +205,24 @@ def test_rows_of_zeros_do_not_hide_small_values(new, dtype):
     run([new], [400], 1, 4, 64, 16, dtype, change=zero_rows(130))
 
 
+@pytest.mark.parametrize("new,window", [(4, 0), (60, 0), (200, 33)])
+def test_bf16_queries_of_every_magnitude(new, window):
+    """Heads and tokens from 2^-120 to 2^6 times as large as others, and values far below their row's largest."""
+    paged = R.Paged4(torch, fw, 5, [700], 2, 128, 16, "heads")
+    g = torch.Generator(DEV)
+    g.manual_seed(9)
+    q = torch.randn((new, 8, 128), generator=g, device=DEV)
+    q *= torch.exp2(torch.randint(-12, 1, q.shape, generator=g, device=DEV).float())
+    q *= torch.exp2(torch.linspace(-120, 6, new * 8, device=DEV)).view(new, 8, 1)[torch.randperm(new, generator=g, device=DEV)]
+    q[0, 1] = 0.0
+    q = q.bfloat16()
+    starts = torch.tensor([0, new], dtype=torch.int32, device=DEV)
+    got = fw.paged_attention(q, paged.cache, paged.table, paged.lens_t, starts=starts, window=window)
+    assert fw.device_error() == 0
+    want, tol = attend(torch, q.double(), *paged.rows[0], new, 700, 128 ** -0.5, window, "bf16")
+    check(torch, got, want, bound(tol, paged.rows[0][1], 700, "bf16"))
+
+
 @pytest.mark.parametrize("new", [1, 30])
 def test_a_query_that_is_not_finite_reaches_its_row_alone(new):
     q, paged, out = run([new, new], [90, 300], 2, 4, 128, 16)
@@ -225,7 +257,7 @@ def test_pages_past_four_gib():
         assert fw.device_error() == 0
         kk, vv = (d(R.values(*b))[order[0].long()].transpose(1, 2).flatten(0, 1)[:length] for b in both)
         want, tol = attend(torch, q.double(), kk, vv, new, length, dim ** -0.5, 0, "bf16")
-        check(torch, got, want, tol)
+        check(torch, got, want, bound(tol, vv, length, "bf16"))
 
 
 def test_a_page_outside_the_cache_is_recorded():
