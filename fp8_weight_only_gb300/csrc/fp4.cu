@@ -10,6 +10,8 @@
 // Bytes a value: 4 or 2 read, 9 / 16 written.  14336 x 4096 of fp32: 44.5 us, 6.0 TB/s
 // (89% of the measured copy rate); its values read back as bf16 32.5 us, 4.6 TB/s (68%:
 // conversions; 43 us with a division by the row and single 16-bit conversions).
+#include <type_traits>
+
 #include "fp4.cuh"
 #include "fp8w_internal.h"
 
@@ -153,10 +155,15 @@ cudaError_t quantize_type(const void* w, int64_t n, int64_t k, uint8_t* codes, u
 // Bytes a value: 9 / 16 read, 2 or 4 written.
 constexpr int kFp4Unroll = 4;
 
-// hi and a sticky last bit: rounds to fewer bits as the exact product does.
+// hi and a sticky last bit: rounds to fewer bits as the exact product does.  kTiny:
+// for scales below kTinyScale, whose product can drop bits below fp32's subnormal
+// numbers; what it drops is looked at 2^64 times as large, exactly.
+constexpr float kTinyScale = 0x1p-100f;
+template <bool kTiny>
 __device__ __forceinline__ float mul_sticky(float c, float s) {
     const float hi = __fmul_rz(c, s);
-    return fmaf(c, s, -hi) != 0.0f ? __uint_as_float(__float_as_uint(hi) | 1u) : hi;
+    const float rest = kTiny ? fmaf(c * 0x1p64f, s, hi * -0x1p64f) : fmaf(c, s, -hi);
+    return rest != 0.0f ? __uint_as_float(__float_as_uint(hi) | 1u) : hi;
 }
 
 struct Fp4Walk {        // blocks of 16 values, a grid of threads apart
@@ -198,26 +205,33 @@ __global__ void __launch_bounds__(kFp4Threads) dequantize_fp4_kernel(const uint8
             const uint32_t factor = both_lo(block_pair_f16(bl[u]));
             constexpr int kWords = OUT == 0 ? 16 : 8;
             uint32_t o[kWords];
+            auto convert = [&](auto tiny) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t p[4];
-                e2m1x8_to_f16x2(h ? cw[u].y : cw[u].x, p[0], p[1], p[2], p[3]);
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t p[4];
+                    e2m1x8_to_f16x2(h ? cw[u].y : cw[u].x, p[0], p[1], p[2], p[3]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    p[e] = f16x2_mul(p[e], factor);  // exact
-                    const float x = f16_lo_to_f32(p[e]), y = f16_hi_to_f32(p[e]);
-                    if constexpr (OUT == 0) {
-                        o[8 * h + 2 * e] = __float_as_uint(__fmul_rn(x, sc[u]));
-                        o[8 * h + 2 * e + 1] = __float_as_uint(__fmul_rn(y, sc[u]));
-                    } else {
-                        const float a = mul_sticky(x, sc[u]), b = mul_sticky(y, sc[u]);
-                        if constexpr (OUT == 1)
-                            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[4 * h + e]) : "f"(b), "f"(a));
-                        else
-                            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[4 * h + e]) : "f"(b), "f"(a));
+                    for (int e = 0; e < 4; ++e) {
+                        p[e] = f16x2_mul(p[e], factor);  // exact
+                        const float x = f16_lo_to_f32(p[e]), y = f16_hi_to_f32(p[e]);
+                        if constexpr (OUT == 0) {
+                            o[8 * h + 2 * e] = __float_as_uint(__fmul_rn(x, sc[u]));
+                            o[8 * h + 2 * e + 1] = __float_as_uint(__fmul_rn(y, sc[u]));
+                        } else {
+                            constexpr bool kTiny = decltype(tiny)::value;
+                            const float a = mul_sticky<kTiny>(x, sc[u]), b = mul_sticky<kTiny>(y, sc[u]);
+                            if constexpr (OUT == 1)
+                                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[4 * h + e]) : "f"(b), "f"(a));
+                            else
+                                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[4 * h + e]) : "f"(b), "f"(a));
+                        }
                     }
                 }
-            }
+            };
+            if (OUT == 1 && fabsf(sc[u]) < kTinyScale)
+                convert(std::integral_constant<bool, OUT == 1>{});
+            else
+                convert(std::false_type{});
             uint4* dst = static_cast<uint4*>(out) + v * (kWords / 4);
 #pragma unroll
             for (int q = 0; q < kWords; q += 4) __stcs(dst + q / 4, make_uint4(o[q], o[q + 1], o[q + 2], o[q + 3]));

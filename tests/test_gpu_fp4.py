@@ -90,6 +90,27 @@ def test_dequantize_rounds_once(n, k, dtype):
         assert float((got.cpu() != rounded).double().mean()) < 1e-3
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_dequantize_of_every_magnitude_rounds_once(dtype):
+    """Scales from the smallest subnormal to the largest, against 64 bits rounded to
+    the type's grid, its subnormal part too: a product has 30 bits, its quotient by
+    the grid's step is exact in 64 bits, and rint takes ties to even."""
+    rng = np.random.default_rng(17)
+    n, k = 4096, 256
+    codes, blocks = rng.integers(0, 256, (n, k // 2), dtype=np.uint8), rng.integers(0, 127, (n, k // 16), dtype=np.uint8)
+    scales = np.ldexp(rng.integers(1, 1 << 24, n).astype(np.float64), rng.integers(-149, 93, n)).astype(np.float32)
+    scales[:1024] = np.ldexp(rng.integers(1 << 23, (1 << 23) + 64, 1024).astype(np.float64), -149)  # at the smallest normal number
+    scales[:4] = np.float32(2.0 ** -149), np.float32(2.0 ** -126), np.float32(2.0 ** -126 + 2.0 ** -149), np.float32(2.0 ** 112)
+    scales[1::2] *= -1                              # a scale that is brought may be negative
+    want = R.values(codes, blocks, scales)
+    bits, lowest, most = {"f32": (24, -126, 128), "bf16": (8, -126, 128), "f16": (11, -14, 16)}[dtype]
+    step = np.ldexp(1.0, np.maximum(np.frexp(want)[1] - 1, lowest) - (bits - 1))
+    want = np.rint(want / step) * step
+    want = np.where(np.abs(want) >= 2.0 ** most, np.copysign(np.inf, want), want)
+    got = fw.dequantize_fp4(*(torch.from_numpy(a).to(DEV) for a in (codes, blocks, scales)), DT[dtype]).cpu().double().numpy()
+    assert np.array_equal(got, want)
+
+
 def test_dequantize_of_a_cache_shape():
     rng = np.random.default_rng(5)
     codes, blocks, scales = R.quantize(rng.standard_normal((3, 2, 16, 96)).astype(np.float32))
