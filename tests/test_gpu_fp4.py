@@ -265,6 +265,30 @@ def test_a_layer_behind_the_quantiser_of_its_weight():
         assert torch.equal(fw.linear_fp4(fw.linear_fp4(x, *f), *f), two)
 
 
+def test_weights_past_four_gib():
+    """Codes beyond 2^32 bytes: the last channels against those alone."""
+    n, k, tail = 140000, 65536, 48
+    g = torch.Generator(DEV)
+    g.manual_seed(23)
+    codes = torch.randint(0, 256, (n, k // 2), generator=g, device=DEV, dtype=torch.uint8)
+    blocks = torch.randint(0x28, 0x48, (n, k // 16), generator=g, device=DEV, dtype=torch.uint8)
+    scales = torch.rand((n,), generator=g, device=DEV) + 0.5
+    ends = [t[-tail:].clone() for t in (codes, blocks, scales)]
+    for m, dtype in ((1, "bf16"), (8, "f16"), (20, "bf16"), (100, "f16")):
+        x = torch.randn((m, k), generator=g, device=DEV).to(DT[dtype])
+        y = fw.linear_fp4(x, codes, blocks, scales)[:, -tail:]
+        want, total, lost = exact(x, *ends, None)
+        tol = U[dtype] * want.abs() + (k / 8 + 32) * 2.0 ** -23 * total + (lost if dtype == "bf16" else 2.0 ** -25)
+        assert bool(((y.double() - want).abs() <= tol).all())
+    assert fw.device_error() == 0
+    w = fw.dequantize_fp4(codes, blocks, scales)
+    want = fw.dequantize_fp4(*ends)
+    assert torch.equal(w[-tail:], want)
+    del codes, blocks
+    for got, alone in zip(fw.quantize_fp4(w), fw.quantize_fp4(want)):
+        assert torch.equal(got[-tail:], alone)
+
+
 def test_the_binding_checks_its_operands():
     codes, blocks, scales = fw.quantize_fp4(torch.randn((8, 64), device=DEV))
     x = torch.randn((2, 64), device=DEV).bfloat16()
