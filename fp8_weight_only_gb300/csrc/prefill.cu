@@ -38,6 +38,7 @@
 
 #include "fp4.cuh"
 #include "fp8w_internal.h"
+#include "rings.h"
 
 namespace fp8w {
 
@@ -62,9 +63,8 @@ constexpr int kPBarTmem = 1;                      // named barrier: MMA warp + e
 // x tiles come from L2.  Both fill 224 KB of shared memory.
 template <int BN>
 struct PrefillSmem {
-    static constexpr int kPCS = BN == 128 ? 6 : 4;  // code stages (16 KB)
-    static constexpr int kPAS = 4;                  // dequantised A stages (16 KB)
-    static constexpr int kPXS = BN == 128 ? 4 : 3;  // x stages (BN x 64 x 2 B)
+    using R = PrefillRings<BN>;
+    static constexpr int kPCS = R::kPCS, kPAS = R::kPAS, kPXS = R::kPXS;
     static constexpr uint32_t kXBytes = BN * kPK * 2;
     static constexpr uint32_t kCodesOff = 0;
     static constexpr uint32_t kAOff = kCodesOff + kPCS * kPCodeBytes;
@@ -460,18 +460,21 @@ __global__ void __launch_bounds__(kMode == kModeGrouped ? kPThreadsGrouped : kMo
     } else if (kFp4 && warp >= kPFirstDqWarp) {
         // ----------------------------------------- dequantising, 4 bits --
         // Four warpgroups, for the four k-blocks of a code stage: two 16-byte chunks
-        // of a row each.  Their four blocks' scales (two 16-bit loads) are read a
-        // stage ahead.
-        const int h = (warp - kPFirstDqWarp) >> 2;
+        // of a row each.  A group's k-blocks, counted over the CTA's tiles, are four
+        // apart and go to one A stage (rings.h).  Their four blocks' scales (two 16-bit
+        // loads) are read a stage ahead.
+        static_assert(!kFp4 || kPAS == kPFp4Groups, "a group waits for every use of its A stage");
+        const int group = (warp - kPFirstDqWarp) >> 2;
         const int r = (warp & 3) * 32 + lane;
         const uint32_t swz = static_cast<uint32_t>(r & 7);
         if (!early) pdl_wait();  // the blocks' scales may come from the previous kernel
         uint32_t next = 0u;
-        int64_t b_t = blockIdx.x;
+        int64_t b_t = blockIdx.x, b_base = 0;
         int b_cs = 0;
         auto ask = [&] {  // the scales of stage (b_t, b_cs), and on to the one after it
             next = 0u;
-            const int64_t wrow = (b_t / token_tiles) * kPM + r, k0 = (static_cast<int64_t>(b_cs) * 4 + h) * kPK;
+            const int64_t wrow = (b_t / token_tiles) * kPM + r;
+            const int64_t k0 = (static_cast<int64_t>(b_cs) * 4 + prefill_fp4_part(group, b_base)) * kPK;
             if (b_t < tiles && wrow < n && k0 < k) {
                 const uint8_t* at = e8 + wrow * (k >> 4) + (k0 >> 4);
                 next = *reinterpret_cast<const uint16_t*>(at);
@@ -480,12 +483,14 @@ __global__ void __launch_bounds__(kMode == kModeGrouped ? kPThreadsGrouped : kMo
             if (++b_cs == ncs) {
                 b_cs = 0;
                 b_t += gridDim.x;
+                b_base += nkb;
             }
         };
         ask();
         int64_t cs_n = 0, kb_base = 0;
         bool ok = true;
         for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x, kb_base += nkb) {
+            const int h = prefill_fp4_part(group, kb_base);  // of each stage's four k-blocks
             for (int cs = 0; cs < ncs; ++cs, ++cs_n) {
                 const int s = static_cast<int>(cs_n % kPCS);
                 const uint32_t scale4 = next;
