@@ -47,9 +47,12 @@
 //    group's two TMEM A slots, where they are the A operand of the MMA (A
 //    from tensor memory: the dequantised weight never touches shared
 //    memory).  Two slots let a group convert the next unit while the MMAs
-//    still read the previous one.
-//  * Unit u uses A slot u % 6 (warpgroup u % 3, its slot (u / 3) % 2) and
-//    activation slot u % kXSlots.
+//    still read the previous one (4 bits: one slot, and a group converts a
+//    quarter of the next unit, into registers, meanwhile).
+//  * Unit u uses A slot u % 6 (warpgroup u % 3, its slot (u / 3) % 2; 4 bits:
+//    u % 3), the barrier u % 6 that says that it is full, and activation slot
+//    u % kXSlots.  Six barriers whatever the slots: each is then always waited
+//    on by the same MMA warp, which a wait by parity relies on (rings.h).
 //  * Warps 2 and 3, the MMA warps, take alternate units in order and issue
 //    each unit's eight tcgen05.mma.kind::f16 (M = 128, N = 16 or 32 tokens,
 //    K = 16) into their own TMEM accumulator of the tile (double-buffered
@@ -76,6 +79,7 @@
 
 #include "fp4.cuh"
 #include "fp8w_internal.h"
+#include "rings.h"
 #include "../../include/fp8w.h"
 
 namespace fp8w {
@@ -84,13 +88,13 @@ static __device__ int g_skinny_error;
 
 constexpr int kTileN = 128;                 // output channels per tile (MMA M)
 constexpr int kUnitK = 128;                 // k per unit (4 bits: twice as much)
-constexpr int kLanes = 3;                   // dequantising warpgroups
+constexpr int kLanes = SkinnyRings<16, false>::kLanes;  // dequantising warpgroups (3)
 constexpr int kACols = 384;                 // TMEM columns of the A slots
 // warps: 0 code TMA, 1 activation TMA, 2-3 MMA (warp 2 also owns TMEM),
 // 4..7 epilogue, 8..19 the dequantising warpgroups (4 warps each)
 constexpr int kXWarp = 1;
 constexpr int kMmaWarp = 2;
-constexpr int kMmaWarps = 2;
+constexpr int kMmaWarps = SkinnyRings<16, false>::kMmaWarps;
 constexpr int kFirstEpilogueWarp = kMmaWarp + kMmaWarps;
 constexpr int kFirstDequantWarp = kFirstEpilogueWarp + 4;
 constexpr int kThreads = 32 * (kFirstDequantWarp + 4 * kLanes);  // 640
@@ -108,16 +112,10 @@ struct SkinnySmem {
     static constexpr int kBlockK = kFp4 ? 2 * kUnitK : kUnitK;
     static constexpr uint32_t kCodeStageBytes = kTileN * 128;                // 16 KB
     static constexpr int kAColsPerSlot = kBlockK / 2;                        // two 16-bit values per column
-    static constexpr int kASlots = kACols / kLanes / kAColsPerSlot;          // TMEM A slots per warpgroup: 2 (4 bits: 1)
-    // per warpgroup: freed as soon as read (9 tiles in flight per SM: deeper
-    // rings on every SM make the HBM stream slower, not faster)
-    static constexpr int kCodeSlots = NT <= 32 ? 3 : 2;
-    static constexpr int kXSlots = (NT == 16 ? 12 : 8) / (kFp4 ? 2 : 1);  // activation ring (freed when the unit's MMAs are done)
-    // accumulator buffers per MMA warp: two (the epilogue drains one tile
-    // while the next accumulates) where TMEM has room, one for 64 tokens
-    static constexpr int kDBuf = NT <= 32 ? 2 : 1;
+    using R = SkinnyRings<NT, kFp4>;
+    static constexpr int kASlots = R::kASlots, kCodeSlots = R::kCodeSlots, kXSlots = R::kXSlots, kDBuf = R::kDBuf;
+    static_assert(kASlots * kLanes * kAColsPerSlot <= kACols, "TMEM columns of the A slots");
     static_assert(kDCol0 + kMmaWarps * kDBuf * NT <= kTmemCols, "TMEM columns");
-    static_assert(kXSlots % kMmaWarps == 0 && (kFp4 || (kLanes * kASlots) % kMmaWarps == 0), "slots alternate between MMA warps");
     static constexpr uint32_t kXBoxBytes = NT * 128;          // 64 k x NT rows x 2 B
     static constexpr uint32_t kXStageBytes = kBlockK / 64 * kXBoxBytes;
     static constexpr uint32_t kCodesOff = 0;
@@ -125,20 +123,18 @@ struct SkinnySmem {
     static constexpr uint32_t kBarOff = kXOff + kXSlots * kXStageBytes;
     // per warpgroup: cfull, cempty [kCodeSlots]
     static constexpr uint32_t kBarsPerLane = 2 * kCodeSlots;
-    // then: aready [6]; udone [kDoneSlots]; xfull [kXSlots]; dfree [2];
+    // then: aready [kReady]; udone [kDoneSlots]; xfull [kXSlots]; dfree [2];
     // dready [MMA warp][2]; drain [MMA warp].  udone(u % kDoneSlots) completes
     // a phase when unit u's MMAs are done: it frees the unit's A slot (for
-    // unit u + 6) and its activation slot (for unit u + kXSlots) with one
-    // commit; kDoneSlots is a multiple of both ring sizes, so each waiter
+    // unit u + kASlotsAll) and its activation slot (for unit u + kXSlots) with
+    // one commit; kDoneSlots is a multiple of both ring sizes, so each waiter
     // finds the phase of the unit it waits for.
-    static constexpr int kASlotsAll = kLanes * kASlots;
-    static constexpr int kDoneSlots = NT == 16 ? 12 : 24;
-    static_assert(kDoneSlots % kASlotsAll == 0 && kDoneSlots % kXSlots == 0, "unit-done ring");
+    static constexpr int kASlotsAll = R::kASlotsAll, kReady = R::kReady, kDoneSlots = R::kDoneSlots;
     static constexpr uint32_t kLaneBars = kLanes * kBarsPerLane;
     // per-group scales: the accumulator columns hold a ring of kGAcc group
     // accumulators (NT columns each); gfull [kGAcc], gfree [kGAcc] follow drain
     static constexpr int kGAcc = (kTmemCols - kDCol0) / NT;
-    static constexpr uint32_t kGBar0 = kLaneBars + kASlotsAll + kDoneSlots + kXSlots + 2 + 3 * kMmaWarps;
+    static constexpr uint32_t kGBar0 = kLaneBars + kReady + kDoneSlots + kXSlots + 2 + 3 * kMmaWarps;
     static constexpr uint32_t kNumBars = kGBar0 + 2 * kGAcc;
     // tmem base, abort flag, last-contributor flag, epilogue abort flag
     static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;
@@ -150,8 +146,8 @@ struct SkinnySmem {
     static __device__ __forceinline__ uint32_t arrivals(uint32_t i) {
         if (i < kLaneBars) return (i % kBarsPerLane) >= static_cast<uint32_t>(kCodeSlots) ? 4u : 1u;
         const uint32_t gi = i - kLaneBars;
-        if (gi < static_cast<uint32_t>(kASlotsAll)) return 4u;  // aready
-        const uint32_t di = static_cast<uint32_t>(kASlotsAll + kDoneSlots + kXSlots);
+        if (gi < static_cast<uint32_t>(kReady)) return 4u;  // aready
+        const uint32_t di = static_cast<uint32_t>(kReady + kDoneSlots + kXSlots);
         if (i >= kGBar0 + kGAcc) return 4u;                     // gfree
         return (gi == di || gi == di + 1) ? 4u : 1u;            // dfree
     }
@@ -318,15 +314,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto lbar = [&](int g, int i) { return bar0 + 8u * (g * L::kBarsPerLane + i); };
     auto cfull = [&](int g, int s) { return lbar(g, s); };
     auto cempty = [&](int g, int s) { return lbar(g, kCS + s); };
-    constexpr int kAS = L::kASlotsAll;
+    constexpr int kAS = L::kASlotsAll, kReady = L::kReady;
     auto gbar = [&](int i) { return bar0 + 8u * (L::kLaneBars + i); };
     constexpr int kDone = L::kDoneSlots;
     auto aready = [&](int r) { return gbar(r); };
-    auto udone = [&](int i) { return gbar(kAS + i); };
-    auto xfull = [&](int s) { return gbar(kAS + kDone + s); };
-    auto dfree = [&](int d) { return gbar(kAS + kDone + kXS + d); };
-    auto dready = [&](int w, int d) { return gbar(kAS + kDone + kXS + 2 + 2 * w + d); };
-    auto drain = [&](int w) { return gbar(kAS + kDone + kXS + 2 + 2 * kMmaWarps + w); };
+    auto udone = [&](int i) { return gbar(kReady + i); };
+    auto xfull = [&](int s) { return gbar(kReady + kDone + s); };
+    auto dfree = [&](int d) { return gbar(kReady + kDone + kXS + d); };
+    auto dready = [&](int w, int d) { return gbar(kReady + kDone + kXS + 2 + 2 * w + d); };
+    auto drain = [&](int w) { return gbar(kReady + kDone + kXS + 2 + 2 * kMmaWarps + w); };
     constexpr int kGAcc = L::kGAcc;
     auto gfull = [&](int b) { return bar0 + 8u * (L::kGBar0 + b); };
     auto gfree = [&](int b) { return bar0 + 8u * (L::kGBar0 + kGAcc + b); };
@@ -389,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // one warp spends ~1300 cycles on all of them while the stream waits.
     if (warp <= kXWarp) {
         // warp 1 sets up udone and xfull, [xb0, xb1): it is the first to wait on udone
-        const uint32_t xb0 = static_cast<uint32_t>(L::kLaneBars + kAS);
+        const uint32_t xb0 = static_cast<uint32_t>(L::kLaneBars + kReady);
         const uint32_t xb1 = xb0 + static_cast<uint32_t>(kDone + kXS);
         if (warp == 0) {
             // the code slots' barriers (the MMA warp sets up the others that
@@ -412,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // barriers
             tmem_alloc(smem_u32(tmem_slot), kTmemCols);
             tmem_relinquish();
-            const uint32_t xb0 = static_cast<uint32_t>(L::kLaneBars + kAS);
+            const uint32_t xb0 = static_cast<uint32_t>(L::kLaneBars + kReady);
             const uint32_t xb1 = xb0 + static_cast<uint32_t>(kDone + kXS);
             for (uint32_t i = L::kLaneBars + lane; i < L::kNumBars; i += 32)
                 if (i < xb0 || i >= xb1) mbar_init(bar0 + 8 * i, L::arrivals(i));
@@ -534,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         UnitCursor cu = cursor0();
         int seg = 0, jj = 0;
         int seg_len = iters > 0 ? cu.seg_left() : 0;
-        int ra = w, rx = w;          // slots of this warp's next unit: A (unit % 6), activation (unit % kXS)
+        int ra = w, rx = w;          // of this warp's next unit: aready barrier (unit % kReady), activation slot (unit % kXS)
         uint32_t pa = 0, px = 0;     // their phase parities
         bool mine_in_seg = false;    // this warp has issued into the segment's accumulator
         bool failed = false;
@@ -554,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (nw == 1 ? w == 0 : (it & 1) == w) {
                 // test this warp's next unit (it + nw) now; the answer is used
                 // after this unit's MMAs, which hide the tests' latency
-                const int ran = ra + nw >= kAS ? ra + nw - kAS : ra + nw;
+                const int ran = ra + nw >= kReady ? ra + nw - kReady : ra + nw;
                 const int rxn = rx + nw >= kXS ? rx + nw - kXS : rx + nw;
                 const uint32_t pan = ran < ra ? pa ^ 1u : pa;
                 const uint32_t pxn = rxn < rx ? px ^ 1u : px;
@@ -563,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool next_x = !more || mbar_test_wait(xfull(rxn), pxn);
                 tc_fence_after();
                 const uint32_t xs = sbase + x_smem(rx);
-                const uint32_t a_tmem = tmem + ra * kAColsPerSlot;  // slot ra = (group ra % 3, A slot ra / 3)
+                const uint32_t a_tmem = tmem + (ra < kAS ? ra : ra - kAS) * kAColsPerSlot;  // A slot unit % kAS
                 if constexpr (kGrp) {
                     // group G = it * gpu + q / mpg of the unit goes to accumulator
                     // G % kGAcc, once the epilogue has drained its previous group
@@ -957,9 +953,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;
         const uint32_t a_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-        int s = 0;         // == j % kCS
-        uint32_t ph = 0;   // == (j / kCS) & 1
-        for (int j = 0, it = group; it < iters; it += kLanes, ++j) {
+        int s = 0;         // the group's units % kCS
+        uint32_t ph = 0;   // (the group's units / kCS) & 1
+        int ready = group;  // aready barrier, it % kReady
+        for (int it = group; it < iters; it += kLanes) {
             if (!mbar_wait_warp(cfull(group, s), ph, abort_flag)) {
                 record_error(kErrWaitTma, abort_flag, cfull(group, s), bar0);
                 break;
@@ -985,7 +982,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 s = 0;
                 ph ^= 1u;
             }
-            // the first half is converted while the MMAs may still read the slot
+            // the first half (4 bits: quarter) is converted while the MMAs may still read the slot
             uint32_t v0[4][8];
             uint32_t mul[4];
             bool twice = false;
@@ -1029,15 +1026,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     dequant16<kBf16>(cw[q], v0[q]);
                 }
             }
-            // A slot of unit it = group + 3j: it % 6 = group + 3 (j % 2) (one slot: it % 3)
-            const int r = group + kLanes * (L::kASlots == 2 ? j & 1 : 0);
-            // the A slot's previous unit (it - 6) must be done
+            const int slot = L::kASlots == 2 ? ready : group;  // A slot it % kAS
+            // the A slot's previous unit (it - kAS) must be done
             if (it >= kAS && !mbar_wait_warp(done_bar(it - kAS), done_parity(it - kAS), abort_flag)) {
                 record_error(kErrWaitMma, abort_flag, done_bar(it - kAS), bar0);
                 break;
             }
             tc_fence_after();
-            const uint32_t a_addr = a_lane + r * kAColsPerSlot;
+            const uint32_t a_addr = a_lane + slot * kAColsPerSlot;
 #pragma unroll
             for (int q = 0; q < 4; ++q) tmem_st_x8(a_addr + q * 8, v0[q]);
 #pragma unroll
@@ -1057,11 +1053,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(aready(r));
+                mbar_arrive(aready(ready));
                 // behind the stores of what was read from the slot: the reads are done
                 // (an arrival right behind the loads can overtake them)
                 mbar_arrive(taken);
             }
+            ready = ready < kLanes ? ready + kLanes : ready - kLanes;
         }
     }
 

@@ -63,3 +63,24 @@ def test_prompts_of_several_tiles_of_any_k_blocks(m, n, blocks, dtype):
 @pytest.mark.parametrize("m,n,blocks", PROMPTS)
 def test_prompts_behind_a_long_kernel(m, n, blocks, dtype):
     behind_a_long_kernel(m, n, 64 * blocks, dtype)
+
+
+# clusters that share a tile, tiles of an SM's own, rows that end inside a unit; prompts
+# that go by slabs of 64 tokens
+FEW = [(16, 14336, 4096), (9, 40009, 1152), (32, 10007, 4128), (23, 4100, 14336), (64, 14336, 4096), (40, 30011, 2080), (65, 40009, 2880),
+       (65, 40009, 4288)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("m,n,k", FEW)
+def test_tokens_of_many_units(m, n, k, dtype):
+    y, x, t, b = run(m, n, k, dtype)
+    for _ in range(20):
+        assert torch.equal(fw.linear_fp4(x, *t, b), y)
+    assert fw.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("m,n,k", FEW)
+def test_tokens_behind_a_long_kernel(m, n, k, dtype):
+    behind_a_long_kernel(m, n, k, dtype)

@@ -38,6 +38,17 @@ template <int BN> static void prefill(int* out) {
     out[0] = PrefillRings<BN>::kPCS, out[1] = PrefillRings<BN>::kPAS, out[2] = PrefillRings<BN>::kPXS, out[3] = kPFp4Groups;
 }
 extern "C" void prefill_rings(int bn, int* out) { bn == 128 ? prefill<128>(out) : prefill<256>(out); }
+template <int NT, bool kFp4> static void skinny(int* out) {
+    using R = SkinnyRings<NT, kFp4>;
+    out[0] = R::kLanes, out[1] = R::kMmaWarps, out[2] = R::kASlotsAll, out[3] = R::kReady, out[4] = R::kCodeSlots, out[5] = R::kXSlots;
+    out[6] = R::kDBuf, out[7] = R::kDoneSlots;
+}
+extern "C" void skinny_rings(int nt, int fp4, int* out) {
+    if (fp4)
+        nt == 16 ? skinny<16, true>(out) : nt == 32 ? skinny<32, true>(out) : skinny<64, true>(out);
+    else
+        nt == 16 ? skinny<16, false>(out) : nt == 32 ? skinny<32, false>(out) : skinny<64, false>(out);
+}
 extern "C" int part(int group, long long before) { return prefill_fp4_part(group, before); }
 """
 
@@ -269,3 +280,156 @@ def test_each_k_block_has_one_warpgroup(rings):
                  if 4 * cs + rings.part(g, t * nkb) < nkb]
         assert sorted(kb for kb, _ in taken) == list(range(5 * nkb))
         assert all(kb % groups == g for kb, g in taken)
+
+
+def skinny_roles(tiles, lanes, mma_warps, slots, ready, code_slots, x_slots, dbuf, done_slots, seed):
+    """K3 with scales a row (or 4 bits): one CTA, tiles of so many units each."""
+    units = sum(tiles)
+    ends = [sum(tiles[:i + 1]) - 1 for i in range(len(tiles))]
+    cfull = [[Bar("cfull%d,%d" % (g, s), 1) for s in range(code_slots)] for g in range(lanes)]
+    cempty = [[Bar("cempty%d,%d" % (g, s), WARPS) for s in range(code_slots)] for g in range(lanes)]
+    aready, done = [Bar("aready%d" % i, WARPS) for i in range(ready)], [Bar("done%d" % i, 1) for i in range(done_slots)]
+    xfull = [Bar("xfull%d" % s, 1) for s in range(x_slots)]
+    dfree = [Bar("dfree%d" % d, 1) for d in range(dbuf)]
+    dready = [[Bar("dready%d,%d" % (w, d), 1) for d in range(dbuf)] for w in range(mma_warps)]
+    codes = [Slots("codes%d" % g, code_slots, 1) for g in range(lanes)]
+    a, x = Slots("A", slots, WARPS), Slots("x", x_slots, 1)
+    readers = {}
+    c_land, x_land, tensor, sums = Queue(), Queue(), [Queue() for _ in range(mma_warps)], {}
+
+    def code_producer():
+        for it in range(units):
+            g, j = it % lanes, it // lanes
+            s, use = j % code_slots, j // code_slots
+            yield wait(cempty[g][s], use & 1 ^ 1, use)
+
+            def land(g=g, s=s, it=it):
+                codes[g].put(s, 0, it)
+                cfull[g][s].arrive()
+            c_land.append(land)
+        c_land.ended = True
+
+    def x_producer():
+        for it in range(units):
+            if it >= x_slots:
+                v = it - x_slots
+                yield wait(done[v % done_slots], v // done_slots & 1, v // done_slots + 1)
+
+            def land(it=it):
+                x.put(it % x_slots, 0, it)
+                xfull[it % x_slots].arrive()
+            x_land.append(land)
+            yield None
+        x_land.ended = True
+
+    def dequantiser(group, warp):
+        for it in range(group, units, lanes):
+            j = it // lanes
+            s, use = j % code_slots, j // code_slots
+            yield wait(cfull[group][s], use & 1, use + 1)
+            if codes[group].held[s][0] != it:
+                raise Fault("codes%d slot %d: %s for %d" % (group, s, codes[group].held[s][0], it))
+            if it >= slots:
+                v = it - slots
+                yield wait(done[v % done_slots], v // done_slots & 1, v // done_slots + 1)
+            a.put(it % slots, warp, it)
+            yield None
+            aready[it % ready].arrive()
+            readers[it] = readers.get(it, 0) + 1
+            if readers[it] == WARPS:
+                codes[group].use(s, it)
+            cempty[group][s].arrive()
+
+    def mma(w):
+        def parts(it):
+            return [wait(aready[it % ready], it // ready & 1, it // ready + 1), wait(xfull[it % x_slots], it // x_slots & 1, it // x_slots + 1)]
+
+        if w < units:
+            for p in parts(w):
+                yield p
+        seg, first, issued = 0, True, False
+        for it in range(units):
+            d = seg % dbuf
+            if first:
+                yield wait(dfree[d], seg // dbuf & 1 ^ 1, seg // dbuf)
+            first = False
+            if it % mma_warps == w:
+                # the next unit's barriers are asked before this unit's products
+                missing = []
+                if it + mma_warps < units:
+                    for p in parts(it + mma_warps):
+                        if not p[0].passes(p[1]):
+                            missing.append(p)
+                        elif p[0].over < p[2]:
+                            raise Fault("%s: passes with %d phases over, for %d" % (p[0].name, p[0].over, p[2]))
+                tensor[w].append((seg, it))
+                issued = True
+                yield None
+                for p in missing:
+                    yield p
+            if it == ends[seg]:
+                if issued:
+                    tensor[w].append((seg, None))
+                else:
+                    dready[w][d].arrive()
+                yield None
+                seg, first, issued = seg + 1, True, False
+        tensor[w].ended = True
+
+    def tensor_core(w):
+        while True:
+            yield tensor[w], 0, 0
+            if not tensor[w].items:
+                return
+            seg, it = tensor[w].items.pop(0)
+            if it is None:
+                dready[w][seg % dbuf].arrive()
+            else:
+                a.use(it % slots, it)
+                x.use(it % x_slots, it)
+                sums.setdefault(seg, []).append(it)
+                done[it % done_slots].arrive()
+
+    def epilogue():
+        for seg in range(len(tiles)):
+            for w in range(mma_warps):
+                yield wait(dready[w][seg % dbuf], seg // dbuf & 1, seg // dbuf + 1)
+            if sorted(sums.get(seg, [])) != list(range(ends[seg] + 1 - tiles[seg], ends[seg] + 1)):
+                raise Fault("tile %d: %s" % (seg, sums.get(seg)))
+            yield None
+            dfree[seg % dbuf].arrive()
+
+    roles = [code_producer(), x_producer(), copier(c_land, seed), copier(x_land, ~seed), epilogue()]
+    roles += [f(w) for w in range(mma_warps) for f in (mma, tensor_core)]
+    return roles + [dequantiser(g, w) for g in range(lanes) for w in range(WARPS)]
+
+
+UNITS = ([1], [2], [3], [5], [16], [1, 1, 1, 1, 1], [2, 2, 2], [3, 1, 4, 1, 5], [4, 4, 4], [7, 7, 7, 7], [13, 20, 6])
+
+
+def skinny_faults(numbers_, tiles, runs):
+    found = []
+    for seed in range(runs):
+        try:
+            play(skinny_roles(tiles, *numbers_, seed), seed)
+        except Fault as f:
+            found.append(str(f))
+    return found
+
+
+@pytest.mark.parametrize("nt", [16, 32, 64])
+@pytest.mark.parametrize("fp4", [1, 0])
+def test_skinny(rings, nt, fp4):
+    n = numbers(rings.skinny_rings, nt, fp4)
+    for tiles in UNITS:
+        assert skinny_faults(n, tiles, 20) == [], tiles
+
+
+@pytest.mark.parametrize("nt", [16, 32, 64])
+def test_the_model_sees_barriers_that_change_their_mma_warp(rings, nt):
+    # a barrier for each of three slots, which two warps wait for in turn
+    n = numbers(rings.skinny_rings, nt, 1)
+    n[3] = n[2]
+    assert n[3] == 3
+    for tiles in ([5], [16], [4, 4, 4], [3, 1, 4, 1, 5]):
+        assert skinny_faults(n, tiles, 20), tiles
