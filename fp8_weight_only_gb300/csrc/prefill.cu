@@ -113,7 +113,7 @@ __device__ __forceinline__ void prefill_error(int code, volatile int* abort_flag
 template <int BN, bool kBf16, int kMode>
 __global__ void __launch_bounds__(kMode == kModeGrouped ? kPThreadsGrouped : kMode == kModeFp4 ? kPThreadsFp4 : kPThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_constant__ CUtensorMap map_x,
-                   const float* __restrict__ scales, const uint8_t* __restrict__ e8, const float* __restrict__ bias,
+                   const float* scales, const uint8_t* e8, const float* bias,
                    uint16_t* __restrict__ y, int64_t m, int64_t n, int64_t k, int early, int gsz) {
     constexpr bool kMx = kMode == kModeMxFold;
     constexpr bool kGrp = kMode == kModeGrouped;
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kMode == kModeGrouped ? kPThreadsGrouped : kMo
         const int nacc = nsc * apg;                                  // accumulators a tile
         auto scale_at = [&](int64_t col, int j) -> float {
             if (col >= n) return 0.0f;  // rows past n hold zero codes
-            return e8 ? e8m0_to_f32(__ldg(e8 + col * nsc + j)) : __ldg(scales + col * nsc + j);
+            return e8 ? e8m0_to_f32(e8[col * nsc + j]) : scales[col * nsc + j];
         };
         pdl_wait();  // y may still be read, and the scales written, by the previous kernel
         int Gc = 0;  // accumulators drained (below 2^31: tiles a CTA x k / 32)
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(kMode == kModeGrouped ? kPThreadsGrouped : kMo
         int mx_j = h;
         auto mx_load = [&]() -> uint32_t {
             const int64_t wrow = (mx_t / token_tiles) * kPM + r;
-            return wrow < n ? static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(e8 + wrow * (k >> 5)) + mx_j))
+            return wrow < n ? static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(e8 + wrow * (k >> 5))[mx_j])
                             : 0x7F7Fu;  // rows past n hold zero codes: any scale does
         };
         auto mx_step = [&]() {

@@ -295,7 +295,7 @@ struct SharedTile {
 template <int NT, bool kBf16, int kMode = kModeRow, int kGpu = 1>
 __global__ void __launch_bounds__(kThreads, 1)
     skinny_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_constant__ CUtensorMap map_x,
-                  const float* __restrict__ scales, const uint8_t* __restrict__ e8, const float* __restrict__ bias,
+                  const float* scales, const uint8_t* e8, const float* bias,
                   uint16_t* __restrict__ y, int m_rows, int m_row0, int64_t n, int64_t k, int cl, int tpc,
                   int early, int gsz) {
     constexpr bool kMx = kMode == kModeMxFold;
@@ -705,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int gpr = static_cast<int>(nsc);
             auto scale_at = [&](int64_t col, int j) -> float {
                 if (col >= n || j >= gpr) return 0.0f;  // rows past n, groups past k: zero codes
-                return e8 ? e8m0_to_f32(__ldg(e8 + col * nsc + j)) : __ldg(scales + col * nsc + j);
+                return e8 ? e8m0_to_f32(e8[col * nsc + j]) : scales[col * nsc + j];
             };
             // the totals as fp32 pairs (packed FMAs); tot(t) is token t's
             uint64_t tot2[NT / 2];
@@ -921,7 +921,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto mx_load = [&](int64_t tile, int kb) -> uint32_t {
             const int64_t row = tile * kTileN + (warp & 3) * 32 + lane;
             // rows past n hold zero codes (the copy's fill): any scale does
-            return row < n ? __ldg(reinterpret_cast<const uint32_t*>(e8 + row * (k >> 5) + kb * 4)) : 0x7F7F7F7Fu;
+            return row < n ? *reinterpret_cast<const uint32_t*>(e8 + row * (k >> 5) + kb * 4) : 0x7F7F7F7Fu;
         };
         if constexpr (kMx) {
             if (!early) pdl_wait();  // the scales may come from the previous kernel
