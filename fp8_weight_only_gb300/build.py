@@ -16,7 +16,7 @@ OBJ_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfp8w.so")
 SOURCES = ["api.cu", "quantize.cu", "gemv.cu", "skinny.cu", "prefill.cu", "w8a8.cu", "rope.cu", "attention.cu", "attention_few.cu",
            "fp4.cu", "fp4_linear.cu"]
-HEADERS = ["fp8w_device.cuh", "fp8w_internal.h", "attention.cuh", "fp4.cuh", "rings.h"]
+HEADERS = ["fp8w_device.cuh", "fp8w_internal.h", "attention.cuh", "fp4.cuh", "rings.h", "device_setup.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -1433,7 +1433,7 @@ template <int DP, bool kBf16, int kForm>
 cudaError_t launch_attn(const AttentionArgs& a, cudaStream_t st) {
     using L = AttnSmem<DP, kForm>;
     auto kern = attention_kernel<DP, kBf16, kForm>;
-    static std::once_flag attr_once[64];
+    static DeviceSetup setup;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -1441,13 +1441,11 @@ cudaError_t launch_attn(const AttentionArgs& a, cudaStream_t st) {
     int sms = 0;
     e = device_sm_count(sms);
     if (e != cudaSuccess) return e;
-    cudaError_t attr_err = cudaSuccess;
-    std::call_once(attr_once[dev], [&] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
-        if (attr_err == cudaSuccess)
-            attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    e = setup(dev, [&] {
+        const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+        return err != cudaSuccess ? err : cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     });
-    if (attr_err != cudaSuccess) return attr_err;
+    if (e != cudaSuccess) return e;
 
     const fp8w_kv_cache& c = *a.cache;
     const int group = a.q_heads / c.kv_heads;

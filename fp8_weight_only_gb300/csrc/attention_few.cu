@@ -37,7 +37,6 @@
 // 349 MB of it, 129 us, 40%, the two long sequences 123, 35%: 436 instructions for 16
 // keys, of them 150 conversions, multiplies and products, on two warps a scheduler
 // (three, with 16 keys a step: 132).
-#include <mutex>
 #include <type_traits>
 
 #include "attention.cuh"
@@ -722,7 +721,7 @@ template <int DP, bool kBf16, int kForm, int NT>
 cudaError_t launch_few(const AttentionArgs& a, cudaStream_t st) {
     using S = FewShape<DP, kForm, NT>;
     auto kern = attention_few_kernel<DP, kBf16, kForm, NT>;
-    static std::once_flag attr_once[64];
+    static DeviceSetup setup;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -730,9 +729,8 @@ cudaError_t launch_few(const AttentionArgs& a, cudaStream_t st) {
     int sms = 0;
     e = device_sm_count(sms);
     if (e != cudaSuccess) return e;
-    cudaError_t attr_err = cudaSuccess;
-    std::call_once(attr_once[dev], [&] { attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); });
-    if (attr_err != cudaSuccess) return attr_err;
+    e = setup(dev, [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); });
+    if (e != cudaSuccess) return e;
 
     AttnParams p = attention_params(a);
     const int64_t tiles = attention_row_tiles(a, p.group, S::kTile), items = tiles * p.kv_heads;

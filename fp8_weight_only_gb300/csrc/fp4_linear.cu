@@ -37,8 +37,6 @@
 // it at 256 a step and 14.8 us; 32 warps of 64 registers spilled: 19.9).  Tiles of 16, 24
 // and 32 tokens in the same way took 17.4, 22 and 32 us where the skinny kernel takes
 // 15 to 16.5: the products (10 cycles each on a scheduler) and the staging.
-#include <mutex>
-
 #include "fp4.cuh"
 #include "fp8w_internal.h"
 
@@ -406,7 +404,7 @@ namespace {
 template <bool kBf16>
 cudaError_t launch_slab(const LinearArgs& a, int most, cudaStream_t st) {
     auto kern = fp4_few_kernel<kBf16>;
-    static std::once_flag attr_once[64];
+    static DeviceSetup setup;
     static int active[64][4];  // clusters of 1, 2, 4, 8 CTAs that fit the device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -415,11 +413,10 @@ cudaError_t launch_slab(const LinearArgs& a, int most, cudaStream_t st) {
     int sms = 0;
     e = device_sm_count(sms);
     if (e != cudaSuccess) return e;
-    cudaError_t attr_err = cudaSuccess;
-    std::call_once(attr_once[dev], [&] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
+    e = setup(dev, [&] {
+        cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
         active[dev][0] = sms;
-        for (int i = 1; i < 4 && attr_err == cudaSuccess; ++i) {
+        for (int i = 1; i < 4 && err == cudaSuccess; ++i) {
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
             attr[0].val.clusterDim.x = 1u << i;
@@ -430,10 +427,11 @@ cudaError_t launch_slab(const LinearArgs& a, int most, cudaStream_t st) {
             cfg.dynamicSmemBytes = kSmemMost;
             cfg.attrs = attr;
             cfg.numAttrs = 1;
-            attr_err = cudaOccupancyMaxActiveClusters(&active[dev][i], kern, &cfg);
+            err = cudaOccupancyMaxActiveClusters(&active[dev][i], kern, &cfg);
         }
+        return err;
     });
-    if (attr_err != cudaSuccess) return attr_err;
+    if (e != cudaSuccess) return e;
 
     Fp4Params p = {};
     p.x = static_cast<const uint16_t*>(a.x);

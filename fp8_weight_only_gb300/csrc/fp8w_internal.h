@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/fp8w.h"
+#include "device_setup.h"
 
 namespace fp8w {
 

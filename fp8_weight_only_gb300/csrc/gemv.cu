@@ -41,7 +41,6 @@
 //  * A row's partial sums are reduced with a shuffle tree; one lane applies
 //    fmaf(acc, scale, bias) and rounds once.
 // HBM bytes per output channel: K (codes) + 4 (scale) + 4 (bias) + 2 (y).
-#include <mutex>
 
 #include "fp8w_device.cuh"
 #include "fp8w_internal.h"
@@ -550,17 +549,17 @@ static cudaError_t launch_dt(const LinearArgs& a, cudaStream_t st) {
         gemv_kernel<2, kBf16, false, 0>, gemv_kernel<2, kBf16, true, 0>, gemv_kernel<2, kBf16, false, 1>,
         gemv_kernel<2, kBf16, true, 1>,  gemv_kernel<2, kBf16, false, 2>, gemv_kernel<2, kBf16, true, 2>};
     auto kern = all[2 * kind + (f32x ? 1 : 0)];
-    static std::once_flag attr_once[64];
+    static DeviceSetup setup;
     int dev = 0;
     e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    cudaError_t attr_err = cudaSuccess;
-    std::call_once(attr_once[dev & 63], [&] {
+    e = setup(dev, [&] {
+        cudaError_t err = cudaSuccess;
         for (auto f : all)
-            if (attr_err == cudaSuccess)
-                attr_err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemvSmemBudget);
+            if (err == cudaSuccess) err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemvSmemBudget);
+        return err;
     });
-    if (attr_err != cudaSuccess) return attr_err;
+    if (e != cudaSuccess) return e;
     // programmatic dependent launch: set-up overlaps the previous kernel's tail
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

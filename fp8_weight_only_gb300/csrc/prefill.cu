@@ -34,8 +34,6 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <mutex>
-
 #include "fp4.cuh"
 #include "fp8w_internal.h"
 #include "rings.h"
@@ -654,15 +652,12 @@ static cudaError_t launch_bn(const LinearArgs& a, cudaStream_t st) {
     constexpr bool kMx = kMode == kModeMxFold;
     constexpr bool kGrp = kMode == kModeGrouped;
     auto kern = prefill_kernel<BN, kBf16, kMode>;
-    static std::once_flag attr_once[64];
+    static DeviceSetup setup;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    cudaError_t attr_err = cudaSuccess;
-    std::call_once(attr_once[dev & 63], [&] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
-    });
-    if (attr_err != cudaSuccess) return attr_err;
+    e = setup(dev, [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc); });
+    if (e != cudaSuccess) return e;
     int sms = 0;
     e = device_sm_count(sms);
     if (e != cudaSuccess) return e;

@@ -1247,7 +1247,7 @@ static cudaError_t launch_nt(const LinearArgs& a, const SkinnyShape* forced, cud
     auto kern = skinny_kernel<NT, kBf16, kMode, kGpu>;
     // per device, once: the kernel's attributes, and how many clusters of
     // each size the device holds at a time (0 where a size cannot launch)
-    static std::once_flag attr_once[64];
+    static DeviceSetup setup;
     static int active[64][kMaxCluster + 1];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1256,10 +1256,9 @@ static cudaError_t launch_nt(const LinearArgs& a, const SkinnyShape* forced, cud
     int sms = 0;
     e = device_sm_count(sms);
     if (e != cudaSuccess) return e;
-    cudaError_t attr_err = cudaSuccess;
-    std::call_once(attr_once[dev], [&] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
-        if (attr_err != cudaSuccess) return;
+    e = setup(dev, [&] {
+        const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+        if (err != cudaSuccess) return err;
         const bool nonportable =
             cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
         active[dev][1] = sms;
@@ -1281,8 +1280,9 @@ static cudaError_t launch_nt(const LinearArgs& a, const SkinnyShape* forced, cud
             if (cudaOccupancyMaxActiveClusters(&num, kern, &qc) == cudaSuccess) active[dev][cl] = num;
             else (void)cudaGetLastError();  // an unsupported size: leave it out
         }
+        return cudaSuccess;
     });
-    if (attr_err != cudaSuccess) return attr_err;
+    if (e != cudaSuccess) return e;
 
     CUtensorMap map_codes, map_x;
     const uint64_t row_bytes = static_cast<uint64_t>(kMode == kModeFp4 ? a.k / 2 : a.k);  // of codes

@@ -43,8 +43,6 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <mutex>
-
 #include "fp8w_device.cuh"
 #include "fp8w_internal.h"
 
@@ -381,15 +379,12 @@ template <int BN, bool kBf16>
 static cudaError_t launch_w8a8_bn(const W8A8Args& a, cudaStream_t st) {
     using L = W8Smem<BN>;
     auto kern = w8a8_kernel<BN, kBf16>;
-    static std::once_flag attr_once[64];
+    static DeviceSetup setup;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    cudaError_t attr_err = cudaSuccess;
-    std::call_once(attr_once[dev & 63], [&] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
-    });
-    if (attr_err != cudaSuccess) return attr_err;
+    e = setup(dev, [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc); });
+    if (e != cudaSuccess) return e;
     int sms = 0;
     e = device_sm_count(sms);
     if (e != cudaSuccess) return e;
