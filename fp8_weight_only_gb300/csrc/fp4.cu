@@ -163,7 +163,8 @@ template <bool kTiny>
 __device__ __forceinline__ float mul_sticky(float c, float s) {
     const float hi = __fmul_rz(c, s);
     const float rest = kTiny ? fmaf(c * 0x1p64f, s, hi * -0x1p64f) : fmaf(c, s, -hi);
-    return rest != 0.0f ? __uint_as_float(__float_as_uint(hi) | 1u) : hi;
+    // (an infinite scale's rest is NaN: its product is what it is)
+    return fabsf(rest) > 0.0f ? __uint_as_float(__float_as_uint(hi) | 1u) : hi;
 }
 
 struct Fp4Walk {        // blocks of 16 values, a grid of threads apart
