@@ -151,8 +151,9 @@ def copier(landing, seed):
 
 
 def prefill_roles(nkb, tiles, pcs, pas, pxs, groups, part, seed):
-    """K4's 4-bit form: one CTA with `tiles` tiles of nkb k-blocks of 64."""
-    ncs = -(-nkb // 4)
+    """K4: one CTA with `tiles` tiles of nkb k-blocks of 64, as many of them a code stage
+    as there are dequantising warpgroups (4 bits: four)."""
+    ncs = -(-nkb // groups)
     cfull, cempty = [Bar("cfull%d" % s, 1) for s in range(pcs)], [Bar("cempty%d" % s, groups * WARPS) for s in range(pcs)]
     afull, aempty = [Bar("afull%d" % s, WARPS) for s in range(pas)], [Bar("aempty%d" % s, 1) for s in range(pas)]
     xfull, xempty = [Bar("xfull%d" % s, 1) for s in range(pxs)], [Bar("xempty%d" % s, 1) for s in range(pxs)]
@@ -193,7 +194,7 @@ def prefill_roles(nkb, tiles, pcs, pas, pxs, groups, part, seed):
                 yield wait(cfull[s], i // pcs & 1, i // pcs + 1)
                 if codes.held[s][0] != i:
                     raise Fault("codes slot %d: %s for %d" % (s, codes.held[s][0], i))
-                j = 4 * cs + h
+                j = groups * cs + h
                 if j < nkb:
                     kb = base + j
                     yield wait(aempty[kb % pas], (kb // pas & 1) ^ 1, kb // pas)
@@ -248,8 +249,9 @@ def prefill_roles(nkb, tiles, pcs, pas, pxs, groups, part, seed):
     return roles + [dequantiser(g, w) for g in range(groups) for w in range(WARPS)]
 
 
-def prefill_faults(rings, bn, nkb, part, runs, tiles=4):
-    pcs, pas, pxs, groups = numbers(rings.prefill_rings, bn)[:4]
+def prefill_faults(rings, bn, nkb, part, runs, tiles=4, groups=None):
+    pcs, pas, pxs, four = numbers(rings.prefill_rings, bn)[:4]
+    groups = groups or four
     found = []
     for seed in range(runs):
         try:
@@ -263,6 +265,13 @@ def prefill_faults(rings, bn, nkb, part, runs, tiles=4):
 def test_prefill_of_four_bits(rings, bn):
     for nkb in range(1, 21):
         assert prefill_faults(rings, bn, nkb, rings.part, 20) == [], nkb
+
+
+@pytest.mark.parametrize("bn", [128, 256])
+def test_prefill_of_eight_bits(rings, bn):
+    # two warpgroups, the same part of a stage in every tile: at most three k-blocks on, one less than the ring
+    for nkb in range(1, 21):
+        assert prefill_faults(rings, bn, nkb, lambda group, before: group, 20, groups=2) == [], nkb
 
 
 def test_the_model_sees_a_warpgroup_that_changes_its_stage(rings):
