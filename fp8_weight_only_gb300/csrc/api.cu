@@ -298,8 +298,9 @@ fp8w_status fp8w_linear_fp4(const void* x, int act_dtype, int64_t m, int64_t k, 
     a.blocks = blocks;
     a.early = (flags & FP8W_FLAG_WEIGHTS_READY) != 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // Codes streamed into registers up to 8 tokens (14336 x 4096, 8 tokens: 13.0 us, 15.1
-    // by the skinny kernel; 16 with a wider form of it: 17.4), the skinny kernel up to 64.
+    // Codes streamed into registers up to 8 tokens (14336 x 4096, 8 tokens: 13.2 us; the
+    // skinny kernel takes 15.8 for up to 16, a wider form of the other 17.4), the skinny
+    // kernel up to 64.
     // Beyond, the prefill GEMM, whose CTA takes about half a microsecond for 64 inputs of
     // its tile, or slabs of 64 by the skinny kernel, about 7 us and one for each of its
     // CTA's units of 128 x 256: these where few channels leave the GEMM few CTAs (4096 x

@@ -1007,8 +1007,7 @@ __global__ void __launch_bounds__(AttnSmem<DP, kForm>::kThreads, 1)
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(full(d));
-                    // behind the stores of what was read from the slot: the reads are done
-                    // (an arrival right behind the loads can overtake them)
+                    // behind the stores of what was read from the slot: sooner gained no time
                     mbar_arrive(rawempty(s));
                 }
                 if (++s == kRaw) s = 0, phase ^= 1u;

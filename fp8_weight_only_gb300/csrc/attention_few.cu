@@ -34,9 +34,11 @@
 // One short sequence: 8 us, four dependent reads of memory and a launch.
 // 4 bits (fp4.cuh): the block's scale goes into the fp16 operands, exactly; a thread
 // has 32 codes of a key row (two blocks) and 16 of a value row (one).  The decode batch,
-// 349 MB of it, 129 us, 40%, the two long sequences 123, 35%: 436 instructions for 16
-// keys, of them 150 conversions, multiplies and products, on two warps a scheduler
-// (three, with 16 keys a step: 132).
+// 349 MB of it, 129 us, 40%, the two long sequences 123, 35%: latency.  A warp needs 436
+// instructions for 16 keys, of them 150 conversions, multiplies and products, and 244
+// registers leave two warps a scheduler, too few to cover each other's waits: 0.37
+// instructions issued a cycle, the busiest pipe (ALU) at 31%.  (Three warps, with 16 keys
+// a step: 132.)
 #include <type_traits>
 
 #include "attention.cuh"
@@ -256,8 +258,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attention_few_kernel(const 
     auto load = [&](int st, const int (&e)[kSubs], H& x) {
         if constexpr (kFp4) {
             // Whole steps of keys that are all wanted, the most of a long cache, without
-            // a test a load: instructions bound this form (a decode batch: 128 us, 167
-            // without this).
+            // a test a load: with so few warps a warp's own instructions are the time (a
+            // decode batch: 129 us, 167 without this).
             bool whole = st < steps && st * kStepKeys >= first && (st + 1) * kStepKeys <= end;
 #pragma unroll
             for (int i = 0; i < kSubs; ++i) whole = whole && static_cast<uint32_t>(e[i]) < static_cast<uint32_t>(p.num_pages);

@@ -28,15 +28,18 @@
 // goes over its tiles with the activations in place.  The launch takes the split of
 // which a model of the steps, the staging and the joins promises the least time.
 //
-// Measured (bf16, weights not in L2): 14336 x 4096, 33 MB, 1 token 10.0 us, 9.1 with
-// the weights ready (48 and 54% of the measured copy rate; e4m3 codes, 59 MB, take
-// 11.9); 8 tokens 13.0; 4096 x 14336 12.0 and 15.4; 1024 x 4096 3.8 and 6.4.  A
-// launch's start and end are 3 us of it.  Then instructions count as much as bytes: 80
-// of a step's 105 are conversions, multiplies and products, and set-up adds half again
-// (divisions on the device, a zeroing before each load and loads under a test each had
-// it at 256 a step and 14.8 us; 32 warps of 64 registers spilled: 19.9).  Tiles of 16, 24
-// and 32 tokens in the same way took 17.4, 22 and 32 us where the skinny kernel takes
-// 15 to 16.5: the products (10 cycles each on a scheduler) and the staging.
+// Measured (bf16, weights not in L2: 420 MB of them in turn): 14336 x 4096, 33 MB, 1
+// token 10.5 us, 9.5 with the weights ready (47 and 51% of the measured copy rate; e4m3
+// codes, 59 MB, take 12.9 and 12.0); 8 tokens 13.2; 4096 x 14336 12.3 and 15.8; 1024 x
+// 4096 4.2 and 6.7.  A launch's start and end are 3 us of it.  The rest is latency: 0.47
+// instructions issued a cycle and scheduler, no pipe above 34%, and the largest stall by
+// far is for loads (two steps in flight a warp, 24 warps an SM, and not all of the time:
+// set-up adds half again to the 105 instructions of a step).  Fewer instructions
+// shortened it all the same (divisions on the device, a zeroing before each load and
+// loads under a test each: 256 a step and 14.8 us; 32 warps of 64 registers spilled:
+// 19.9).  Tiles of 16, 24 and 32 tokens in the same way took 17.4, 22 and 32 us where the
+// skinny kernel takes 15.5 to 16.6 (both with 132 MB of weights in turn): the products
+// (10 cycles each on a scheduler) and the staging.
 #include "fp4.cuh"
 #include "fp8w_internal.h"
 

@@ -27,8 +27,8 @@
 //               * 2^120, or the hardware e4m3 -> f16 conversion), written in
 //               the 128-byte swizzled K-major layout the descriptor reads
 //               (4 bits: four warpgroups, warps 8-23, one for each k-block of a
-//               code stage of 256 codes a row; 2048 tokens on 14336 x 4096 181 us,
-//               68% of the measured rate, 195 with two; e4m3 170)
+//               code stage of 256 codes a row; 2048 tokens on 14336 x 4096 182 us,
+//               68% of the measured rate, 195 with two; e4m3 172)
 // Every wait is bounded; a CTA that gives up records a code, raises its abort
 // flag, lets its copies and MMAs land and frees TMEM.
 #include <cuda.h>
@@ -523,10 +523,9 @@ __global__ void __launch_bounds__(kMode == kModeGrouped ? kPThreadsGrouped : kMo
                 for (int q = 0; q < 8; ++q) sts128(arow + ((static_cast<uint32_t>(q) ^ swz) << 4), v[q][0], v[q][1], v[q][2], v[q][3]);
                 fence_proxy_async_smem();
                 __syncwarp();
-                // The codes' slot goes back here and no sooner: behind these stores,
-                // which hold what was read from it, the reads are done for sure.  (An
-                // arrival right behind the loads can overtake them where shared memory
-                // is busy: with it a slot was filled again before all had read it.)
+                // The codes' slot goes back behind these stores, which hold what was
+                // read from it: sooner (the arrival orders the reads either way) gained
+                // no time.
                 if (lane == 0) {
                     mbar_arrive(afull(as));
                     mbar_arrive(cempty(s));

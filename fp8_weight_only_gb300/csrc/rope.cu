@@ -21,8 +21,8 @@
 // those ahead of it in the stream still write, and its wait orders ordinary loads.
 // 16384 tokens of 40 heads of 128, three axes: 59.3 us, 5.8 TB/s (87% of the
 // measured copy rate), one axis 54.8 us; 8192 tokens appended 34.6 us (88%), as
-// codes 42.4 us (66%: sixteen IEEE divisions a lane); one token 1.7 us.  As 4 bits 37.6
-// us (70%), one token 2.0: multiplies by reciprocals in place of the divisions, and a
+// codes 42.4 us (66%: sixteen IEEE divisions a lane); one token 1.7 us.  As 4 bits 37.9
+// us (69%), one token 2.0: multiplies by reciprocals in place of the divisions, and a
 // maximum for each block of 16, whose halves two lanes hold where pairs lie in halves.
 #include "fp4.cuh"
 #include "fp8w_internal.h"

@@ -37,10 +37,12 @@
 //    producer and one in-order consumer.
 //  * 4-bit codes: a unit is 256 k, the same 16 KB of codes, with one A slot of
 //    twice the columns a warpgroup; the scales of the blocks are loaded by the
-//    dequantising threads a unit ahead (14336 x 4096, 32 tokens: 16.5 us, 30% of
-//    the copy rate; fp16, whose conversion is two instructions a pair instead of
-//    five, 13.7.  Bound by the conversion and by 112 tiles on 152 SMs.  Six
-//    warpgroups of 64 registers: 19.8).
+//    dequantising threads a unit ahead (14336 x 4096, 32 tokens, weights not in
+//    L2: 16.9 us, 29% of the copy rate; fp16, whose conversion is two instructions
+//    a pair instead of five, 14.0.  112 tiles leave 40 of 152 SMs idle; on the
+//    others the schedulers issue every other cycle, ALU pipe 41%, and the
+//    dequantising warps wait most for loads.  Six warpgroups of 64 registers: 19.8;
+//    one MMA warp for all units: 17.9).
 //  * In each warpgroup, thread r reads the 128 codes of channel r
 //    (conflict-free through the swizzle), converts them exactly to bf16 /
 //    fp16 in registers and stores them with tcgen05.st into one of the
@@ -107,8 +109,8 @@ constexpr int kMaxNT = 64;
 template <int NT, bool kFp4 = false>
 struct SkinnySmem {
     // A unit's codes are 128 bytes a channel, a line of the copy.  (4 bits with units of
-    // 128 k, 64 bytes a channel: 32 tokens on 14336 x 4096 17.8 us, 16.5 so; fp16 15.7
-    // and 13.7.)
+    // 128 k, 64 bytes a channel: 32 tokens on 14336 x 4096 17.8 us, 16.6 so; fp16 15.7
+    // and 13.6; four weights in turn.)
     static constexpr int kBlockK = kFp4 ? 2 * kUnitK : kUnitK;
     static constexpr uint32_t kCodeStageBytes = kTileN * 128;                // 16 KB
     static constexpr int kAColsPerSlot = kBlockK / 2;                        // two 16-bit values per column
@@ -1054,8 +1056,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(aready(ready));
-                // behind the stores of what was read from the slot: the reads are done
-                // (an arrival right behind the loads can overtake them)
+                // behind the stores of what was read from the slot: sooner gained no time
                 mbar_arrive(taken);
             }
             ready = ready < kLanes ? ready + kLanes : ready - kLanes;

@@ -354,7 +354,8 @@ FP8W_API fp8w_status fp8w_linear_w8a8(const uint8_t *x_codes, const float *x_sca
  *          6)[c & 7], negative where c & 8.
  *   blocks [k / 16] e4m3 bytes: the scales of 16 values each.
  *   scale  one fp32.
- * value = scale * e4m3(block) * e2m1(code).  The product of a block's scale and a
+ * value = scale * e4m3(block) * e2m1(code).  A checkpoint with one fp32 scale a tensor
+ * is loaded with that scale for every row.  The product of a block's scale and a
  * code is exact in fp16 and bf16, so kernels that multiply in 16 bits lose
  * nothing to the form.  The pages have no counterpart; they name the precision
  * (page "11. Inference with NVFP4/MXFP8").
