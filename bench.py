@@ -365,7 +365,7 @@ def kernel_name(m, k):
     return "fp8w::skinny_kernel<%d, 1, 0, 1>" % (16 if m <= 16 else 32)
 
 
-KERNEL_SOURCES = {"skinny_kernel": ["skinny.cu", "rings.h", "fp8w_device.cuh"], "gemv_kernel": ["gemv.cu", "fp8w_device.cuh"]}
+KERNEL_SOURCES = {"skinny_kernel": ["skinny.cu", "fp8w_device.cuh"], "gemv_kernel": ["gemv.cu", "fp8w_device.cuh"]}
 
 
 def kernel_source_hash(kernel):
